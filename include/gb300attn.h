@@ -22,7 +22,8 @@
  *   segment ids  int32 [b, s]   0 = padding slot, >0 = segment id
  *   segment pos  int32 [b, s]   position of the token inside its segment
  *   visible(i,j) <=> ids_q[i] == ids_kv[j] != 0 and pos_kv[j] <= pos_q[i]
- *                    and (window_left < 0 or pos_q[i] - pos_kv[j] <= window_left)
+ *                    and (window_left < 0 or pos_q[i] - pos_kv[j] <= window_left
+ *                         or pos_kv[j] < sink_tokens)
  *   out          O = softmax(scale * Q K^T + M) V   per head, M = 0 / -inf
  *   lse          fp32 [b, h_q, s_q], natural log of the softmax denominator
  *                including the scale; rows with no visible key: O = 0, lse = -inf
@@ -102,6 +103,10 @@ enum { ATTN_REORDER_DUAL_CHUNK = 0, ATTN_REORDER_STRIPED = 1 };
  *                 with d_v = 128 (the MLA shape the TE tutorial's closing
  *                 section points to), forward and backward: v is then bf16
  *                 [b, s_kv, h_kv, 128], contiguous.
+ *  sink_tokens    0 .. 2^30: keys at positions (kv_segment_pos) below it stay
+ *                 visible behind the window to every later query of their
+ *                 segment; 0 = the window alone.  No effect without a window.
+ *                 Forward, backward, merge and plan calls all take it.
  */
 typedef struct attn_fwd_params {
   const void* q;
@@ -124,6 +129,7 @@ typedef struct attn_fwd_params {
   void* out_final;
   int64_t kv_token_stride;
   int64_t d_v;
+  int64_t sink_tokens;
 } attn_fwd_params;
 
 /* Backward parameters: gradient of sum(out * dout) with respect to q, k, v

@@ -49,6 +49,7 @@ class FwdParams(ctypes.Structure):
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("merge_into_out", ctypes.c_int32), ("out_final", ctypes.c_void_p),
         ("kv_token_stride", ctypes.c_int64), ("d_v", ctypes.c_int64),
+        ("sink_tokens", ctypes.c_int64),
     ]
 
 
@@ -153,7 +154,8 @@ def _kv_token_stride(*ts) -> int:
     return 0 if ts_ == h * d else int(ts_)
 
 
-def _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, out_fp32):
+def _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, out_fp32,
+                sink_tokens=0):
     b, s_q, hq, d = q.shape
     _, s_kv, hkv, _ = k.shape
     p = FwdParams()
@@ -167,6 +169,7 @@ def _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, 
     p.out_fp32 = 1 if out_fp32 else 0
     p.out = out.data_ptr() if out is not None else None
     p.lse = lse.data_ptr() if lse is not None else None
+    p.sink_tokens = int(sink_tokens)
     return p
 
 
@@ -188,12 +191,15 @@ def _workspace(nbytes: int, device) -> torch.Tensor:
 def attn_fwd(q, k, v, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left: int = -1,
              scale: Optional[float] = None, out=None, lse=None, out_fp32: bool = False,
              merge_into_out: bool = False, out_final=None,
-             workspace: Optional[torch.Tensor] = None, check_status: bool = False):
+             workspace: Optional[torch.Tensor] = None, check_status: bool = False,
+             sink_tokens: int = 0):
     """Forward attention.  Returns (out [b,s_q,Hq,d_v], lse fp32 [b,Hq,s_q]).
 
     q bf16 [b,s_q,Hq,d]; k bf16 [b,s_kv,Hkv,d]; v bf16 [b,s_kv,Hkv,d_v] (d_v = d,
     or d = 192 with d_v = 128); ids/pos int32 [b,s].
     kv_ids / kv_pos default to the query descriptor (self-attention).
+    ``sink_tokens``: keys at positions below it stay visible behind the window
+    (the first tokens of every segment; 0 = the window alone).
     With ``merge_into_out`` the given fp32 ``out`` / ``lse`` hold a finished
     partial over other key blocks and this call's result is merged into them
     (into bf16 ``out_final`` instead of ``out`` when given).
@@ -204,7 +210,8 @@ def attn_fwd(q, k, v, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left: in
     :func:`read_device_status`.
     """
     return _attn_fwd_call("attn_fwd", q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale,
-                          out, lse, out_fp32, merge_into_out, out_final, workspace, check_status)
+                          out, lse, out_fp32, merge_into_out, out_final, workspace, check_status,
+                          sink_tokens)
 
 
 def attn_fwd_test_timeout(q, k, v, q_ids, q_pos, kv_ids=None, kv_pos=None, *,
@@ -226,7 +233,7 @@ def _raise_on_device_status(workspace: torch.Tensor, what: str):
 
 
 def _attn_fwd_call(entry, q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse,
-                   out_fp32, merge_into_out, out_final, workspace, check_status):
+                   out_fp32, merge_into_out, out_final, workspace, check_status, sink_tokens=0):
     kv_ids = q_ids if kv_ids is None else kv_ids
     kv_pos = q_pos if kv_pos is None else kv_pos
     _need_cuda(q, q_ids, q_pos, kv_ids, kv_pos, out, lse, workspace, out_final)
@@ -246,7 +253,8 @@ def _attn_fwd_call(entry, q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, sc
                           dtype=torch.float32 if out_fp32 else torch.bfloat16)
     if lse is None:
         lse = torch.empty(b, hq, s_q, device=q.device, dtype=torch.float32)
-    p = _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, out_fp32)
+    p = _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, out_fp32,
+                    sink_tokens)
     p.merge_into_out = 1 if merge_into_out else 0
     p.out_final = out_final.data_ptr() if out_final is not None else None
     p.kv_token_stride = kv_stride
@@ -264,7 +272,7 @@ def attn_bwd(q, k, v, out, lse, dout, q_ids, q_pos, kv_ids=None, kv_pos=None, *,
              window_left: int = -1, scale: Optional[float] = None, dq=None, dk=None, dv=None,
              accumulate_fp32: bool = False, workspace: Optional[torch.Tensor] = None,
              check_status: bool = False, deterministic: bool = False, kernel_events=None,
-             delta=None):
+             delta=None, sink_tokens: int = 0):
     """Backward attention.  Returns (dq, dk, dv): bf16, or with
     ``accumulate_fp32`` the given fp32 tensors with this call's gradients added.
     ``deterministic`` takes the dK / dV + dQ kernel pair, whose results are
@@ -274,8 +282,8 @@ def attn_bwd(q, k, v, out, lse, dout, q_ids, q_pos, kv_ids=None, kv_pos=None, *,
     before and after the main kernel(s), without the plan, the D pre-pass and
     the dQ finalise.  ``delta`` (fp32 [b, Hq, s_q], optional) receives
     D = rowsum(dO * O) of every query row and head; its sum is vdot(out,
-    dout), the loss whose gradient this call computes.  ``check_status`` as in
-    :func:`attn_fwd`."""
+    dout), the loss whose gradient this call computes.  ``check_status`` and
+    ``sink_tokens`` as in :func:`attn_fwd`."""
     kv_ids = q_ids if kv_ids is None else kv_ids
     kv_pos = q_pos if kv_pos is None else kv_pos
     _need_cuda(q, out, lse, dout, q_ids, q_pos, kv_ids, kv_pos, workspace, dq)
@@ -308,7 +316,8 @@ def attn_bwd(q, k, v, out, lse, dout, q_ids, q_pos, kv_ids=None, kv_pos=None, *,
     else:
         _kv_token_stride(k, v, dk, dv)  # dk / dv must have the layout of k / v
     p = BwdParams()
-    p.fwd = _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, False)
+    p.fwd = _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, False,
+                        sink_tokens)
     p.fwd.kv_token_stride = kv_stride
     p.dout, p.dq, p.dk, p.dv = dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr()
     p.accumulate_fp32 = 1 if accumulate_fp32 else 0
@@ -413,7 +422,7 @@ def inverse_reorder_causal_lb(x, strategy: int = DUAL_CHUNK, cp_size: int = 4,
 
 
 def attn_tile_plan(q, k, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left: int = -1,
-                   workspace=None):
+                   workspace=None, sink_tokens: int = 0):
     """Per-tile classes (uint8 [b,nq,nk]: 0 SKIP, 1 PARTIAL, 2 FULL) and q ranges."""
     kv_ids = q_ids if kv_ids is None else kv_ids
     kv_pos = q_pos if kv_pos is None else kv_pos
@@ -421,7 +430,8 @@ def attn_tile_plan(q, k, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left:
     b, s_q = q.shape[:2]
     s_kv = k.shape[1]
     nq, nk = -(-s_q // TILE), -(-s_kv // TILE)
-    p = _fwd_params(q, k, k, q_ids, q_pos, kv_ids, kv_pos, window_left, None, q, q, False)
+    p = _fwd_params(q, k, k, q_ids, q_pos, kv_ids, kv_pos, window_left, None, q, q, False,
+                    sink_tokens)
     need = lib().attn_fwd_workspace_bytes(ctypes.byref(p))
     workspace = _workspace(need, q.device) if workspace is None else workspace
     p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()
@@ -433,7 +443,7 @@ def attn_tile_plan(q, k, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left:
 
 
 def attn_tile_order(q, k, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left: int = -1,
-                    workspace=None):
+                    workspace=None, sink_tokens: int = 0):
     """The kernels' work order (debug hook): (q_order int32 [b*nq], kv_order
     int32 [b*nk]) as the forward and the fused backward take their units:
     index order (descending on the query side) when the heaviest unit is a
@@ -444,7 +454,8 @@ def attn_tile_order(q, k, q_ids, q_pos, kv_ids=None, kv_pos=None, *, window_left
     b, s_q = q.shape[:2]
     s_kv = k.shape[1]
     nq, nk = -(-s_q // TILE), -(-s_kv // TILE)
-    p = _fwd_params(q, k, k, q_ids, q_pos, kv_ids, kv_pos, window_left, None, q, q, False)
+    p = _fwd_params(q, k, k, q_ids, q_pos, kv_ids, kv_pos, window_left, None, q, q, False,
+                    sink_tokens)
     need = lib().attn_fwd_workspace_bytes(ctypes.byref(p))
     workspace = _workspace(need, q.device) if workspace is None else workspace
     p.workspace, p.workspace_bytes = workspace.data_ptr(), workspace.numel()

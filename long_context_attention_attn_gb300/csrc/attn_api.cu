@@ -46,6 +46,8 @@ int check_fwd(const attn_fwd_params* p) {
   if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
   if (p->s_q > (1ll << 30) || p->s_kv > (1ll << 30) || p->h_q > 65535 || p->b > 65535)
     return ATTN_ERR_UNSUPPORTED;
+  if (p->sink_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (p->sink_tokens > (1ll << 30)) return ATTN_ERR_UNSUPPORTED;
   if (p->d_v < 0) return ATTN_ERR_INVALID_ARG;
   const int64_t dv = fwd_dv(p);
   // head dims (q/k, v): (64, 64), (128, 128), (256, 256), (192, 128)

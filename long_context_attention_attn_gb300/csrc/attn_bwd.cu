@@ -99,6 +99,7 @@ struct BwdArgs {
   int* status;
   int b, s_q, s_kv, hq, hkv, g, nq, nk;
   int window;
+  int sink;  // keys at positions below it stay visible behind the window
   int accumulate;  // dk / dv are fp32 accumulators (add), else bf16 (overwrite)
   int64_t kv_stride;  // elements between consecutive tokens of dk / dv
   float scale;
@@ -493,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
+    const int window = pk < a.sink ? -1 : a.window;  // this key's window
     const float sl2 = a.scale_log2;
     uint8_t* ds_smem = smem + L::ds_off + w * L::kChunk + kr * 128;
     constexpr int kHalf = D / 2;         // dQ columns read back by this half
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             bool vis = (ia[u] == ik) && (ik != 0) && (pk <= qa[u]);
-            if (a.window >= 0) vis = vis && (qa[u] - pk <= a.window);
+            if (window >= 0) vis = vis && (qa[u] - pk <= window);
             if (!vis) p[4 * c + u] = 0.f;
           }
         }
@@ -704,6 +706,7 @@ cudaError_t launch_attn_bwd(const BwdLaunch& Lc, cudaStream_t st) {
   a.nq = (int)Lc.nq;
   a.nk = (int)Lc.nk;
   a.window = f.window_left;
+  a.sink = (int)f.sink_tokens;
   a.accumulate = p.accumulate_fp32 ? 1 : 0;
   a.kv_stride = f.kv_token_stride > 0 ? f.kv_token_stride : f.h_kv * f.d;
   a.scale = f.scale;

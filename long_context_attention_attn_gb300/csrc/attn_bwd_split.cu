@@ -82,6 +82,7 @@ struct SplitArgs {
   int* status;
   int b, s_q, s_kv, hq, hkv, g, nq, nk;
   int window;
+  int sink;          // keys at positions below it stay visible behind the window
   int accumulate;    // dq / dk / dv are fp32 accumulators (add), else bf16 (overwrite)
   int64_t k_stride;  // elements between consecutive tokens of dk
   int64_t v_stride;  // ... of dv
@@ -524,6 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
+    const int window = pk < a.sink ? -1 : a.window;  // this key's window
     const float sl2 = a.scale_log2;
     if constexpr (KT || VT) {
       // this thread's key (KT) and value (VT) rows into TMEM as bf16 pairs
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qa[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (!visible(ia[u], qa[u], ik, pk, a.window)) p[4 * c + u] = 0.f;
+            if (!visible(ia[u], qa[u], ik, pk, window)) p[4 * c + u] = 0.f;
         }
       }
       uint32_t pk2[kHB / 2];
@@ -1040,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ka[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (!visible(iq, pq, ia[u], ka[u], a.window)) p[4 * c + u] = 0.f;
+            if (!visible(iq, pq, ia[u], ka[u], ka[u] < a.sink ? -1 : a.window)) p[4 * c + u] = 0.f;
         }
       }
       mbar_arrive(&bars->id_empty[en]);
@@ -1189,6 +1191,7 @@ cudaError_t launch_attn_bwd_split(const SplitLaunch& Lc, cudaStream_t st) {
   a.nq = (int)Lc.nq;
   a.nk = (int)Lc.nk;
   a.window = f.window_left;
+  a.sink = (int)f.sink_tokens;
   a.accumulate = p.accumulate_fp32 ? 1 : 0;
   a.k_stride = f.kv_token_stride > 0 ? f.kv_token_stride : f.h_kv * f.d;
   a.v_stride = f.kv_token_stride > 0 ? f.kv_token_stride : f.h_kv * dv;

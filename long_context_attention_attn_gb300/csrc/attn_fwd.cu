@@ -83,6 +83,7 @@ struct FwdArgs {
   int* status;
   int b, s_q, s_kv, hq, hkv, g, npairs, nq, nk;
   int window;
+  int sink;  // keys at positions below it stay visible behind the window
   int out_fp32;
   int merge;               // fold the result into (out, lse) instead of writing it
   __nv_bfloat16* out_final;  // merge mode: merged O as bf16 here instead of into out
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               bool vis = (ika[u] == iq) && (iq != 0) && (pka[u] <= pq);
-              if (a.window >= 0) vis = vis && (pq - pka[u] <= a.window);
+              if (a.window >= 0) vis = vis && (pq - pka[u] <= a.window || pka[u] < a.sink);
               if (!vis) sr[4 * c + u] = __float_as_uint(-INFINITY);
             }
           }
@@ -684,6 +685,7 @@ cudaError_t launch_attn_fwd(const FwdLaunch& Lc, cudaStream_t st) {
   a.nq = (int)Lc.nq;
   a.nk = (int)Lc.nk;
   a.window = p.window_left;
+  a.sink = (int)p.sink_tokens;
   a.out_fp32 = p.out_fp32 ? 1 : 0;
   a.merge = p.merge_into_out ? 1 : 0;
   a.out_final = static_cast<__nv_bfloat16*>(p.out_final);

@@ -67,15 +67,18 @@ __global__ void tile_summary_kernel(const int* __restrict__ ids, const int* __re
   if (lane == 0) out[w] = r;
 }
 
-__device__ __forceinline__ uint8_t classify(const TileSummary& q, const TileSummary& k, int window) {
+// sink: keys at positions below it stay visible behind the window.
+__device__ __forceinline__ uint8_t classify(const TileSummary& q, const TileSummary& k, int window,
+                                            int sink) {
   if (!q.any_valid || !k.any_valid) return kSkip;
   if (q.id_max < k.id_min || k.id_max < q.id_min) return kSkip;
   if (k.pos_min > q.pos_max) return kSkip;  // every key after every query
-  if (window >= 0 && (int64_t)k.pos_max < (int64_t)q.pos_min - window) return kSkip;
+  if (window >= 0 && (int64_t)k.pos_max < (int64_t)q.pos_min - window && k.pos_min >= sink)
+    return kSkip;
   const bool one_id = !q.has_pad && !k.has_pad && q.id_min == q.id_max && k.id_min == k.id_max &&
                       q.id_min == k.id_min;
   if (one_id && k.pos_max <= q.pos_min &&
-      (window < 0 || (int64_t)q.pos_max - k.pos_min <= window))
+      (window < 0 || (int64_t)q.pos_max - k.pos_min <= window || k.pos_max < sink))
     return kFull;
   return kPartial;
 }
@@ -83,8 +86,8 @@ __device__ __forceinline__ uint8_t classify(const TileSummary& q, const TileSumm
 // One CTA per (q tile, b): the class of every kv tile and the q-side range.
 __global__ void tile_class_kernel(const TileSummary* __restrict__ qs,
                                   const TileSummary* __restrict__ ks, int64_t nq, int64_t nk,
-                                  int window, uint8_t* __restrict__ cls, int2* __restrict__ qrange,
-                                  int* __restrict__ qweight) {
+                                  int window, int sink, uint8_t* __restrict__ cls,
+                                  int2* __restrict__ qrange, int* __restrict__ qweight) {
   const int64_t a = blockIdx.x, bi = blockIdx.y;
   __shared__ int s_first, s_last, s_count;
   if (threadIdx.x == 0) {
@@ -96,7 +99,7 @@ __global__ void tile_class_kernel(const TileSummary* __restrict__ qs,
   const TileSummary q = qs[bi * nq + a];
   int first = INT_MAX, last = -1, count = 0;
   for (int64_t c = threadIdx.x; c < nk; c += blockDim.x) {
-    const uint8_t k = classify(q, ks[bi * nk + c], window);
+    const uint8_t k = classify(q, ks[bi * nk + c], window, sink);
     cls[(bi * nq + a) * nk + c] = k;
     if (k != kSkip) {
       first = min(first, (int)c);
@@ -474,7 +477,7 @@ struct SmallPlanArgs {
   const int* kv_ids;
   const int* kv_pos;
   int64_t b, s_q, s_kv, nq, nk, q_ctas, kv_ctas;
-  int window, need_kv, sms;
+  int window, sink, need_kv, sms;
 };
 
 __global__ void __launch_bounds__(kSmallPlanUnits)
@@ -498,7 +501,7 @@ __global__ void __launch_bounds__(kSmallPlanUnits)
     const TileSummary qsum = pp.q_sum[r];
     int first = INT_MAX, last = -1, count = 0;
     for (int64_t c = lane; c < a.nk; c += 32) {
-      const uint8_t k = classify(qsum, pp.kv_sum[bi * a.nk + c], a.window);
+      const uint8_t k = classify(qsum, pp.kv_sum[bi * a.nk + c], a.window, a.sink);
       pp.classes[r * a.nk + c] = k;
       if (k != kSkip) {
         first = min(first, (int)c);
@@ -561,6 +564,7 @@ cudaError_t launch_tile_plan(const attn_fwd_params& p, const PlanPtrs& pp, int64
     a.q_ctas = q_ctas;
     a.kv_ctas = kv_ctas;
     a.window = (int)p.window_left;
+    a.sink = (int)p.sink_tokens;
     a.need_kv = need_kv_side ? 1 : 0;
     a.sms = sm_count();
     small_plan_kernel<<<1, kSmallPlanUnits, 0, st>>>(a, pp);
@@ -572,7 +576,8 @@ cudaError_t launch_tile_plan(const attn_fwd_params& p, const PlanPtrs& pp, int64
   tile_summary_kernel<<<(unsigned)((p.b * nk + wpb - 1) / wpb), wpb * 32, 0, st>>>(
       p.kv_segment_ids, p.kv_segment_pos, p.b, p.s_kv, nk, pp.kv_sum);
   tile_class_kernel<<<dim3((unsigned)nq, (unsigned)p.b), 256, 0, st>>>(
-      pp.q_sum, pp.kv_sum, nq, nk, p.window_left, pp.classes, pp.q_range, pp.q_weight);
+      pp.q_sum, pp.kv_sum, nq, nk, p.window_left, (int)p.sink_tokens, pp.classes, pp.q_range,
+      pp.q_weight);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = launch_work_order(pp.q_weight, p.b * nq, q_ctas, true, pp, pp.q_order, st);

@@ -51,7 +51,7 @@ class _StatusLog:
 def ring_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1,
                   scale: Optional[float] = None, strategy: int = DUAL_CHUNK, stripe_size: int = 1,
                   fused_merge: bool = True, check_status: bool = True,
-                  batch_shards: bool = False):
+                  batch_shards: bool = False, sink_tokens: int = 0):
     """Forward attention computed as cp_size ring steps per logical shard.
 
     q bf16 [b,s,Hq,d]; k, v bf16 [b,s,Hkv,d]; ids/pos int32 [b,s] (natural
@@ -65,6 +65,8 @@ def ring_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1,
     shards' queries as a batch of b*R rows, the K/V blocks they hold at that
     step rotated into place, as a ring's send / receive would move them)
     instead of one call per shard and step; the result is the same.
+    ``sink_tokens`` as in :func:`attn_fwd` (positions are global, so the kept
+    tokens are those of the whole sequence).
     """
     b, s, hq, d = q.shape
     dv = v.shape[3]  # the output takes V's head dim
@@ -77,7 +79,7 @@ def ring_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1,
     qr, kr, vr, idr, posr = re(q), re(k), re(v), re(ids), re(pos)
     if batch_shards:
         return _ring_fwd_batched(qr, kr, vr, idr, posr, R, window_left, scale, strategy,
-                                 stripe_size, fused_merge, check_status, dv)
+                                 stripe_size, fused_merge, check_status, dv, sink_tokens)
     out = torch.empty(b, s, hq, dv, dtype=q.dtype, device=dev)
     lse = torch.empty(b, hq, s, dtype=torch.float32, device=dev)
     acc = torch.empty(1, n, hq, dv, dtype=torch.float32, device=dev)
@@ -101,16 +103,20 @@ def ring_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1,
                       posr[bi:bi + 1, cols])
                 if R == 1:
                     attn_fwd(qv, kv[0], kv[1], iq, pq, kv[2], kv[3], window_left=window_left,
+                             sink_tokens=sink_tokens,
                              scale=scale, out=out_r[:, rows], lse=lacc, workspace=ws)
                 elif t == 0:
                     attn_fwd(qv, kv[0], kv[1], iq, pq, kv[2], kv[3], window_left=window_left,
+                             sink_tokens=sink_tokens,
                              scale=scale, out=acc, lse=lacc, out_fp32=True, workspace=ws)
                 elif fused_merge:
                     attn_fwd(qv, kv[0], kv[1], iq, pq, kv[2], kv[3], window_left=window_left,
+                             sink_tokens=sink_tokens,
                              scale=scale, out=acc, lse=lacc, out_fp32=True, merge_into_out=True,
                              out_final=out_r[:, rows] if t == R - 1 else None, workspace=ws)
                 else:
                     attn_fwd(qv, kv[0], kv[1], iq, pq, kv[2], kv[3], window_left=window_left,
+                             sink_tokens=sink_tokens,
                              scale=scale, out=blk, lse=blk_lse, out_fp32=True, workspace=ws)
                     attn_merge_partial(acc, lacc, blk, blk_lse,
                                        out_final=out_r[:, rows] if t == R - 1 else None)
@@ -130,7 +136,7 @@ def ring_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1,
 
 def allgather_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1,
                        scale: Optional[float] = None, strategy: int = STRIPED,
-                       stripe_size: int = 512, check_status: bool = True):
+                       stripe_size: int = 512, check_status: bool = True, sink_tokens: int = 0):
     """All-gather context parallelism on one GPU (TE tutorial section 5,
     "AllGather" with a striped reorder, stripe_size 512; "Context parallelism
     and ring attention", section "Communication choices").
@@ -165,6 +171,7 @@ def allgather_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1
             rows = slice(r * n, (r + 1) * n)
             attn_fwd(qr[bi:bi + 1, rows], kv[0], kv[1], idr[bi:bi + 1, rows],
                      posr[bi:bi + 1, rows], kv[2], kv[3], window_left=window_left, scale=scale,
+                     sink_tokens=sink_tokens,
                      out=out_r[:, rows], lse=lse_sh[r:r + 1], workspace=ws)
             if log is not None:
                 log.record(ws)
@@ -181,7 +188,7 @@ def allgather_attn_fwd(q, k, v, ids, pos, cp_size: int, *, window_left: int = -1
 def ring_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *, window_left: int = -1,
                   scale: Optional[float] = None, strategy: int = DUAL_CHUNK,
                   stripe_size: int = 1, check_status: bool = True,
-                  deterministic: bool = False, batch_shards: bool = False):
+                  deterministic: bool = False, batch_shards: bool = False, sink_tokens: int = 0):
     """Backward of ring attention, emulated on one GPU.
 
     Shard r keeps its query rows, final output O_r, LSE_r and dO_r; at step t
@@ -215,7 +222,7 @@ def ring_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *, window_lef
     idr, posr = re(ids), re(pos)
     if batch_shards:
         return _ring_bwd_batched(qr, kr, vr, outr, dor, idr, posr, lse, R, window_left, scale,
-                                 strategy, stripe_size, check_status, deterministic)
+                                 strategy, stripe_size, check_status, deterministic, sink_tokens)
     dq = torch.zeros(b, s, hq, d, dtype=torch.float32, device=dev)
     dk = torch.zeros(b, s, hkv, d, dtype=torch.float32, device=dev)
     dv = torch.zeros(b, s, hkv, v.shape[3], dtype=torch.float32, device=dev)
@@ -240,6 +247,7 @@ def ring_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *, window_lef
                          outr[bi:bi + 1, rq], lse_sh[r:r + 1], dor[bi:bi + 1, rq],
                          idr[bi:bi + 1, rq], posr[bi:bi + 1, rq], idr[bi:bi + 1, rk],
                          posr[bi:bi + 1, rk], window_left=window_left, scale=scale,
+                         sink_tokens=sink_tokens,
                          dq=dq[bi:bi + 1, rq], dk=dk[bi:bi + 1, rk], dv=dv[bi:bi + 1, rk],
                          accumulate_fp32=True, workspace=ws, deterministic=deterministic)
                 if log is not None:
@@ -253,7 +261,8 @@ def ring_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *, window_lef
 def allgather_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *,
                        window_left: int = -1, scale: Optional[float] = None,
                        strategy: int = STRIPED, stripe_size: int = 512,
-                       check_status: bool = True, deterministic: bool = False):
+                       check_status: bool = True, deterministic: bool = False,
+                       sink_tokens: int = 0):
     """Backward of all-gather context parallelism, emulated on one GPU (TE
     tutorial section 5, "AllGather"; "Context parallelism and ring attention",
     section "Communication choices").
@@ -295,6 +304,7 @@ def allgather_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *,
             rows = slice(r * n, (r + 1) * n)
             attn_bwd(qr[kv, rows], kr[kv], vr[kv], outr[kv, rows], lse_sh[r:r + 1], dor[kv, rows],
                      idr[kv, rows], posr[kv, rows], idr[kv], posr[kv], window_left=window_left,
+                     sink_tokens=sink_tokens,
                      scale=scale, dq=dq[kv, rows], dk=dk[kv], dv=dv[kv], accumulate_fp32=True,
                      workspace=ws, deterministic=deterministic)
             if log is not None:
@@ -335,7 +345,7 @@ def _held_blocks(x, R, t):
 
 
 def _ring_fwd_batched(qr, kr, vr, idr, posr, R, window_left, scale, strategy, stripe_size,
-                      fused_merge, check_status, dv):
+                      fused_merge, check_status, dv, sink_tokens):
     b, s, hq, d = qr.shape
     n = s // R
     B = b * R
@@ -354,7 +364,7 @@ def _ring_fwd_batched(qr, kr, vr, idr, posr, R, window_left, scale, strategy, st
     for t in range(R):
         kt, vt = _held_blocks(kr, R, t), _held_blocks(vr, R, t)
         it, pt = _held_blocks(idr, R, t), _held_blocks(posr, R, t)
-        kw = dict(window_left=window_left, scale=scale, workspace=ws)
+        kw = dict(window_left=window_left, scale=scale, workspace=ws, sink_tokens=sink_tokens)
         if R == 1:
             attn_fwd(qa, kt, vt, ida, pa, it, pt, out=out_ra, lse=lse_a, **kw)
         elif t == 0:
@@ -377,7 +387,7 @@ def _ring_fwd_batched(qr, kr, vr, idr, posr, R, window_left, scale, strategy, st
 
 
 def _ring_bwd_batched(qr, kr, vr, outr, dor, idr, posr, lse, R, window_left, scale, strategy,
-                      stripe_size, check_status, deterministic):
+                      stripe_size, check_status, deterministic, sink_tokens):
     b, s, hq, d = qr.shape
     hkv, dv = kr.shape[2], vr.shape[3]
     n = s // R
@@ -401,6 +411,7 @@ def _ring_bwd_batched(qr, kr, vr, outr, dor, idr, posr, lse, R, window_left, sca
         kt, vt = _held_blocks(kr, R, t), _held_blocks(vr, R, t)
         it, pt = _held_blocks(idr, R, t), _held_blocks(posr, R, t)
         attn_bwd(qa, kt, vt, outa, lse_a, doa, ida, pa, it, pt, window_left=window_left,
+                 sink_tokens=sink_tokens,
                  scale=scale, dq=dq.view(B, n, hq, d), dk=dk_held.view(B, n, hkv, d),
                  dv=dv_held.view(B, n, hkv, dv), accumulate_fp32=True, workspace=ws,
                  deterministic=deterministic)

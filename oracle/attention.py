@@ -12,7 +12,8 @@ inputs" and section 3) is read as:
 
     visible(i, j)  <=>  ids_q[i] == ids_kv[j] != 0
                         and pos_kv[j] <= pos_q[i]
-                        and (W < 0 or pos_q[i] - pos_kv[j] <= W)
+                        and (W < 0 or pos_q[i] - pos_kv[j] <= W
+                             or pos_kv[j] < sink_tokens)
 
 id 0 marks padding; positions, not array indices, decide causality and the
 window (the window is inclusive: W + 1 keys including the query itself).
@@ -48,7 +49,7 @@ def _i64(x):
     return np.asarray(x).astype(np.int64)
 
 
-def visible(ids_q, pos_q, ids_kv, pos_kv, window_left):
+def visible(ids_q, pos_q, ids_kv, pos_kv, window_left, sink_tokens=0):
     """Boolean mask [len(ids_q), len(ids_kv)] of visible (query, key) pairs."""
     iq = np.asarray(ids_q, dtype=np.int64)[:, None]
     pq = np.asarray(pos_q, dtype=np.int64)[:, None]
@@ -56,7 +57,7 @@ def visible(ids_q, pos_q, ids_kv, pos_kv, window_left):
     pk = np.asarray(pos_kv, dtype=np.int64)[None, :]
     m = (iq == ik) & (iq != 0) & (pk <= pq)
     if window_left >= 0:
-        m &= (pq - pk) <= window_left
+        m &= ((pq - pk) <= window_left) | (pk < sink_tokens)
     return m
 
 
@@ -92,7 +93,7 @@ def _row_blocks(rows, block=ROW_BLOCK):
 
 
 def attn_fwd(q, k, v, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
-             *, batches=None, heads=None, rows=None):
+             *, batches=None, heads=None, rows=None, sink_tokens=0):
     """Forward attention.  Returns (out, lse) in float64.
 
     ``batches``/``heads``/``rows`` restrict the computation to a subset of
@@ -114,7 +115,8 @@ def attn_fwd(q, k, v, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
     rows = np.arange(s_q) if rows is None else np.asarray(rows)
     for bi in batches:
         for blk in _row_blocks(rows):
-            mask = visible(ids_q[bi, blk], pos_q[bi, blk], ids_kv[bi], pos_kv[bi], window_left)
+            mask = visible(ids_q[bi, blk], pos_q[bi, blk], ids_kv[bi], pos_kv[bi], window_left,
+                           sink_tokens)
             cols = np.nonzero(mask.any(axis=0))[0]
             if cols.size == 0:
                 continue
@@ -135,7 +137,7 @@ def attn_fwd(q, k, v, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
 
 
 def attn_bwd(q, k, v, dout, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
-             *, out=None, batches=None, kv_heads=None, rows=None):
+             *, out=None, batches=None, kv_heads=None, rows=None, sink_tokens=0):
     """Gradient of loss = sum(out * dout) with respect to q, k, v (float64).
 
     Uses the explicit probability matrix P of each row:
@@ -159,7 +161,7 @@ def attn_bwd(q, k, v, dout, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
     if out is None:
         heads = None if kv_heads is None else [h for kh in kv_heads for h in range(kh * g, kh * g + g)]
         out, _ = attn_fwd(q, k, v, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
-                          batches=batches, heads=heads, rows=rows)
+                          batches=batches, heads=heads, rows=rows, sink_tokens=sink_tokens)
     else:
         out = _f64(out)
     dq = np.zeros_like(q)
@@ -170,7 +172,8 @@ def attn_bwd(q, k, v, dout, ids_q, pos_q, ids_kv, pos_kv, window_left, scale,
     rows = np.arange(s_q) if rows is None else np.asarray(rows)
     for bi in batches:
         for blk in _row_blocks(rows):
-            mask = visible(ids_q[bi, blk], pos_q[bi, blk], ids_kv[bi], pos_kv[bi], window_left)
+            mask = visible(ids_q[bi, blk], pos_q[bi, blk], ids_kv[bi], pos_kv[bi], window_left,
+                           sink_tokens)
             cols = np.nonzero(mask.any(axis=0))[0]
             if cols.size == 0:
                 continue

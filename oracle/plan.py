@@ -101,7 +101,7 @@ def ranges(cls):
     return rng
 
 
-def brute_classes(ids_q, pos_q, ids_kv, pos_kv, window_left, tile=TILE):
+def brute_classes(ids_q, pos_q, ids_kv, pos_kv, window_left, tile=TILE, sink_tokens=0):
     """Exact classification from the element mask (small inputs only)."""
     ids_q, pos_q = np.asarray(ids_q), np.asarray(pos_q)
     ids_kv, pos_kv = np.asarray(ids_kv), np.asarray(pos_kv)
@@ -110,7 +110,7 @@ def brute_classes(ids_q, pos_q, ids_kv, pos_kv, window_left, tile=TILE):
     nq, nk = -(-s_q // tile), -(-s_kv // tile)
     cls = np.zeros((b, nq, nk), dtype=np.uint8)
     for bi in range(b):
-        m = visible(ids_q[bi], pos_q[bi], ids_kv[bi], pos_kv[bi], window_left)
+        m = visible(ids_q[bi], pos_q[bi], ids_kv[bi], pos_kv[bi], window_left, sink_tokens)
         for a in range(nq):
             for c in range(nk):
                 blk = m[a * tile:(a + 1) * tile, c * tile:(c + 1) * tile]

@@ -1,0 +1,113 @@
+"""First tokens that stay visible behind the sliding window, forward and backward, against
+the fp64 oracle.  Tolerances: tests/parity.py (the hot path's)."""
+import numpy as np
+import pytest
+import torch
+
+import workload
+from oracle import attention as A
+from oracle import plan as P
+from tests.parity import check_grad, check_lse, check_out
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _inputs(b, s, hq, hkv, d, dv, packing, seed):
+    q, k, v, dout = workload.qkv(b, s, hq, hkv, d, seed=seed, with_dout=True, dv=dv)
+    if packing == "one":
+        ids, pos = workload.segments(b, s, None)
+    else:
+        ids, pos = workload.random_segments(b, s, seed=seed, max_segments=3)
+    return dict(q=q, k=k, v=v, dout=dout, ids=ids, pos=pos)
+
+
+def _gpu(ga, x, window, sink, scale, det=False):
+    g = {n: t.to(DEV) for n, t in x.items()}
+    kw = dict(window_left=window, sink_tokens=sink, scale=scale, check_status=True)
+    out, lse = ga.attn_fwd(g["q"], g["k"], g["v"], g["ids"], g["pos"], **kw)
+    grads = ga.attn_bwd(g["q"], g["k"], g["v"], out, lse, g["dout"], g["ids"], g["pos"], deterministic=det, **kw)
+    return out, lse, grads
+
+
+@pytest.mark.parametrize("b,s,hq,hkv,d,dv,window,sink,packing", [
+    (1, 1, 2, 1, 64, 64, 0, 1, "one"),          # one token
+    (1, 129, 2, 2, 64, 64, 0, 1, "one"),        # each token sees itself and the first
+    (1, 700, 4, 2, 64, 64, 16, 4, "one"),       # tiles between the first and the window are skipped
+    (1, 700, 4, 2, 128, 128, 100, 130, "one"),  # the kept tokens end inside the second tile
+    (1, 900, 2, 1, 128, 128, 127, 128, "one"),  # a whole kept tile, seen without a mask
+    (2, 640, 8, 2, 128, 128, 40, 7, "packed"),
+    (1, 515, 5, 1, 64, 64, 3, 600, "packed"),   # more kept tokens than there are
+    (1, 600, 4, 2, 256, 256, 50, 5, "packed"),
+    (1, 600, 4, 2, 192, 128, 50, 5, "packed"),
+])
+@pytest.mark.parametrize("det", [False, True])
+def test_forward_and_backward(b, s, hq, hkv, d, dv, window, sink, packing, det):
+    import long_context_attention_attn_gb300 as ga
+    x = _inputs(b, s, hq, hkv, d, dv, packing, seed=s + d)
+    scale = d ** -0.5
+    out, lse, grads = _gpu(ga, x, window, sink, scale, det)
+    ro, rl = A.attn_fwd(x["q"], x["k"], x["v"], x["ids"], x["pos"], x["ids"], x["pos"], window, scale,
+                        sink_tokens=sink)
+    check_out(out.cpu(), ro)
+    check_lse(lse.cpu(), rl)
+    ref = A.attn_bwd(x["q"], x["k"], x["v"], x["dout"], x["ids"], x["pos"], x["ids"], x["pos"], window, scale,
+                     sink_tokens=sink)
+    for name, got, want in zip(("dq", "dk", "dv"), grads, ref):
+        check_grad(got.cpu(), want, name)
+
+
+@pytest.mark.parametrize("window,sink,same", [(40, 0, (40, 0)), (-1, 9, (-1, 0)), (40, 1 << 30, (-1, 0))])
+def test_same_bits_as_the_mask_it_amounts_to(window, sink, same):
+    """No kept tokens is the window alone, any without a window and all of them is causal:
+    the same tiles with the same visible keys, so the same bits (dq through the
+    deterministic pair, whose sums have one order)."""
+    import long_context_attention_attn_gb300 as ga
+    x = _inputs(1, 517, 4, 2, 128, 128, "packed", seed=4)
+    a = _gpu(ga, x, window, sink, 0.1, det=True)
+    b = _gpu(ga, x, *same, 0.1, det=True)
+    for t, u in zip((a[0], a[1], *a[2]), (b[0], b[1], *b[2])):
+        assert torch.equal(t, u)
+
+
+@pytest.mark.parametrize("s,window,sink,packing", [(1500, 100, 4, "one"), (1500, 100, 300, "one"),
+                                                   (1300, 20, 5, "packed"), (9000, 1000, 140, "one")])
+def test_tile_plan_covers_the_mask(s, window, sink, packing):
+    """Tiles with a visible pair are not skipped, tiles taken without a mask are all visible."""
+    import long_context_attention_attn_gb300 as ga
+    x = _inputs(1, s, 2, 1, 64, 64, packing, seed=s)
+    g = {n: t.to(DEV) for n, t in x.items()}
+    cls, _ = ga.attn_tile_plan(g["q"], g["k"], g["ids"], g["pos"], window_left=window, sink_tokens=sink)
+    got = cls.cpu().numpy()
+    want = P.brute_classes(x["ids"].numpy(), x["pos"].numpy(), x["ids"].numpy(), x["pos"].numpy(), window,
+                           sink_tokens=sink)
+    assert not np.any((got == P.SKIP) & (want != P.SKIP))
+    assert not np.any((got == P.FULL) & (want != P.FULL))
+    if packing == "one":  # one segment: exact, the ragged last tile apart
+        n = s // 128
+        assert np.array_equal(got[:, :n, :n], want[:, :n, :n])
+
+
+@pytest.mark.parametrize("batch_shards", [False, True])
+def test_ring_and_allgather(batch_shards):
+    from long_context_attention_attn_gb300 import ring
+    x = _inputs(1, 768, 4, 2, 64, 64, "one", seed=11)
+    g = {n: t.to(DEV) for n, t in x.items()}
+    kw = dict(window_left=70, sink_tokens=6, scale=0.125)
+    ro, rl = A.attn_fwd(x["q"], x["k"], x["v"], x["ids"], x["pos"], x["ids"], x["pos"], 70, 0.125, sink_tokens=6)
+    ref = A.attn_bwd(x["q"], x["k"], x["v"], x["dout"], x["ids"], x["pos"], x["ids"], x["pos"], 70, 0.125,
+                     sink_tokens=6)
+    out, lse = ring.ring_attn_fwd(g["q"], g["k"], g["v"], g["ids"], g["pos"], 4, batch_shards=batch_shards, **kw)
+    check_out(out.cpu(), ro)
+    check_lse(lse.cpu(), rl)
+    grads = [ring.ring_attn_bwd(g["q"], g["k"], g["v"], out, lse, g["dout"], g["ids"], g["pos"], 4,
+                                batch_shards=batch_shards, **kw)]
+    if not batch_shards:
+        ag = dict(stripe_size=64, **kw)
+        out2, lse2 = ring.allgather_attn_fwd(g["q"], g["k"], g["v"], g["ids"], g["pos"], 4, **ag)
+        check_out(out2.cpu(), ro)
+        grads.append(ring.allgather_attn_bwd(g["q"], g["k"], g["v"], out2, lse2, g["dout"], g["ids"], g["pos"], 4,
+                                             **ag))
+    for got3 in grads:
+        for name, got, want in zip(("dq", "dk", "dv"), got3, ref):
+            check_grad(got.cpu(), want, name)
