@@ -346,6 +346,121 @@ GB300ATTN_API int attn_fwd_noalloc(const attn_fwd_params* p, attn_stream_t strea
  * no counterpart to this call either. */
 GB300ATTN_API int attn_fwd_noalloc_status(attn_stream_t stream);
 
+/* A paged key / value cache held in 8 bits, with one scale per page and head.
+ * The pages have no counterpart to it; it is the serving side of the packed
+ * attention above (the same mask, GQA mapping, O and lse).
+ *  k, v       e4m3 [num_pages, h_kv, page_size, d]: slot t of page p holds one
+ *             token's head row; a value is its code times the page's scale
+ *  k_scale, v_scale  fp32 [num_pages, h_kv], contiguous, finite and >= 0
+ *  page_size  16, 32, 64 or 128;  d  64, 128 or 256
+ *  page_stride  bytes between consecutive pages of k and of v, 0 = contiguous;
+ *             else >= h_kv * page_size * d and a multiple of 16 (k and v may
+ *             be the halves of one [num_pages, 2, h_kv, page_size, d] buffer)
+ *  k, v 16-byte aligned, scales 4-byte aligned; num_pages <= 2^31 - 1.
+ * A page table is int32 [n, max_pages]: entry (i, j) is the page that holds
+ * tokens j * page_size .. of sequence i.  An entry outside [0, num_pages) is
+ * no page: what would be written there is dropped and what would be read is
+ * not visible.  max_pages * page_size <= 2^30.
+ */
+typedef struct attn_kv_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t num_pages, h_kv, page_size, d;
+  int64_t page_stride;
+} attn_kv_cache;
+
+/* Appends new tokens to the cache.
+ *  k, v       bf16 [tokens, h_kv, d], token rows token_stride elements apart
+ *             (0 = h_kv * d; else >= h_kv * d and a multiple of 8), 16-byte
+ *             aligned; a packed [b, s, h_kv, d] tensor has tokens = b * s
+ *  start      int32 [n]: where sequence i's first new token goes (the tokens
+ *             cached before it); a negative start appends nothing
+ *  lens       int32 [n] new tokens of each sequence, clamped to [0, max_new];
+ *             NULL = max_new each
+ *  tok_start  int32 [n]: token row of sequence i's first new token; NULL =
+ *             i * row_tokens.  Rows outside [0, tokens) are dropped.
+ *  max_new    upper bound of lens (sizes the launch), 1 .. 2^30
+ * For each sequence, touched page and head, K and V apart:
+ *   need  = the smallest power of two with max |x| <= 448 * need over the
+ *           finite new values of that page (at least 2^-126),
+ *   scale = need where the new tokens begin at the page's first slot, else
+ *           max(old scale, need),
+ *   the codes of the slots before the new tokens become
+ *           e4m3(code * old scale / scale) where the scale grew,
+ *   a new value x becomes e4m3(x / scale): round to nearest even, saturating
+ *           at +-448 (infinities too); NaN stays NaN.
+ * Slots behind the new tokens keep their bytes.  Powers of two make x / scale
+ * and the rescaling exact, so a value is rounded once (again only where it
+ * turns subnormal).  Each touched page has to belong to one sequence of the
+ * call alone; pages that several sequences share are copied first
+ * (attn_kv_copy_pages), otherwise the page's contents are unspecified. */
+typedef struct attn_kv_append_params {
+  attn_kv_cache cache;
+  const void* k;
+  const void* v;
+  int64_t tokens, token_stride;
+  const int32_t* page_table;
+  int64_t n, max_pages;
+  const int32_t* start;
+  const int32_t* lens;
+  const int32_t* tok_start;
+  int64_t row_tokens, max_new;
+} attn_kv_append_params;
+
+GB300ATTN_API int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream);
+
+/* Copies whole pages of K and V with their scales inside a cache: page src[i]
+ * to page dst[i] for i < n_pairs (int32 device arrays).  Forking a sequence
+ * shares its full pages and copies the last one; compaction moves pages to
+ * free ones.  A pair with an index outside [0, num_pages), or with src ==
+ * dst, is skipped.  One source may go to several pages; a page that is a
+ * destination twice, or a destination and a source, ends with unspecified
+ * contents (its own and no other page's). */
+GB300ATTN_API int attn_kv_copy_pages(const attn_kv_cache* cache, const int32_t* src,
+                                     const int32_t* dst, int64_t n_pairs, attn_stream_t stream);
+
+/* Attention of the last s_q tokens of each sequence over the cache.
+ *  q          bf16 [n, s_q, h_q, d], contiguous, 16-byte aligned; h_q % h_kv
+ *             == 0; s_q * (h_q / h_kv) <= 1024
+ *  seqlens    int32 [n]: tokens of sequence i, the new ones (appended before
+ *             this call) among them; query t sits at position
+ *             seqlens[i] - s_q + t.  A query at a negative position (a shorter
+ *             sequence, 0 = an empty slot) sees nothing: O = 0, lse = -inf.
+ *  key j is visible from a query at position p iff j <= p, its page is in the
+ *             table, and (window_left < 0 or p - j <= window_left or
+ *             j < sink_tokens).  Pages without a visible key are not read, so
+ *             those behind the window may be given back (table entry -1).
+ *  scale      softmax scale
+ *  out        bf16 (fp32 when out_fp32) [n, s_q, h_q, d];  lse fp32
+ *             [n, h_q, s_q]: finished partials that attn_merge_partial takes
+ *  workspace  >= attn_decode_workspace_bytes() bytes, 256-byte aligned; no
+ *             initialisation needed.  Calls that overlap on the GPU need one
+ *             each.
+ * Results are bit-identical from run to run. */
+typedef struct attn_decode_params {
+  attn_kv_cache cache;
+  const void* q;
+  const int32_t* page_table;
+  int64_t n, max_pages;
+  const int32_t* seqlens;
+  int64_t s_q, h_q;
+  int32_t window_left;
+  int32_t out_fp32;
+  int64_t sink_tokens;
+  float scale;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+} attn_decode_params;
+
+/* Scratch size (bytes) of attn_decode for the given problem on the current
+ * device; 0 on invalid sizes. */
+GB300ATTN_API size_t attn_decode_workspace_bytes(const attn_decode_params* p);
+GB300ATTN_API int attn_decode(const attn_decode_params* p, attn_stream_t stream);
+
 /* Static description of a status code. */
 GB300ATTN_API const char* attn_status_string(int status);
 

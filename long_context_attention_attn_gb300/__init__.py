@@ -26,7 +26,8 @@ EXPORTS = (
     "attn_merge_partial", "reorder_causal_lb", "inverse_reorder_causal_lb", "attn_tile_plan",
     "attn_read_device_status", "attn_status_string", "attn_fwd_noalloc",
     "attn_fwd_test_timeout", "attn_segments_from_seqlens", "attn_fwd_noalloc_status",
-    "attn_tile_order",
+    "attn_tile_order", "attn_kv_append", "attn_kv_copy_pages", "attn_decode_workspace_bytes",
+    "attn_decode",
 )
 
 
@@ -59,6 +60,36 @@ class BwdParams(ctypes.Structure):
         ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p), ("accumulate_fp32", ctypes.c_int32),
         ("deterministic", ctypes.c_int32), ("kernel_events", ctypes.c_void_p * 2),
         ("delta", ctypes.c_void_p),
+    ]
+
+
+class KvCache(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int64), ("h_kv", ctypes.c_int64),
+        ("page_size", ctypes.c_int64), ("d", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+    ]
+
+
+class KvAppendParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCache), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("page_table", ctypes.c_void_p), ("n", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+        ("start", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("tok_start", ctypes.c_void_p),
+        ("row_tokens", ctypes.c_int64), ("max_new", ctypes.c_int64),
+    ]
+
+
+class DecodeParams(ctypes.Structure):
+    _fields_ = [
+        ("cache", KvCache), ("q", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+        ("n", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("seqlens", ctypes.c_void_p),
+        ("s_q", ctypes.c_int64), ("h_q", ctypes.c_int64), ("window_left", ctypes.c_int32),
+        ("out_fp32", ctypes.c_int32), ("sink_tokens", ctypes.c_int64), ("scale", ctypes.c_float),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
     ]
 
 
@@ -103,6 +134,14 @@ def lib() -> ctypes.CDLL:
         h.attn_fwd_noalloc_status.restype = c_int
         h.attn_segments_from_seqlens.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp]
         h.attn_segments_from_seqlens.restype = c_int
+        h.attn_kv_append.argtypes = [ctypes.POINTER(KvAppendParams), vp]
+        h.attn_kv_append.restype = c_int
+        h.attn_kv_copy_pages.argtypes = [ctypes.POINTER(KvCache), vp, vp, i64, vp]
+        h.attn_kv_copy_pages.restype = c_int
+        h.attn_decode_workspace_bytes.argtypes = [ctypes.POINTER(DecodeParams)]
+        h.attn_decode_workspace_bytes.restype = ctypes.c_size_t
+        h.attn_decode.argtypes = [ctypes.POINTER(DecodeParams), vp]
+        h.attn_decode.restype = c_int
         h.attn_status_string.argtypes = [c_int]
         h.attn_status_string.restype = ctypes.c_char_p
         _lib_handle = h
@@ -385,6 +424,191 @@ def attn_merge_partial(out_acc, lse_acc, out_blk, lse_blk, out_final=None):
         _stream(out_acc.device))
     _check(rc, "attn_merge_partial")
     return (out_final if out_final is not None else out_acc), lse_acc
+
+
+def _on(device, *ts):
+    for t in ts:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors of a call must be on one CUDA device")
+
+
+def _index(t, shape, what: str):
+    if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous int32 {list(shape)} tensor")
+
+
+def _kv_cache(c: KvCache, k_cache, v_cache, k_scale, v_scale):
+    """Fills c from a cache: k / v e4m3 (or uint8) [num_pages, h_kv, page_size, d], pages dense
+    inside (they may be the halves of one buffer), scales fp32 [num_pages, h_kv]."""
+    dev = k_cache.device
+    if dev.type != "cuda":
+        raise ValueError("gb300attn runs on CUDA tensors only")
+    _on(dev, v_cache, k_scale, v_scale)
+    shape, st = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st:
+        raise ValueError("k_cache / v_cache must share one shape [num_pages, h_kv, page_size, d] and layout")
+    if any(t.dtype not in (torch.float8_e4m3fn, torch.uint8) for t in (k_cache, v_cache)):
+        raise ValueError("k_cache / v_cache hold float8_e4m3fn (or its bytes as uint8)")
+    pages, h, size, d = shape
+    if (d > 1 and st[3] != 1) or (size > 1 and st[2] != d) or (h > 1 and st[1] != size * d):
+        raise ValueError("k_cache / v_cache: each page must be contiguous")
+    for t in (k_scale, v_scale):
+        if t.dtype != torch.float32 or t.shape != (pages, h) or not t.is_contiguous():
+            raise ValueError("k_scale / v_scale must be contiguous fp32 [num_pages, h_kv] tensors")
+    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
+    c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+    c.num_pages, c.h_kv, c.page_size, c.d = pages, h, size, d
+    c.page_stride = st[0] if pages > 1 and st[0] != h * size * d else 0
+    return dev, shape
+
+
+def _row_stride(x) -> int:
+    """Elements between consecutive token rows of [b, s, h, d] (sizes of one have no stride)."""
+    (b, s, h, d), st = x.shape, x.stride()
+    step = st[1] if s > 1 else st[0] if b > 1 else h * d
+    if (d > 1 and st[3] != 1) or (h > 1 and st[2] != d) or (s > 1 and b > 1 and st[0] != s * step):
+        raise ValueError("k / v: heads must be contiguous and token rows evenly spaced")
+    return step
+
+
+def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens=None,
+                    tok_start=None, max_new: Optional[int] = None):
+    """Appends new tokens to a paged 8-bit cache, in place.
+
+    k, v bf16 [b, s, h_kv, d] (or the halves of a packed [b, s, 2, h_kv, d]);
+    k_cache / v_cache float8_e4m3fn [num_pages, h_kv, page_size, d] with fp32
+    scales [num_pages, h_kv]; page_table int32 [n, max_pages]; start int32 [n]
+    the position of each sequence's first new token (negative: none).
+    Sequence i's new tokens are row i's first ``lens[i]`` (n = b; all s without
+    ``lens``), or with ``tok_start`` int32 [n] the ``lens[i]`` tokens from flat
+    token ``tok_start[i]`` of the b * s on (packed prompts).  ``max_new`` bounds
+    lens and sizes the launch (default: s, with ``tok_start`` b * s).  Each
+    page's scale is the smallest power of two that fits its values; where a
+    page already holds tokens the larger of that and its scale is kept and
+    grown scales requantise them.  Pages shared between sequences are copied
+    first (:func:`kv_cache_copy_pages`)."""
+    p = KvAppendParams()
+    dev, shape = _kv_cache(p.cache, k_cache, v_cache, k_scale, v_scale)
+    if k.dim() != 4 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise ValueError("k / v must be bf16 [b, s, h_kv, d] tensors")
+    b, s, h, d = k.shape
+    if h != shape[1] or d != shape[3]:
+        raise ValueError("k / v must have the cache's heads and head dim")
+    p.token_stride = _row_stride(k)
+    if v.shape != k.shape or _row_stride(v) != p.token_stride:
+        raise ValueError("k / v must share one shape and token stride")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be a contiguous int32 [n, max_pages] tensor")
+    n = page_table.shape[0]
+    _on(dev, k, v, page_table, start, lens, tok_start)
+    _index(page_table, page_table.shape, "page_table")
+    for t, what in ((start, "start"), (lens, "lens"), (tok_start, "tok_start")):
+        _index(t, (n,), what)
+    if tok_start is None and n != b:
+        raise ValueError("page_table must have a row per row of k (or pass tok_start)")
+    p.k, p.v, p.tokens = k.data_ptr(), v.data_ptr(), b * s
+    p.page_table, p.n, p.max_pages = page_table.data_ptr(), n, page_table.shape[1]
+    p.start = start.data_ptr()
+    p.lens = None if lens is None else lens.data_ptr()
+    p.row_tokens = s
+    if tok_start is not None:
+        p.tok_start = tok_start.data_ptr()
+    most = s if tok_start is None else b * s
+    p.max_new = most if max_new is None else min(int(max_new), most)
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_append(ctypes.byref(p), _stream(dev)), "attn_kv_append")
+
+
+def kv_cache_copy_pages(k_cache, v_cache, k_scale, v_scale, src, dst):
+    """Copies pages src[i] to dst[i] (int32 [n]) of a cache with their scales,
+    in place: the partly filled last page of a forked sequence, or pages moved
+    to the front of a pool.  Pairs with an index that is no page, or with src
+    == dst, are skipped; a page must not be a destination twice, or both a
+    destination and a source."""
+    c = KvCache()
+    dev, _ = _kv_cache(c, k_cache, v_cache, k_scale, v_scale)
+    _on(dev, src, dst)
+    if src.dim() != 1:
+        raise ValueError("src / dst must be contiguous int32 [n] tensors")
+    _index(src, src.shape, "src")
+    _index(dst, src.shape, "dst")
+    if src.shape[0] == 0:
+        return
+    with torch.cuda.device(dev):
+        _check(lib().attn_kv_copy_pages(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                        _stream(dev)), "attn_kv_copy_pages")
+
+
+def _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
+                   sink_tokens, scale, out, lse, out_fp32):
+    p = DecodeParams()
+    dev, shape = _kv_cache(p.cache, k_cache, v_cache, k_scale, v_scale)
+    _on(dev, q, page_table, seqlens, out, lse)
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[3] != shape[3]:
+        raise ValueError("q must be a contiguous bf16 [n, s_q, h_q, d] tensor with the cache's head dim")
+    n, s_q, h_q, d = q.shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be a contiguous int32 [n, max_pages] tensor")
+    _index(page_table, (n, page_table.shape[1]), "page_table")
+    _index(seqlens, (n,), "seqlens")
+    if out is not None and (out.shape != q.shape or not out.is_contiguous()
+                            or out.dtype != (torch.float32 if out_fp32 else torch.bfloat16)):
+        raise ValueError("out must be a contiguous [n, s_q, h_q, d] tensor, bf16 (fp32 with out_fp32)")
+    if lse is not None and (lse.shape != (n, h_q, s_q) or lse.dtype != torch.float32
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [n, h_q, s_q] tensor")
+    p.q, p.page_table, p.seqlens = q.data_ptr(), page_table.data_ptr(), seqlens.data_ptr()
+    p.n, p.max_pages, p.s_q, p.h_q = n, page_table.shape[1], s_q, h_q
+    p.window_left, p.sink_tokens = int(window_left), int(sink_tokens)
+    p.out_fp32 = 1 if out_fp32 else 0
+    p.scale = float(d ** -0.5 if scale is None else scale)
+    p.out = q.data_ptr() if out is None else out.data_ptr()
+    p.lse = q.data_ptr() if lse is None else lse.data_ptr()
+    return p, dev
+
+
+def workspace_bytes_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens) -> int:
+    """Workspace bytes attn_decode needs for these shapes on q's device (0 if it rejects them)."""
+    p, dev = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, -1, 0, None,
+                            None, None, False)
+    with torch.cuda.device(dev):
+        return int(lib().attn_decode_workspace_bytes(ctypes.byref(p)))
+
+
+def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
+                window_left: int = -1, sink_tokens: int = 0, scale: Optional[float] = None,
+                out=None, lse=None, out_fp32: bool = False,
+                workspace: Optional[torch.Tensor] = None):
+    """Attention of the last s_q tokens of each sequence over a paged 8-bit
+    cache.  Returns (out [n, s_q, h_q, d], lse fp32 [n, h_q, s_q]).
+
+    q bf16 [n, s_q, h_q, d]; the cache and page_table [n, max_pages] as in
+    :func:`kv_cache_append`; seqlens int32 [n]: the tokens of each sequence in
+    the cache, the s_q new ones among them, so query t sits at position
+    seqlens[i] - s_q + t (nothing is visible from a negative one: O = 0, lse =
+    -inf).  ``window_left`` / ``sink_tokens`` as in :func:`attn_fwd`; pages
+    that no query sees are not read and may be given back (table entry -1).
+    With ``out_fp32`` out is a partial for :func:`attn_merge_partial`.  Calls
+    that overlap on the GPU need a ``workspace`` each (by default each call
+    allocates its own)."""
+    p, dev = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
+                            sink_tokens, scale, out, lse, out_fp32)
+    if out is None:
+        out = torch.empty(q.shape, device=dev, dtype=torch.float32 if out_fp32 else torch.bfloat16)
+        p.out = out.data_ptr()
+    if lse is None:
+        lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], device=dev, dtype=torch.float32)
+        p.lse = lse.data_ptr()
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = _workspace(int(lib().attn_decode_workspace_bytes(ctypes.byref(p))), dev)
+        else:
+            _need_cuda(workspace)
+            _on(dev, workspace)
+        p.workspace = workspace.data_ptr()
+        p.workspace_bytes = workspace.numel() * workspace.element_size()
+        _check(lib().attn_decode(ctypes.byref(p), _stream(dev)), "attn_decode")
+    return out, lse
 
 
 def _seq_view(x: torch.Tensor, seq_dim: int):

@@ -412,6 +412,118 @@ int inverse_reorder_causal_lb(const void* in, void* out, int64_t outer, int64_t 
                         stream);
 }
 
+// ---- the paged cache
+static bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
+
+// Bytes from the first to the last value of k (or v).
+static uint64_t cache_extent(const attn_kv_cache& c) {
+  const int64_t page = c.h_kv * c.page_size * c.d;
+  const int64_t stride = c.page_stride > 0 ? c.page_stride : page;
+  return (uint64_t)(c.num_pages - 1) * stride + page;
+}
+
+static int check_cache(const attn_kv_cache& c) {
+  if (!c.k || !c.v || !c.k_scale || !c.v_scale) return ATTN_ERR_INVALID_ARG;
+  if (c.num_pages < 1 || c.h_kv < 1 || c.page_size < 1 || c.d < 1 || c.page_stride < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scale, 4) || !aligned(c.v_scale, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (c.num_pages > 0x7fffffffll || c.h_kv > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128)
+    return ATTN_ERR_UNSUPPORTED;
+  if (c.d != 64 && c.d != 128 && c.d != 256) return ATTN_ERR_UNSUPPORTED;
+  if (c.page_stride != 0 &&
+      (c.page_stride < c.h_kv * c.page_size * c.d || c.page_stride % 16 != 0 ||
+       c.page_stride > (1ll << 40)))
+    return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+static int check_table(const attn_kv_cache& c, const int32_t* table, int64_t n, int64_t max_pages) {
+  if (!table || !aligned(table, 4) || n < 1 || max_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if (n > 65535 || max_pages > (1ll << 30) / c.page_size) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  const attn_kv_cache& c = p->cache;
+  int rc = check_cache(c);
+  if (rc == ATTN_OK) rc = check_table(c, p->page_table, p->n, p->max_pages);
+  if (rc != ATTN_OK) return rc;
+  if (!p->k || !p->v || !p->start || !aligned(p->k, 16) || !aligned(p->v, 16) ||
+      !aligned(p->start, 4) || !aligned(p->lens, 4) || !aligned(p->tok_start, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->tokens < 1 || p->max_new < 1 || p->row_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (p->token_stride != 0 && (p->token_stride < c.h_kv * c.d || p->token_stride % 8 != 0 ||
+                               p->token_stride > (1ll << 24)))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->tokens > (1ll << 40) || p->row_tokens > (1ll << 40) || p->max_new > (1ll << 30))
+    return ATTN_ERR_UNSUPPORTED;
+  const int64_t ts = p->token_stride > 0 ? p->token_stride : c.h_kv * c.d;
+  const uint64_t in_bytes = ((uint64_t)(p->tokens - 1) * ts + c.h_kv * c.d) * 2;
+  const uint64_t sc_bytes = (uint64_t)c.num_pages * c.h_kv * 4;
+  for (const void* in : {p->k, p->v})
+    if (overlap(in, in_bytes, c.k, cache_extent(c)) || overlap(in, in_bytes, c.v, cache_extent(c)) ||
+        overlap(in, in_bytes, c.k_scale, sc_bytes) || overlap(in, in_bytes, c.v_scale, sc_bytes))
+      return ATTN_ERR_INVALID_ARG;
+  const cudaError_t e = launch_kv_append(*p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+int attn_kv_copy_pages(const attn_kv_cache* cache, const int32_t* src, const int32_t* dst,
+                       int64_t n_pairs, attn_stream_t stream) {
+  if (!cache) return ATTN_ERR_INVALID_ARG;
+  const int rc = check_cache(*cache);
+  if (rc != ATTN_OK) return rc;
+  if (!src || !dst || !aligned(src, 4) || !aligned(dst, 4) || n_pairs < 1)
+    return ATTN_ERR_INVALID_ARG;
+  const cudaError_t e =
+      launch_kv_copy(*cache, src, dst, n_pairs, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+static int check_decode(const attn_decode_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  const attn_kv_cache& c = p->cache;
+  int rc = check_cache(c);
+  if (rc == ATTN_OK) rc = check_table(c, p->page_table, p->n, p->max_pages);
+  if (rc != ATTN_OK) return rc;
+  if (!p->q || !p->seqlens || !p->out || !p->lse || !aligned(p->q, 16) || !aligned(p->out, 16) ||
+      !aligned(p->seqlens, 4) || !aligned(p->lse, 4))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->s_q < 1 || p->h_q < 1 || p->h_q % c.h_kv || p->window_left < -1 || p->sink_tokens < 0)
+    return ATTN_ERR_INVALID_ARG;
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale)) return ATTN_ERR_INVALID_ARG;
+  if (p->s_q > 1024 || p->h_q > 65535 || p->s_q * (p->h_q / c.h_kv) > 1024 ||
+      p->sink_tokens > (1ll << 30))
+    return ATTN_ERR_UNSUPPORTED;
+  // one CTA of the combine kernel per sequence, kv head and tile of (at least 8) rows
+  if (p->n * c.h_kv * cdiv(p->s_q * (p->h_q / c.h_kv), 8) > 0x7fffffffll)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+size_t attn_decode_workspace_bytes(const attn_decode_params* p) {
+  size_t n = 0;
+  if (check_decode(p) != ATTN_OK || decode_workspace(*p, &n) != cudaSuccess) return 0;
+  return n;
+}
+
+int attn_decode(const attn_decode_params* p, attn_stream_t stream) {
+  const int rc = check_decode(p);
+  if (rc != ATTN_OK) return rc;
+  size_t need = 0;
+  if (!p->workspace || !aligned(p->workspace, 256)) return ATTN_ERR_INVALID_ARG;
+  cudaError_t e = decode_workspace(*p, &need);
+  if (e != cudaSuccess) return ATTN_ERR_CUDA;
+  if (p->workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+  return cuda_status(launch_attn_decode(*p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int attn_read_device_status(const void* workspace, attn_stream_t stream) {
   if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -1,0 +1,922 @@
+// Attention of a few query tokens per sequence over the paged 8-bit cache.
+//
+//   O = softmax(scale * q K^T + M) V,  K = codes * k_scale, V = codes * v_scale
+//
+// Bound by reading the cache once (2 * d bytes per key and kv head); the GQA
+// group's query heads and the query tokens share each key read as the rows of
+// one small matrix product.
+//
+// Work is cut by keys, not by sequence: the 32-key blocks of all (sequence, kv
+// head, row tile) items form one list, and every CTA of a grid that fills the
+// GPU once takes an equal run of it, so ragged batches and single long
+// sequences load every SM alike.  A run that ends inside an item leaves a
+// finished partial (O, lse) in the workspace, and the combine kernel folds an
+// item's partials in their order (the result does not depend on timing).
+//
+// A CTA's four warps take the blocks of a piece in turn, each with a ring of
+// its own in shared memory, filled by 16-byte asynchronous copies, so that no
+// warp waits for another before the piece's end.  Both products run with the
+// keys on the matrix unit's M side:
+//   S^T[keys, rows] = K q^T,  O^T[d, rows] += V^T P^T   (m16n8k16, f16 in, fp32
+// sums), so a group of 8 rows is one N tile and the 8-bit codes are widened to
+// f16 (exactly) once for all rows.  q enters as f16 after a power-of-two scale
+// of its row (its 8 bits fit; what lies 2^-38 below the row's largest value is
+// dropped), P as f16 relative to a running maximum (11 bits).
+// The sums over d and over keys do not care for order, so a thread takes its
+// d's as 16 neighbouring bytes of a key (K) or of four keys (V) and byte
+// permutes pair the keys: no transposing loads.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gb300 {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBlock = kDecodeBlock;  // keys per block
+constexpr float kLn2 = 0.69314718055994530942f;
+// The running maximum is raised only when a value exceeds it by more than this
+// (in powers of two), so P <= 256.
+constexpr float kRescale = 8.f;
+
+struct DecodeArgs {
+  const __nv_bfloat16* q;
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int* table;
+  const int* lens;
+  void* out;
+  float* lse;
+  float* part_o;    // [2 * grid, R, D]
+  float* part_lse;  // [2 * grid, R] (base 2)
+  int64_t page_stride;
+  int n, s_q, h_q, h_kv, g, rows, row_tiles, max_pages, page_shift, num_pages;
+  int window, sink, out_fp32, grid;
+  float scale_log2;
+};
+
+// The blocks of keys that some query of a sequence of length `len` may see:
+// first those of the kept tokens, then those from the window's start on.
+struct Span {
+  int hi;        // keys below this exist
+  int lo;        // first key of the window of the first query
+  int sink_hi;   // kept keys
+  int nb_sink;   // blocks taken before the window's first
+  int first;     // the window's first block
+  int count;     // blocks
+  __device__ __forceinline__ int block(int t) const { return t < nb_sink ? t : first + t - nb_sink; }
+};
+
+__device__ __forceinline__ Span span_of(const DecodeArgs& a, int len) {
+  Span s;
+  const int cap = a.max_pages << a.page_shift;
+  s.hi = max(min(len, cap), 0);
+  const int p0 = max(len - a.s_q, 0);
+  s.lo = a.window < 0 ? 0 : max(p0 - a.window, 0);
+  s.sink_hi = a.window < 0 ? 0 : min(a.sink, s.hi);
+  const int last = (s.hi + kBlock - 1) / kBlock;
+  s.first = min(s.lo / kBlock, last);
+  s.nb_sink = min((s.sink_hi + kBlock - 1) / kBlock, s.first);
+  s.count = s.nb_sink + last - s.first;
+  return s;
+}
+
+// Where the list of all blocks puts each sequence: thread t of the CTA sums
+// the blocks of `per` neighbouring sequences; `before` is the sum ahead of
+// them (shared memory, one entry per thread, then the total).
+struct Placement {
+  const int64_t* before;
+  int per;
+};
+
+__device__ __forceinline__ Placement place(const DecodeArgs& a, int64_t* before) {
+  __shared__ int64_t warp_sum[kWarps];
+  const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
+  const int per = (a.n + kThreads - 1) / kThreads;
+  int64_t sum = 0;
+  for (int i = t * per; i < min((t + 1) * per, a.n); ++i) sum += span_of(a, a.lens[i]).count;
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) warp_sum[wid] = incl;
+  __syncthreads();
+  int64_t base = 0;
+  for (int w = 0; w < wid; ++w) base += warp_sum[w];
+  before[t] = base + incl - sum;
+  if (t == kThreads - 1) before[kThreads] = base + incl;
+  __syncthreads();
+  return Placement{before, per};
+}
+
+// Blocks per CTA: an equal share of the list, and no less than a block for
+// each warp (a shorter run would only add partials to fold).
+__device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total) {
+  return max((total + a.grid - 1) / a.grid, (int64_t)kWarps);
+}
+
+// ---------------------------------------------------------------- primitives
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 4 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// f16 pair of the two e4m3 codes in the low / high half of a word (exact)
+__device__ __forceinline__ uint32_t widen_lo(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transposes the 8 x 8 f16 matrix that the warp holds one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Key of matrix row r (0..7) inside its group of 8: rows 2i and 2i + 1 are keys
+// i and i + 4, whose shared-memory chunks sit in different bank halves.
+__device__ __forceinline__ int key_of_row(int r) { return (r >> 1) | ((r & 1) << 2); }
+
+// Byte offset of 16-byte chunk c of key row `key` inside a block's K or V tile.
+// D = 128: the chunk index is XORed with the row.  D = 256: the same within
+// each 128-byte half.  D = 64: two rows share 128 bytes; the row's half and the
+// 32-byte part are chosen so that both the K reads (four chunks of keys i and
+// i + 4) and the V reads (one 8-byte piece of four keys i, i + 1, ..) meet all
+// banks once.
+template <int D>
+__device__ __forceinline__ int tile_offset(int key, int c) {
+  if constexpr (D == 64)
+    return (key >> 1) * 128 + (((key ^ (key >> 2)) & 1) << 6) + ((c ^ (key & 2)) << 4);
+  else
+    return key * D + ((c & 8) << 4) + (((c ^ key) & 7) << 4);
+}
+
+// 0xff in the bytes of w that are the e4m3 NaN (0x7f or 0xff)
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
+  return ((((w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u) * 0xffu;
+}
+
+// O^T += V^T P^T over one block: o[i][nt] are the d's of thread n8 (16 (or 8)
+// neighbouring ones, two per i) against rows 8 nt + 2 t4 + {0, 1}.  kNoNan
+// takes zeros for NaN codes; kOnlyNan turns o to NaN where a NaN code meets a
+// key whose value in pb (0 or 1) says that the row sees it.
+enum { kPlain, kNoNan, kOnlyNan };
+template <int D, int NT, int kMode>
+__device__ __forceinline__ void add_pv(float (&o)[D / 16][NT][4], const uint8_t* vt,
+                                       const uint32_t (&pb)[2][NT][2], int n8, int t4) {
+  constexpr int kParts = D == 256 ? 2 : 1;  // 16-byte pieces of a key per thread
+  constexpr int kWords = D == 64 ? 2 : 4;   // words per piece
+#pragma unroll
+  for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+    for (int hh = 0; hh < kParts; ++hh) {
+      uint32_t w[4][kWords];  // keys t4, t4 + 4, t4 + 8, t4 + 12 of the group
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int key = mt * 16 + t4 + 4 * y;
+        if constexpr (D == 64) {
+          const uint2 x = *reinterpret_cast<const uint2*>(vt + tile_offset<D>(key, n8 >> 1) + (n8 & 1) * 8);
+          w[y][0] = x.x;
+          w[y][1] = x.y;
+        } else {
+          const uint4 x = *reinterpret_cast<const uint4*>(vt + tile_offset<D>(key, key_of_row(n8) + 8 * hh));
+          w[y][0] = x.x;
+          w[y][1] = x.y;
+          w[y][2] = x.z;
+          w[y][3] = x.w;
+        }
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          if constexpr (kMode == kNoNan) w[y][j] &= ~nan_bytes(w[y][j]);
+          if constexpr (kMode == kOnlyNan) w[y][j] = nan_bytes(w[y][j]) & 0x38383838u;  // e4m3 1.0
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        const uint32_t ab0 = __byte_perm(w[0][j], w[1][j], 0x5140), ab1 = __byte_perm(w[0][j], w[1][j], 0x7362);
+        const uint32_t cd0 = __byte_perm(w[2][j], w[3][j], 0x5140), cd1 = __byte_perm(w[2][j], w[3][j], 0x7362);
+        const uint32_t f0[4] = {widen_lo(ab0), widen_hi(ab0), widen_lo(cd0), widen_hi(cd0)};
+        const uint32_t f1[4] = {widen_lo(ab1), widen_hi(ab1), widen_lo(cd1), widen_hi(cd1)};
+        const int i = (hh * kWords + j) * 2;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (kMode == kOnlyNan) {
+            float n0[4] = {0.f, 0.f, 0.f, 0.f}, n1[4] = {0.f, 0.f, 0.f, 0.f};
+            mma16816(n0, f0, pb[mt][nt][0], pb[mt][nt][1]);
+            mma16816(n1, f1, pb[mt][nt][0], pb[mt][nt][1]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (n0[c] != 0.f) o[i][nt][c] = __int_as_float(0x7fffffff);
+              if (n1[c] != 0.f) o[i + 1][nt][c] = __int_as_float(0x7fffffff);
+            }
+          } else {
+            mma16816(o[i][nt], f0, pb[mt][nt][0], pb[mt][nt][1]);
+            mma16816(o[i + 1][nt], f1, pb[mt][nt][0], pb[mt][nt][1]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Whether a block's V tile holds the e4m3 NaN (0x7f or 0xff) anywhere.
+template <int D>
+__device__ __forceinline__ bool holds_nan(const uint8_t* vt, int lane) {
+  bool nan = false;
+#pragma unroll 2
+  for (int u = lane; u < kBlock * D / 16; u += 32) {
+    const uint4 x = reinterpret_cast<const uint4*>(vt)[u];
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) nan |= nan_bytes(w[j]) != 0u;
+  }
+  return __any_sync(0xffffffffu, nan);
+}
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int R = NT * 8;                  // rows per tile
+  static constexpr int kTile = kBlock * D;          // bytes of a K or V tile
+  static constexpr int kStage = 2 * kTile;
+  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kKSteps = D / 16;
+  static constexpr bool kQRegs = D * NT <= 256;     // q fragments in registers
+  static constexpr int q_off = kWarps * kStages * kStage;          // uint4 [NT * kKSteps / 2][32]
+  static constexpr int meta_off = q_off + NT * kKSteps / 2 * 512;  // per warp and stage: 8 words
+  static constexpr int row_off = meta_off + kWarps * kStages * 32; // row factors, positions
+  static constexpr int bytes = row_off + 2 * R * 4;
+  // the ring's room holds the four warps' results at the end of a piece
+  static constexpr int kMergeRow = D + 4;
+  static_assert(kWarps * R * (kMergeRow + 3) * 4 <= q_off, "merge buffer");
+};
+
+// One piece of work: blocks [t0, t1) of an item.
+struct Piece {
+  int seq, kvh, rt, t0, t1;
+  Span span;
+  int len;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs a) {
+  using C = Cfg<D, NT>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t before[kThreads + 1];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int n8 = lane >> 2, t4 = lane & 3;
+
+  const Placement pl = place(a, before);
+  const int items = a.h_kv * a.row_tiles;  // per sequence
+  const int64_t total = before[kThreads] * items;
+  const int64_t run = run_length(a, total);
+  int64_t at = blockIdx.x * run;
+  const int64_t end = min(at + run, total);
+  if (at >= end) return;
+
+  // the sequence of the run's first block
+  int seq;
+  int64_t seq_at;  // where it starts in the list
+  {
+    int t = 0;
+#pragma unroll
+    for (int step = kThreads / 2; step > 0; step >>= 1)
+      if (before[t + step] * items <= at) t += step;
+    // (entries behind the last sequence repeat the total, which is above `at`)
+    seq = t * pl.per;
+    seq_at = before[t] * items;
+    for (;; ++seq) {
+      const int64_t c = (int64_t)span_of(a, a.lens[seq]).count * items;
+      if (at < seq_at + c) break;
+      seq_at += c;
+    }
+  }
+
+  uint8_t* ring = smem + warp * C::kStages * C::kStage;
+  uint32_t* meta = reinterpret_cast<uint32_t*>(smem + C::meta_off) + warp * C::kStages * 8;
+  uint4* s_q = reinterpret_cast<uint4*>(smem + C::q_off);
+  float* s_fac = reinterpret_cast<float*>(smem + C::row_off);
+  int* s_pos = reinterpret_cast<int*>(s_fac + C::R);
+  const uint32_t ring_u = smem_u32(ring), meta_u = smem_u32(meta);
+
+  while (at < end) {
+    Piece p;
+    p.seq = seq;
+    p.len = a.lens[seq];
+    p.span = span_of(a, p.len);
+    if (p.span.count == 0) {
+      ++seq;
+      continue;
+    }
+    const int64_t in_seq = at - seq_at;
+    const int item = (int)(in_seq / p.span.count);
+    p.kvh = item / a.row_tiles;
+    p.rt = item % a.row_tiles;
+    p.t0 = (int)(in_seq - (int64_t)item * p.span.count);
+    p.t1 = (int)min((int64_t)p.span.count, p.t0 + (end - at));
+    at += p.t1 - p.t0;
+    const bool item_done = p.t1 == p.span.count;
+    if (item_done && item == items - 1) {
+      seq_at += (int64_t)p.span.count * items;
+      ++seq;
+    }
+
+    // ---- the asynchronous copies of one block into a ring slot
+    const int* table = a.table + (int64_t)p.seq * a.max_pages;
+    const int page_mask = (1 << a.page_shift) - 1;
+    auto fetch = [&](int t, int slot) {
+      if (t < p.t1) {
+        const int key0 = p.span.block(t) * kBlock;
+        // the block's two groups of 16 keys lie on one page each
+        int pid[2];
+        bool ok[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int key = key0 + 16 * u;
+          const int col = key >> a.page_shift;
+          pid[u] = key < p.span.hi ? table[col] : -1;
+          ok[u] = pid[u] >= 0 && pid[u] < a.num_pages;
+          if (!ok[u]) pid[u] = 0;
+        }
+        const uint32_t dst = ring_u + slot * C::kStage;
+        constexpr int kRowChunks = D / 16;
+        constexpr int kPer = kBlock * kRowChunks / 32;  // chunks per lane and tile
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const int c = u * 32 + lane;
+          const int row = c / kRowChunks, ch = c % kRowChunks;
+          const int half = u >= kPer / 2;  // which group of 16 keys
+          const int key = key0 + row;
+          const bool take = ok[half] && key < p.span.hi && (key >= p.span.lo || key < p.span.sink_hi);
+          const int64_t src = (int64_t)pid[half] * a.page_stride +
+                              (((int64_t)p.kvh << a.page_shift) + (key & page_mask)) * D + ch * 16;
+          const uint32_t off = tile_offset<D>(row, ch);
+          cp_async16(dst + off, a.k + src, take);
+          cp_async16(dst + C::kTile + off, a.v + src, take);
+        }
+        // K and V scales of the two groups, and whether they have a page
+        if (lane < 4) {
+          const int u = lane & 1;
+          const float* sc = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)pid[u] * a.h_kv + p.kvh;
+          cp_async4(meta_u + slot * 32 + lane * 4, sc, ok[u]);
+        }
+        if (lane == 0) meta[slot * 8 + 4] = (ok[0] ? 1u : 0u) | (ok[1] ? 2u : 0u);
+      }
+      cp_async_commit();
+    };
+    int t_load = p.t0 + warp;
+#pragma unroll
+    for (int s = 0; s < C::kStages - 1; ++s) {
+      fetch(t_load, s);
+      t_load += kWarps;
+    }
+
+    // ---- q of the item's rows as f16 fragments, row factors and positions
+    for (int r = warp; r < C::R; r += kWarps) {
+      const int row = p.rt * C::R + r;
+      const bool in = row < a.rows;
+      const int tok = in ? row / a.g : 0, head = p.kvh * a.g + (in ? row % a.g : 0);
+      const __nv_bfloat16* src = a.q + (((int64_t)p.seq * a.s_q + tok) * a.h_q + head) * D;
+      // lane holds D / 32 neighbouring values
+      constexpr int kE = D / 32;
+      float x[kE];
+      float amax = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; e += 2) {
+        const uint32_t w = in ? reinterpret_cast<const uint32_t*>(src)[(lane * kE + e) / 2] : 0u;
+        x[e] = __uint_as_float(w << 16);
+        x[e + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+#pragma unroll
+      for (int e = 0; e < kE; ++e)
+        if (fabsf(x[e]) < INFINITY) amax = fmaxf(amax, fabsf(x[e]));
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+      // the row's largest value goes to [2^14, 2^15)
+      const int ex = bits ? max((int)(bits >> 23) - 127, -100) - 14 : 0;
+      const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+      __half* sq = reinterpret_cast<__half*>(s_q);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) {
+        const int d = lane * kE + e;
+        const int ks = (d >> 6) * 4 + ((d & 15) >> 2);  // k step
+        const int ln = (r & 7) * 4 + ((d >> 4) & 3);    // lane that owns it
+        const int idx = ((((r >> 3) * C::kKSteps + ks) >> 1) * 32 + ln) * 8 + (ks & 1) * 4 + (d & 3);
+        sq[idx] = __float2half_rn(x[e] * inv);
+      }
+      if (lane == 0) {
+        s_fac[r] = in ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) : 0.f;
+        s_pos[r] = in ? p.len - a.s_q + tok : -1;
+      }
+    }
+    __syncthreads();
+    uint4 qf[C::kQRegs ? NT * C::kKSteps / 2 : 1];
+    if constexpr (C::kQRegs) {
+#pragma unroll
+      for (int i = 0; i < NT * C::kKSteps / 2; ++i) qf[i] = s_q[i * 32 + lane];
+    }
+
+    // ---- running state: thread (n8, t4) holds rows 8 nt + 2 t4 + {0, 1}
+    float o[D / 16][NT][4];
+    float m[NT][2], mo[NT][2], l[NT][2];  // reference of P, of P * v_scale (base 2); sum of P
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[nt][c] = mo[nt][c] = -INFINITY;
+        l[nt][c] = 0.f;
+      }
+    }
+    const int p_first = p.len - a.s_q, p_last = p.len - 1;  // query positions
+
+    int slot = 0;
+    for (int t = p.t0 + warp; t < p.t1; t += kWarps) {
+      cp_async_wait<C::kStages - 2>();
+      __syncwarp();
+      {
+        const int next = slot == 0 ? C::kStages - 1 : slot - 1;  // the slot read last time
+        fetch(t_load, next);
+        t_load += kWarps;
+      }
+      const uint8_t* kt = ring + slot * C::kStage;
+      const uint8_t* vt = kt + C::kTile;
+      const uint32_t* mw = meta + slot * 8;
+      const uint32_t pages_ok = mw[4];
+      const int key0 = p.span.block(t) * kBlock;
+
+      // S^T = K q^T
+      float s[2][NT][4];
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[mt][nt][c] = 0.f;
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t w[2][2][4];  // [mt][key group of 8][4 words of 4 codes]
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint4 x = *reinterpret_cast<const uint4*>(
+                kt + tile_offset<D>(mt * 16 + hf * 8 + key_of_row(n8), t4 + 4 * cc));
+            w[mt][hf][0] = x.x;
+            w[mt][hf][1] = x.y;
+            w[mt][hf][2] = x.z;
+            w[mt][hf][3] = x.w;
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t af[2][4];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) {
+            af[mt][0] = widen_lo(w[mt][0][j]);
+            af[mt][1] = widen_lo(w[mt][1][j]);
+            af[mt][2] = widen_hi(w[mt][0][j]);
+            af[mt][3] = widen_hi(w[mt][1][j]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int ks = cc * 4 + j;
+            const int qi = (nt * C::kKSteps + ks) >> 1;
+            uint4 f;
+            if constexpr (C::kQRegs)
+              f = qf[qi];
+            else
+              f = s_q[qi * 32 + lane];
+            const uint32_t b0 = (ks & 1) ? f.z : f.x, b1 = (ks & 1) ? f.w : f.y;
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt) mma16816(s[mt][nt], af[mt], b0, b1);
+          }
+        }
+      }
+
+      // scores in base 2; s[mt][nt][c]: key 16 mt + 8 (c >> 1) + key_of_row(n8),
+      // row 8 nt + 2 t4 + (c & 1)
+      const float ks_[2] = {__uint_as_float(mw[0]), __uint_as_float(mw[1])};
+      const float lvs[2] = {log2f(__uint_as_float(mw[2])), log2f(__uint_as_float(mw[3]))};
+      const bool all_seen = pages_ok == 3u && key0 + kBlock - 1 <= p_first &&
+                            (a.window < 0 || p_last - key0 <= a.window || key0 + kBlock - 1 < a.sink);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float2 fac = *reinterpret_cast<const float2*>(s_fac + 8 * nt + 2 * t4);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[mt][nt][c] *= ((c & 1) ? fac.y : fac.x) * ks_[mt];
+        }
+      }
+      if (!all_seen) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int2 pq = *reinterpret_cast<const int2*>(s_pos + 8 * nt + 2 * t4);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int key = key0 + 16 * mt + 8 * (c >> 1) + key_of_row(n8);
+              const int q = (c & 1) ? pq.y : pq.x;
+              const bool see = ((pages_ok >> mt) & 1u) && key < p.span.hi && key <= q &&
+                               (a.window < 0 || q - key <= a.window || key < a.sink);
+              if (!see) s[mt][nt][c] = -INFINITY;
+            }
+        }
+      }
+
+      // raise the references where a score passed them by more than kRescale
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const float x0 = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+          const float x1 = fmaxf(s[1][nt][c], s[1][nt][c + 2]);
+          raise |= fmaxf(x0, x1) > m[nt][c] + kRescale;
+          raise |= fmaxf(x0 + lvs[0], x1 + lvs[1]) > mo[nt][c] + kRescale;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float x0 = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
+            const float x1 = fmaxf(s[1][nt][c], s[1][nt][c + 2]);
+            float a0 = fmaxf(x0, x1), a1 = fmaxf(x0 + lvs[0], x1 + lvs[1]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, off));
+              a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, off));
+            }
+            if (a0 > m[nt][c]) {
+              l[nt][c] *= ex2(m[nt][c] - a0);
+              m[nt][c] = a0;
+            }
+            if (a1 > mo[nt][c]) {
+              const float f = ex2(mo[nt][c] - a1);
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                o[i][nt][c] *= f;
+                o[i][nt][c + 2] *= f;
+              }
+              mo[nt][c] = a1;
+            }
+          }
+      }
+
+      // P^T fragments: p = 2^(x - m) for the sum, p * 2^(lvs + m - mo) for O
+      uint32_t pb[2][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float sub[2], up[2][2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          sub[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
+          const float so = mo[nt][c] == -INFINITY ? 0.f : mo[nt][c];
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt) up[mt][c] = ex2(fminf(lvs[mt] + sub[c] - so, 120.f));
+        }
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt) {
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            e[c] = ex2(s[mt][nt][c] - sub[c & 1]);
+            l[nt][c & 1] += e[c];
+            e[c] *= up[mt][c & 1];
+          }
+          pb[mt][nt][0] = transpose8x8(pack_f16(e[0], e[1]));
+          pb[mt][nt][1] = transpose8x8(pack_f16(e[2], e[3]));
+        }
+      }
+
+      // O^T += V^T P^T
+      if (a.s_q > 1 && !all_seen && holds_nan<D>(vt, lane)) {
+        // NaN among keys that not every query sees (0 * NaN is NaN): the product
+        // without them, then NaN where a query sees one
+        uint32_t see[2][NT][2];
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const int2 pq = *reinterpret_cast<const int2*>(s_pos + 8 * nt + 2 * t4);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              const int key = key0 + 16 * mt + 8 * hf + key_of_row(n8);
+              const bool s0 = key <= pq.x && (a.window < 0 || pq.x - key <= a.window || key < a.sink);
+              const bool s1 = key <= pq.y && (a.window < 0 || pq.y - key <= a.window || key < a.sink);
+              see[mt][nt][hf] = transpose8x8(pack_f16(s0 ? 1.f : 0.f, s1 ? 1.f : 0.f));
+            }
+          }
+        add_pv<D, NT, kNoNan>(o, vt, pb, n8, t4);
+        add_pv<D, NT, kOnlyNan>(o, vt, see, n8, t4);
+      } else {
+        add_pv<D, NT, kPlain>(o, vt, pb, n8, t4);
+      }
+      slot = slot == C::kStages - 1 ? 0 : slot + 1;
+    }
+    cp_async_wait<0>();
+
+    // ---- the four warps' results through shared memory (the ring is empty)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
+    __syncthreads();
+    float* buf = reinterpret_cast<float*>(smem);                        // [warp][R][kMergeRow]
+    float* st = buf + kWarps * C::R * C::kMergeRow;                     // [warp][R][3]
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 8 * nt + 2 * t4 + c;
+        float* row = buf + (warp * C::R + r) * C::kMergeRow;
+        if constexpr (D == 64) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)  // d = 8 n8 + 4 j ..
+            *reinterpret_cast<float4*>(row + 8 * n8 + 4 * j) =
+                make_float4(o[2 * j][nt][c], o[2 * j][nt][c + 2], o[2 * j + 1][nt][c], o[2 * j + 1][nt][c + 2]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j)  // d = 128 (j / 4) + 16 key_of_row(n8) + 4 (j % 4) ..
+            *reinterpret_cast<float4*>(row + (j >> 2) * 128 + 16 * key_of_row(n8) + 4 * (j & 3)) =
+                make_float4(o[2 * j][nt][c], o[2 * j][nt][c + 2], o[2 * j + 1][nt][c], o[2 * j + 1][nt][c + 2]);
+        }
+        if (n8 == 0) {
+          float* x = st + (warp * C::R + r) * 3;
+          x[0] = m[nt][c];
+          x[1] = mo[nt][c];
+          x[2] = l[nt][c];
+        }
+      }
+    __syncthreads();
+    {
+      const bool whole = p.t0 == 0 && item_done;
+      // a piece that starts inside its item is the first of this CTA, one that
+      // ends inside it the last: one slot each
+      const int64_t part = 2 * (int64_t)blockIdx.x + (p.t0 == 0 ? 1 : 0);
+      constexpr int kVec = D / 4;
+      for (int u = threadIdx.x; u < C::R * kVec; u += kThreads) {
+        const int r = u / kVec, d4 = u % kVec;
+        const int row = p.rt * C::R + r;
+        if (row >= a.rows) break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st[(w * C::R + r) * 3]);
+        const float ref = top == -INFINITY ? 0.f : top;
+        float z = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float* x = st + (w * C::R + r) * 3;
+          z += x[2] * ex2(x[0] - ref);
+          const float f = ex2(x[1] - ref);
+          const float4 v = *reinterpret_cast<const float4*>(buf + (w * C::R + r) * C::kMergeRow + 4 * d4);
+          acc.x += v.x * f;
+          acc.y += v.y * f;
+          acc.z += v.z * f;
+          acc.w += v.w * f;
+        }
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+        acc.x *= inv;
+        acc.y *= inv;
+        acc.z *= inv;
+        acc.w *= inv;
+        const float lse2 = z == 0.f ? -INFINITY : ref + log2f(z);
+        if (whole) {
+          const int tok = row / a.g, head = p.kvh * a.g + row % a.g;
+          const int64_t orow = ((int64_t)p.seq * a.s_q + tok) * a.h_q + head;
+          if (a.out_fp32)
+            reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = acc;
+          else
+            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
+                make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+          if (d4 == 0) a.lse[((int64_t)p.seq * a.h_q + head) * a.s_q + tok] = lse2 * kLn2;
+        } else {
+          reinterpret_cast<float4*>(a.part_o + (part * C::R + r) * D)[d4] = acc;
+          if (d4 == 0) a.part_lse[part * C::R + r] = lse2;
+        }
+      }
+    }
+    __syncthreads();  // the ring, q and the row values are free again
+  }
+}
+
+// One CTA per item: folds the partials of an item that several CTAs shared,
+// and writes the empty result of a sequence without keys.
+template <int D, int R>
+__global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const DecodeArgs a) {
+  __shared__ int64_t before[kThreads + 1];
+  const Placement pl = place(a, before);
+  const int items = a.h_kv * a.row_tiles;
+  const int seq = blockIdx.x / items, item = blockIdx.x % items;
+  const int64_t total = before[kThreads] * items;
+  const int64_t run = run_length(a, total);
+  const int t = seq / pl.per;
+  int64_t seq_at = before[t];
+  for (int i = t * pl.per; i < seq; ++i) seq_at += span_of(a, a.lens[i]).count;
+  const int count = span_of(a, a.lens[seq]).count;
+  const int64_t s0 = seq_at * items + (int64_t)item * count;  // the item's blocks: [s0, s0 + count)
+  const int64_t c0 = count ? s0 / run : 0, c1 = count ? (s0 + count - 1) / run : 0;
+  // every CTA waits, so that this grid never ends before the one it depends on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (count && c0 == c1) return;  // written whole
+  const int kvh = item / a.row_tiles, rt = item % a.row_tiles;
+  constexpr int kVec = D / 4;
+  for (int u = threadIdx.x; u < R * kVec; u += kThreads) {
+    const int r = u / kVec, d4 = u % kVec;
+    const int row = rt * R + r;
+    if (row >= a.rows) break;
+    float top = -INFINITY;
+    // only the first piece can be a CTA's last one (it starts at the item's start)
+    auto slot = [&](int64_t c) { return 2 * c + (c * run <= s0 ? 1 : 0); };
+    if (count)
+      for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, a.part_lse[slot(c) * R + r]);
+    const float ref = top == -INFINITY ? 0.f : top;
+    float z = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (count)
+      for (int64_t c = c0; c <= c1; ++c) {
+        const float f = ex2(a.part_lse[slot(c) * R + r] - ref);
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(c) * R + r) * D)[d4];
+        z += f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+      }
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    const int tok = row / a.g, head = kvh * a.g + row % a.g;
+    const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
+    acc.x *= inv;
+    acc.y *= inv;
+    acc.z *= inv;
+    acc.w *= inv;
+    if (a.out_fp32)
+      reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = acc;
+    else
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
+          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+    if (d4 == 0)
+      a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (ref + log2f(z)) * kLn2;
+  }
+}
+
+// N tiles of 8 rows per CTA: the fewest that hold the rows, up to what the
+// registers allow for the accumulators (D * NT <= 512 values per row tile).
+int n_tiles(int64_t d, int64_t rows) {
+  const int most = d == 256 ? 2 : 4;
+  const int need = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+  return need < most ? need : most;
+}
+
+template <int D, int NT>
+struct Kernel {
+  using C = Cfg<D, NT>;
+  // CTAs that fill the device once
+  static cudaError_t grid(int* n) {
+    static std::atomic<int> cache[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool cached = dev >= 0 && dev < kMaxDevices;
+    *n = cached ? cache[dev].load(std::memory_order_acquire) : 0;
+    if (*n > 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes);
+    int per_sm = 0;
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_decode_kernel<D, NT>, kThreads, C::bytes);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    *n = per_sm * sm_count();
+    if (cached) cache[dev].store(*n, std::memory_order_release);
+    return cudaSuccess;
+  }
+  static cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
+    int n = 0;
+    cudaError_t e = grid(&n);
+    if (e != cudaSuccess) return e;
+    a.grid = n;
+    a.part_lse = a.part_o + (int64_t)2 * n * C::R * D;
+    attn_decode_kernel<D, NT><<<n, kThreads, C::bytes, st>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.h_kv * a.row_tiles));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel<D, C::R>, a);
+  }
+};
+
+template <typename F>
+cudaError_t dispatch(int64_t d, int nt, F&& f) {
+  if (d == 64) {
+    if (nt == 1) return f(Kernel<64, 1>());
+    if (nt == 2) return f(Kernel<64, 2>());
+    return f(Kernel<64, 4>());
+  }
+  if (d == 128) {
+    if (nt == 1) return f(Kernel<128, 1>());
+    if (nt == 2) return f(Kernel<128, 2>());
+    return f(Kernel<128, 4>());
+  }
+  if (nt == 1) return f(Kernel<256, 1>());
+  return f(Kernel<256, 2>());
+}
+
+}  // namespace
+
+cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes) {
+  const int64_t d = p.cache.d, rows = p.s_q * (p.h_q / p.cache.h_kv);
+  const int nt = n_tiles(d, rows);
+  return dispatch(d, nt, [&](auto k) {
+    int n = 0;
+    const cudaError_t e = k.grid(&n);
+    *bytes = align_up((size_t)2 * n * nt * 8 * (d + 1) * 4, 256);
+    return e;
+  });
+}
+
+cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
+  const attn_kv_cache& c = p.cache;
+  DecodeArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(p.q);
+  a.k = static_cast<const uint8_t*>(c.k);
+  a.v = static_cast<const uint8_t*>(c.v);
+  a.k_scale = c.k_scale;
+  a.v_scale = c.v_scale;
+  a.table = p.page_table;
+  a.lens = p.seqlens;
+  a.out = p.out;
+  a.lse = p.lse;
+  a.part_o = static_cast<float*>(p.workspace);
+  a.page_stride = c.page_stride > 0 ? c.page_stride : c.h_kv * c.page_size * c.d;
+  a.n = (int)p.n;
+  a.s_q = (int)p.s_q;
+  a.h_q = (int)p.h_q;
+  a.h_kv = (int)c.h_kv;
+  a.g = (int)(p.h_q / c.h_kv);
+  a.rows = a.s_q * a.g;
+  const int nt = n_tiles(c.d, a.rows);
+  a.row_tiles = (a.rows + nt * 8 - 1) / (nt * 8);
+  a.max_pages = (int)p.max_pages;
+  a.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
+  a.num_pages = (int)c.num_pages;
+  a.window = p.window_left;
+  a.sink = (int)p.sink_tokens;
+  a.out_fp32 = p.out_fp32 ? 1 : 0;
+  a.scale_log2 = p.scale * 1.4426950408889634f;
+  return dispatch(c.d, nt, [&](auto k) { return k.launch(a, st); });
+}
+
+}  // namespace gb300

@@ -135,6 +135,7 @@ inline PlanPtrs plan_ptrs(void* ws, const PlanLayout& L) {
 }
 
 // ---- kernels_misc.cu
+int sm_count();  // SMs of the current device
 // q_ctas / kv_ctas: CTAs the kernel that takes the query / key side's work
 // order launches per unit (the order is chosen from it; kernels_misc.cu).
 cudaError_t launch_tile_plan(const attn_fwd_params& p, const PlanPtrs& pp, int64_t nq, int64_t nk,
@@ -199,6 +200,16 @@ int split_bwd_key_rows(int64_t d, int64_t dv);
 // dK / dV kernel CTAs per (b, key tile) and kv head: column slices of dK / dV
 int split_bwd_col_slices(int64_t d, int64_t dv);
 cudaError_t launch_attn_bwd_split(const SplitLaunch& L, cudaStream_t st);
+
+// ---- kv_cache.cu
+cudaError_t launch_kv_append(const attn_kv_append_params& p, cudaStream_t st);
+cudaError_t launch_kv_copy(const attn_kv_cache& c, const int* src, const int* dst, int64_t n,
+                           cudaStream_t st);
+
+// ---- attn_decode.cu
+constexpr int kDecodeBlock = 32;  // keys per block of the decode kernel's work list
+cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes);
+cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st);
 
 // ---- attn_api.cu
 bool encode_qkv_map(CUtensorMap* m, const void* base, int64_t b, int64_t s, int64_t h, int64_t d,

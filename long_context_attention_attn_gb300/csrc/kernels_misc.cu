@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(1024)
 }
 
 // SM count of the current device (cached per device; safe across host threads).
-static int sm_count() {
+int sm_count() {
   static std::atomic<int> cache[kMaxDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = 0;
