@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "libgb300attn.so")
 ATTN_OK, ATTN_ERR_INVALID_ARG, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_TIMEOUT = range(5)
 DUAL_CHUNK, STRIPED = 0, 1
 TILE = 128
+_CODES = (torch.float8_e4m3fn, torch.uint8)  # what a cache's pages may be typed as
 
 EXPORTS = (
     "attn_fwd_workspace_bytes", "attn_bwd_workspace_bytes", "attn_fwd", "attn_bwd",
@@ -426,40 +427,57 @@ def attn_merge_partial(out_acc, lse_acc, out_blk, lse_blk, out_final=None):
     return (out_final if out_final is not None else out_acc), lse_acc
 
 
-def _on(device, *ts):
-    for t in ts:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors of a call must be on one CUDA device")
+class _Device:
+    """Makes a device current for a call (nothing where it is already)."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
 
 
-def _index(t, shape, what: str):
-    if t is not None and (t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous()):
+def _index(t, shape, index: int, what: str) -> int:
+    """Address of a contiguous int32 tensor of this shape on CUDA device ``index``."""
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous int32 {list(shape)} tensor")
+    if t.get_device() != index:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    return t.data_ptr()
 
 
-def _kv_cache(c: KvCache, k_cache, v_cache, k_scale, v_scale):
-    """Fills c from a cache: k / v e4m3 (or uint8) [num_pages, h_kv, page_size, d], pages dense
-    inside (they may be the halves of one buffer), scales fp32 [num_pages, h_kv]."""
-    dev = k_cache.device
-    if dev.type != "cuda":
+def _kv_cache(k_cache, v_cache, k_scale, v_scale):
+    """The KvCache of a cache: k / v e4m3 (or uint8) [num_pages, h_kv, page_size, d], pages dense
+    inside (they may be the halves of one buffer), scales fp32 [num_pages, h_kv].  Returns it
+    with its CUDA device index, heads and head dim."""
+    index = k_cache.get_device()
+    if index < 0:
         raise ValueError("gb300attn runs on CUDA tensors only")
-    _on(dev, v_cache, k_scale, v_scale)
+    if v_cache.get_device() != index or k_scale.get_device() != index or v_scale.get_device() != index:
+        raise ValueError("all tensors of a call must be on one CUDA device")
     shape, st = k_cache.shape, k_cache.stride()
     if len(shape) != 4 or v_cache.shape != shape or v_cache.stride() != st:
         raise ValueError("k_cache / v_cache must share one shape [num_pages, h_kv, page_size, d] and layout")
-    if any(t.dtype not in (torch.float8_e4m3fn, torch.uint8) for t in (k_cache, v_cache)):
+    if k_cache.dtype not in _CODES or v_cache.dtype not in _CODES:
         raise ValueError("k_cache / v_cache hold float8_e4m3fn (or its bytes as uint8)")
     pages, h, size, d = shape
+    page = h * size * d
     if (d > 1 and st[3] != 1) or (size > 1 and st[2] != d) or (h > 1 and st[1] != size * d):
         raise ValueError("k_cache / v_cache: each page must be contiguous")
-    for t in (k_scale, v_scale):
-        if t.dtype != torch.float32 or t.shape != (pages, h) or not t.is_contiguous():
-            raise ValueError("k_scale / v_scale must be contiguous fp32 [num_pages, h_kv] tensors")
-    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
-    c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-    c.num_pages, c.h_kv, c.page_size, c.d = pages, h, size, d
-    c.page_stride = st[0] if pages > 1 and st[0] != h * size * d else 0
-    return dev, shape
+    if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32
+            or k_scale.shape != (pages, h) or v_scale.shape != (pages, h)
+            or not k_scale.is_contiguous() or not v_scale.is_contiguous()):
+        raise ValueError("k_scale / v_scale must be contiguous fp32 [num_pages, h_kv] tensors")
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   pages, h, size, d, st[0] if pages > 1 and st[0] != page else 0), index, h, d
 
 
 def _row_stride(x) -> int:
@@ -487,36 +505,31 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
     page already holds tokens the larger of that and its scale is kept and
     grown scales requantise them.  Pages shared between sequences are copied
     first (:func:`kv_cache_copy_pages`)."""
-    p = KvAppendParams()
-    dev, shape = _kv_cache(p.cache, k_cache, v_cache, k_scale, v_scale)
-    if k.dim() != 4 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
-        raise ValueError("k / v must be bf16 [b, s, h_kv, d] tensors")
-    b, s, h, d = k.shape
-    if h != shape[1] or d != shape[3]:
-        raise ValueError("k / v must have the cache's heads and head dim")
-    p.token_stride = _row_stride(k)
-    if v.shape != k.shape or _row_stride(v) != p.token_stride:
-        raise ValueError("k / v must share one shape and token stride")
+    cache, index, h, d = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    if (k.dim() != 4 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.shape != k.shape
+            or k.shape[2] != h or k.shape[3] != d):
+        raise ValueError("k / v must be bf16 [b, s, h_kv, d] tensors with the cache's heads and head dim")
+    if k.get_device() != index or v.get_device() != index:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    step = _row_stride(k)
+    if _row_stride(v) != step:
+        raise ValueError("k / v must share one token stride")
     if page_table.dim() != 2:
         raise ValueError("page_table must be a contiguous int32 [n, max_pages] tensor")
-    n = page_table.shape[0]
-    _on(dev, k, v, page_table, start, lens, tok_start)
-    _index(page_table, page_table.shape, "page_table")
-    for t, what in ((start, "start"), (lens, "lens"), (tok_start, "tok_start")):
-        _index(t, (n,), what)
+    b, s = k.shape[:2]
+    n, max_pages = page_table.shape
     if tok_start is None and n != b:
         raise ValueError("page_table must have a row per row of k (or pass tok_start)")
-    p.k, p.v, p.tokens = k.data_ptr(), v.data_ptr(), b * s
-    p.page_table, p.n, p.max_pages = page_table.data_ptr(), n, page_table.shape[1]
-    p.start = start.data_ptr()
-    p.lens = None if lens is None else lens.data_ptr()
-    p.row_tokens = s
-    if tok_start is not None:
-        p.tok_start = tok_start.data_ptr()
     most = s if tok_start is None else b * s
-    p.max_new = most if max_new is None else min(int(max_new), most)
-    with torch.cuda.device(dev):
-        _check(lib().attn_kv_append(ctypes.byref(p), _stream(dev)), "attn_kv_append")
+    p = KvAppendParams(
+        cache, k.data_ptr(), v.data_ptr(), b * s, step,
+        _index(page_table, page_table.shape, index, "page_table"), n, max_pages,
+        _index(start, (n,), index, "start"),
+        None if lens is None else _index(lens, (n,), index, "lens"),
+        None if tok_start is None else _index(tok_start, (n,), index, "tok_start"),
+        s, most if max_new is None else min(int(max_new), most))
+    with _Device(index):
+        _check(lib().attn_kv_append(ctypes.byref(p), _stream(index)), "attn_kv_append")
 
 
 def kv_cache_copy_pages(k_cache, v_cache, k_scale, v_scale, src, dst):
@@ -525,53 +538,52 @@ def kv_cache_copy_pages(k_cache, v_cache, k_scale, v_scale, src, dst):
     to the front of a pool.  Pairs with an index that is no page, or with src
     == dst, are skipped; a page must not be a destination twice, or both a
     destination and a source."""
-    c = KvCache()
-    dev, _ = _kv_cache(c, k_cache, v_cache, k_scale, v_scale)
-    _on(dev, src, dst)
+    c, index, _, _ = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     if src.dim() != 1:
         raise ValueError("src / dst must be contiguous int32 [n] tensors")
-    _index(src, src.shape, "src")
-    _index(dst, src.shape, "dst")
+    a, b = _index(src, src.shape, index, "src"), _index(dst, src.shape, index, "dst")
     if src.shape[0] == 0:
         return
-    with torch.cuda.device(dev):
-        _check(lib().attn_kv_copy_pages(ctypes.byref(c), src.data_ptr(), dst.data_ptr(), src.shape[0],
-                                        _stream(dev)), "attn_kv_copy_pages")
+    with _Device(index):
+        _check(lib().attn_kv_copy_pages(ctypes.byref(c), a, b, src.shape[0], _stream(index)),
+               "attn_kv_copy_pages")
 
 
 def _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
                    sink_tokens, scale, out, lse, out_fp32):
-    p = DecodeParams()
-    dev, shape = _kv_cache(p.cache, k_cache, v_cache, k_scale, v_scale)
-    _on(dev, q, page_table, seqlens, out, lse)
-    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[3] != shape[3]:
+    """(DecodeParams without a workspace, device index, out, lse): allocates out / lse where None."""
+    cache, index, _, d = _kv_cache(k_cache, v_cache, k_scale, v_scale)
+    if q.dim() != 4 or q.dtype != torch.bfloat16 or not q.is_contiguous() or q.shape[3] != d:
         raise ValueError("q must be a contiguous bf16 [n, s_q, h_q, d] tensor with the cache's head dim")
-    n, s_q, h_q, d = q.shape
+    if q.get_device() != index:
+        raise ValueError("all tensors of a call must be on one CUDA device")
     if page_table.dim() != 2:
         raise ValueError("page_table must be a contiguous int32 [n, max_pages] tensor")
-    _index(page_table, (n, page_table.shape[1]), "page_table")
-    _index(seqlens, (n,), "seqlens")
-    if out is not None and (out.shape != q.shape or not out.is_contiguous()
-                            or out.dtype != (torch.float32 if out_fp32 else torch.bfloat16)):
+    n, s_q, h_q, _ = q.shape
+    kind = torch.float32 if out_fp32 else torch.bfloat16
+    if out is None:
+        out = torch.empty_like(q, dtype=kind)
+    elif (out.shape != q.shape or out.dtype != kind or not out.is_contiguous()
+          or out.get_device() != index):
         raise ValueError("out must be a contiguous [n, s_q, h_q, d] tensor, bf16 (fp32 with out_fp32)")
-    if lse is not None and (lse.shape != (n, h_q, s_q) or lse.dtype != torch.float32
-                            or not lse.is_contiguous()):
+    if lse is None:
+        lse = torch.empty((n, h_q, s_q), dtype=torch.float32, device=q.device)
+    elif (lse.shape != (n, h_q, s_q) or lse.dtype != torch.float32 or not lse.is_contiguous()
+          or lse.get_device() != index):
         raise ValueError("lse must be a contiguous fp32 [n, h_q, s_q] tensor")
-    p.q, p.page_table, p.seqlens = q.data_ptr(), page_table.data_ptr(), seqlens.data_ptr()
-    p.n, p.max_pages, p.s_q, p.h_q = n, page_table.shape[1], s_q, h_q
-    p.window_left, p.sink_tokens = int(window_left), int(sink_tokens)
-    p.out_fp32 = 1 if out_fp32 else 0
-    p.scale = float(d ** -0.5 if scale is None else scale)
-    p.out = q.data_ptr() if out is None else out.data_ptr()
-    p.lse = q.data_ptr() if lse is None else lse.data_ptr()
-    return p, dev
+    max_pages = page_table.shape[1]
+    return DecodeParams(
+        cache, q.data_ptr(), _index(page_table, (n, max_pages), index, "page_table"), n, max_pages,
+        _index(seqlens, (n,), index, "seqlens"), s_q, h_q, int(window_left), 1 if out_fp32 else 0,
+        int(sink_tokens), d ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        lse.data_ptr()), index, out, lse
 
 
 def workspace_bytes_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens) -> int:
     """Workspace bytes attn_decode needs for these shapes on q's device (0 if it rejects them)."""
-    p, dev = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, -1, 0, None,
-                            None, None, False)
-    with torch.cuda.device(dev):
+    p, index, _, _ = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, -1, 0,
+                                    None, None, None, False)
+    with _Device(index):
         return int(lib().attn_decode_workspace_bytes(ctypes.byref(p)))
 
 
@@ -591,23 +603,16 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
     With ``out_fp32`` out is a partial for :func:`attn_merge_partial`.  Calls
     that overlap on the GPU need a ``workspace`` each (by default each call
     allocates its own)."""
-    p, dev = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
-                            sink_tokens, scale, out, lse, out_fp32)
-    if out is None:
-        out = torch.empty(q.shape, device=dev, dtype=torch.float32 if out_fp32 else torch.bfloat16)
-        p.out = out.data_ptr()
-    if lse is None:
-        lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], device=dev, dtype=torch.float32)
-        p.lse = lse.data_ptr()
-    with torch.cuda.device(dev):
+    p, index, out, lse = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens,
+                                        window_left, sink_tokens, scale, out, lse, out_fp32)
+    with _Device(index):
         if workspace is None:
-            workspace = _workspace(int(lib().attn_decode_workspace_bytes(ctypes.byref(p))), dev)
-        else:
-            _need_cuda(workspace)
-            _on(dev, workspace)
+            workspace = _workspace(lib().attn_decode_workspace_bytes(ctypes.byref(p)), q.device)
+        elif workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the call's device")
         p.workspace = workspace.data_ptr()
-        p.workspace_bytes = workspace.numel() * workspace.element_size()
-        _check(lib().attn_decode(ctypes.byref(p), _stream(dev)), "attn_decode")
+        p.workspace_bytes = workspace.nbytes
+        _check(lib().attn_decode(ctypes.byref(p), _stream(index)), "attn_decode")
     return out, lse
 
 

@@ -40,6 +40,8 @@
 // element-wise warps' path costs latency per step.
 #include <cuda_bf16.h>
 
+#include <climits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -494,7 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
-    const int window = pk < a.sink ? -1 : a.window;  // this key's window
+    // farthest query that sees this key (no branch per pair: a warp's keys may differ)
+    const int reach = (a.window < 0 || pk < a.sink) ? INT_MAX : a.window;
     const float sl2 = a.scale_log2;
     uint8_t* ds_smem = smem + L::ds_off + w * L::kChunk + kr * 128;
     constexpr int kHalf = D / 2;         // dQ columns read back by this half
@@ -538,9 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qa[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            bool vis = (ia[u] == ik) && (ik != 0) && (pk <= qa[u]);
-            if (window >= 0) vis = vis && (qa[u] - pk <= window);
-            if (!vis) p[4 * c + u] = 0.f;
+            const bool vis = (ia[u] == ik) & (ik != 0) & (pk <= qa[u]) & (qa[u] - pk <= reach);
+            p[4 * c + u] = vis ? p[4 * c + u] : 0.f;
           }
         }
       }

@@ -35,6 +35,8 @@
 // latency every step.
 #include <cuda_bf16.h>
 
+#include <climits>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -91,10 +93,12 @@ struct SplitArgs {
   float c_shift;     // -ln(scale) / scale
 };
 
-__device__ __forceinline__ bool visible(int iq, int pq, int ik, int pk, int window) {
-  bool v = (iq == ik) && (iq != 0) && (pk <= pq);
-  if (window >= 0) v = v && (pq - pk <= window);
-  return v;
+// reach: how far behind a query the key at pk may lie (key_reach below)
+__device__ __forceinline__ bool visible(int iq, int pq, int ik, int pk, int reach) {
+  return (iq == ik) & (iq != 0) & (pk <= pq) & (pq - pk <= reach);
+}
+__device__ __forceinline__ int key_reach(int pk, int window, int sink) {
+  return (window < 0 || pk < sink) ? INT_MAX : window;
 }
 
 // ============================================================== dK / dV
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
-    const int window = pk < a.sink ? -1 : a.window;  // this key's window
+    const int reach = key_reach(pk, a.window, a.sink);  // this key's
     const float sl2 = a.scale_log2;
     if constexpr (KT || VT) {
       // this thread's key (KT) and value (VT) rows into TMEM as bf16 pairs
@@ -594,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qa[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (!visible(ia[u], qa[u], ik, pk, window)) p[4 * c + u] = 0.f;
+            p[4 * c + u] = visible(ia[u], qa[u], ik, pk, reach) ? p[4 * c + u] : 0.f;
         }
       }
       uint32_t pk2[kHB / 2];
@@ -1042,7 +1046,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ka[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (!visible(iq, pq, ia[u], ka[u], ka[u] < a.sink ? -1 : a.window)) p[4 * c + u] = 0.f;
+            p[4 * c + u] = visible(iq, pq, ia[u], ka[u], key_reach(ka[u], a.window, a.sink)) ? p[4 * c + u] : 0.f;
         }
       }
       mbar_arrive(&bars->id_empty[en]);

@@ -124,7 +124,10 @@ __device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total
 }
 
 // ---------------------------------------------------------------- primitives
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(take ? 16 : 0)
                : "memory");
@@ -158,6 +161,13 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Hardware base-2 logarithm (exact for powers of two); of 0 -inf.
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // Transposes the 8 x 8 f16 matrix that the warp holds one row per four lanes.
@@ -272,6 +282,15 @@ __device__ __forceinline__ bool holds_nan(const uint8_t* vt, int lane) {
   return __any_sync(0xffffffffu, nan);
 }
 
+// Where the 512 bytes number u of a tile go, from the place of the lane's 16 in
+// the first 512 (tile_offset of row lane / (D / 16)): the following rows only
+// turn the XORed chunk bits.
+template <int D>
+__device__ __forceinline__ uint32_t copy_offset(uint32_t lane_off, int u) {
+  const uint32_t turn = D == 64 ? 0 : D == 128 ? (u & 1) * 64 : (u & 3) * 32;
+  return (lane_off ^ turn) + u * 512;
+}
+
 template <int D, int NT>
 struct Cfg {
   static constexpr int R = NT * 8;                  // rows per tile
@@ -337,6 +356,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
   float* s_fac = reinterpret_cast<float*>(smem + C::row_off);
   int* s_pos = reinterpret_cast<int*>(s_fac + C::R);
   const uint32_t ring_u = smem_u32(ring), meta_u = smem_u32(meta);
+  const uint32_t lane_off = tile_offset<D>(lane / (D / 16), lane % (D / 16));
 
   while (at < end) {
     Piece p;
@@ -369,29 +389,44 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
         // the block's two groups of 16 keys lie on one page each
         int pid[2];
         bool ok[2];
+        pid[0] = table[key0 >> a.page_shift];
+        pid[1] = pid[0];
+        if (a.page_shift == 4) pid[1] = key0 + 16 < p.span.hi ? table[(key0 >> 4) + 1] : -1;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int key = key0 + 16 * u;
-          const int col = key >> a.page_shift;
-          pid[u] = key < p.span.hi ? table[col] : -1;
           ok[u] = pid[u] >= 0 && pid[u] < a.num_pages;
           if (!ok[u]) pid[u] = 0;
         }
+        // a group's rows are neighbours in memory, 32 lanes take 512 bytes at a time
         const uint32_t dst = ring_u + slot * C::kStage;
-        constexpr int kRowChunks = D / 16;
-        constexpr int kPer = kBlock * kRowChunks / 32;  // chunks per lane and tile
+        constexpr int kPer = kBlock * D / 512;
+        const uint8_t *kp[2], *vp[2];
 #pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          const int c = u * 32 + lane;
-          const int row = c / kRowChunks, ch = c % kRowChunks;
-          const int half = u >= kPer / 2;  // which group of 16 keys
-          const int key = key0 + row;
-          const bool take = ok[half] && key < p.span.hi && (key >= p.span.lo || key < p.span.sink_hi);
-          const int64_t src = (int64_t)pid[half] * a.page_stride +
-                              (((int64_t)p.kvh << a.page_shift) + (key & page_mask)) * D + ch * 16;
-          const uint32_t off = tile_offset<D>(row, ch);
-          cp_async16(dst + off, a.k + src, take);
-          cp_async16(dst + C::kTile + off, a.v + src, take);
+        for (int u = 0; u < 2; ++u) {
+          const int64_t src = (int64_t)pid[u] * a.page_stride +
+                              (((int64_t)p.kvh << a.page_shift) + ((key0 + 16 * u) & page_mask)) * D + lane * 16;
+          kp[u] = a.k + src;
+          vp[u] = a.v + src;
+        }
+        const bool whole = ok[0] && ok[1] && key0 + kBlock <= p.span.hi &&
+                           (key0 >= p.span.lo || key0 + kBlock <= p.span.sink_hi);
+        if (whole) {
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const uint32_t off = copy_offset<D>(lane_off, u);
+            cp_async16(dst + off, kp[2 * u / kPer] + (u % (kPer / 2)) * 512);
+            cp_async16(dst + C::kTile + off, vp[2 * u / kPer] + (u % (kPer / 2)) * 512);
+          }
+        } else {
+          // zeros for what no query sees
+#pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int key = key0 + u * (512 / D) + lane / (D / 16);
+            const bool take = ok[2 * u / kPer] && key < p.span.hi && (key >= p.span.lo || key < p.span.sink_hi);
+            const uint32_t off = copy_offset<D>(lane_off, u);
+            cp_async16_or_zero(dst + off, kp[2 * u / kPer] + (u % (kPer / 2)) * 512, take);
+            cp_async16_or_zero(dst + C::kTile + off, vp[2 * u / kPer] + (u % (kPer / 2)) * 512, take);
+          }
         }
         // K and V scales of the two groups, and whether they have a page
         if (lane < 4) {
@@ -537,7 +572,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
       // scores in base 2; s[mt][nt][c]: key 16 mt + 8 (c >> 1) + key_of_row(n8),
       // row 8 nt + 2 t4 + (c & 1)
       const float ks_[2] = {__uint_as_float(mw[0]), __uint_as_float(mw[1])};
-      const float lvs[2] = {log2f(__uint_as_float(mw[2])), log2f(__uint_as_float(mw[3]))};
+      const float lvs[2] = {lg2(__uint_as_float(mw[2])), lg2(__uint_as_float(mw[3]))};
       const bool all_seen = pages_ok == 3u && key0 + kBlock - 1 <= p_first &&
                             (a.window < 0 || p_last - key0 <= a.window || key0 + kBlock - 1 < a.sink);
 #pragma unroll
@@ -766,43 +801,72 @@ __global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const Dec
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (count && c0 == c1) return;  // written whole
   const int kvh = item / a.row_tiles, rt = item % a.row_tiles;
-  constexpr int kVec = D / 4;
-  for (int u = threadIdx.x; u < R * kVec; u += kThreads) {
-    const int r = u / kVec, d4 = u % kVec;
+  // The weights of up to kMost pieces at a time through shared memory, then
+  // their rows, several loads in flight; later batches of pieces rescale.
+  constexpr int kMost = 32;
+  __shared__ float s_w[kMost][R];
+  __shared__ float s_ref[R], s_old[R];
+  constexpr int kVec = D / 4, kPer = R * kVec / kThreads;
+  float4 acc[kPer];
+  float z[kPer];
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+    z[x] = 0.f;
+  }
+  if (threadIdx.x < R) s_ref[threadIdx.x] = -INFINITY;
+  __syncthreads();
+  for (int64_t b0 = c0; count && b0 <= c1; b0 += kMost) {
+    const int np = (int)min((int64_t)kMost, c1 - b0 + 1);
+    // only the first piece can be a CTA's last one (it starts at the item's start)
+    auto slot = [&](int i) { return 2 * (b0 + i) + ((b0 + i) * run <= s0 ? 1 : 0); };
+    for (int u = threadIdx.x; u < np * R; u += kThreads) s_w[u / R][u % R] = a.part_lse[slot(u / R) * R + u % R];
+    __syncthreads();
+    if (threadIdx.x < R) {
+      float top = s_ref[threadIdx.x];
+      for (int i = 0; i < np; ++i) top = fmaxf(top, s_w[i][threadIdx.x]);
+      s_old[threadIdx.x] = top == -INFINITY ? 0.f : ex2(s_ref[threadIdx.x] - top);
+      s_ref[threadIdx.x] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int u = x * kThreads + threadIdx.x, r = u / kVec, d4 = u % kVec;
+      const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
+      z[x] *= old;
+      acc[x].x *= old;
+      acc[x].y *= old;
+      acc[x].z *= old;
+      acc[x].w *= old;
+#pragma unroll 4
+      for (int i = 0; i < np; ++i) {
+        const float f = ex2(s_w[i][r] - ref);
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(i) * R + r) * D)[d4];
+        z[x] += f;
+        acc[x].x += v.x * f;
+        acc[x].y += v.y * f;
+        acc[x].z += v.z * f;
+        acc[x].w += v.w * f;
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int x = 0; x < kPer; ++x) {
+    const int u = x * kThreads + threadIdx.x, r = u / kVec, d4 = u % kVec;
     const int row = rt * R + r;
     if (row >= a.rows) break;
-    float top = -INFINITY;
-    // only the first piece can be a CTA's last one (it starts at the item's start)
-    auto slot = [&](int64_t c) { return 2 * c + (c * run <= s0 ? 1 : 0); };
-    if (count)
-      for (int64_t c = c0; c <= c1; ++c) top = fmaxf(top, a.part_lse[slot(c) * R + r]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float z = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (count)
-      for (int64_t c = c0; c <= c1; ++c) {
-        const float f = ex2(a.part_lse[slot(c) * R + r] - ref);
-        const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(c) * R + r) * D)[d4];
-        z += f;
-        acc.x += v.x * f;
-        acc.y += v.y * f;
-        acc.z += v.z * f;
-        acc.w += v.w * f;
-      }
-    const float inv = z == 0.f ? 0.f : 1.f / z;
+    const float inv = z[x] == 0.f ? 0.f : 1.f / z[x];
     const int tok = row / a.g, head = kvh * a.g + row % a.g;
     const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
-    acc.x *= inv;
-    acc.y *= inv;
-    acc.z *= inv;
-    acc.w *= inv;
+    const float4 o = make_float4(acc[x].x * inv, acc[x].y * inv, acc[x].z * inv, acc[x].w * inv);
     if (a.out_fp32)
-      reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = acc;
+      reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = o;
     else
       reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
-          make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+          make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
     if (d4 == 0)
-      a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (ref + log2f(z)) * kLn2;
+      a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z[x] == 0.f ? -INFINITY : (s_ref[r] + log2f(z[x])) * kLn2;
   }
 }
 

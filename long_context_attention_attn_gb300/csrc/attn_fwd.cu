@@ -35,6 +35,8 @@
 // reference m.
 #include <cuda_bf16.h>
 
+#include <climits>
+
 #include "internal.h"
 #include "merge_math.cuh"
 #include "ptx.cuh"
@@ -446,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         const int kind = s_ids[en * kIdEntry + 2 * BN];
         if (kind == kPartial) {
+          const int reach = a.window < 0 ? INT_MAX : a.window;
           const int4* ids4 = reinterpret_cast<const int4*>(s_ids + en * kIdEntry);
           const int4* pos4 = reinterpret_cast<const int4*>(s_ids + en * kIdEntry + BN);
 #pragma unroll
@@ -456,9 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pka[4] = {pk4.x, pk4.y, pk4.z, pk4.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              bool vis = (ika[u] == iq) && (iq != 0) && (pka[u] <= pq);
-              if (a.window >= 0) vis = vis && (pq - pka[u] <= a.window || pka[u] < a.sink);
-              if (!vis) sr[4 * c + u] = __float_as_uint(-INFINITY);
+              // (no branch per pair: the rows of a warp may differ)
+              const bool vis = (ika[u] == iq) & (iq != 0) & (pka[u] <= pq) &
+                               ((pq - pka[u] <= reach) | (pka[u] < a.sink));
+              sr[4 * c + u] = vis ? sr[4 * c + u] : __float_as_uint(-INFINITY);
             }
           }
         }
