@@ -166,6 +166,19 @@ def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
+def _on_device(index: int, call, *args):
+    """call(*args, stream) on device ``index`` and its current stream (as a raw
+    handle: torch's Stream object would cost more than the launch it is for)."""
+    here = torch._C._cuda_getDevice()
+    if here == index:
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    torch.cuda.set_device(index)
+    try:
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    finally:
+        torch.cuda.set_device(here)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
@@ -427,24 +440,6 @@ def attn_merge_partial(out_acc, lse_acc, out_blk, lse_blk, out_final=None):
     return (out_final if out_final is not None else out_acc), lse_acc
 
 
-class _Device:
-    """Makes a device current for a call (nothing where it is already)."""
-
-    __slots__ = ("index", "before")
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
-
-
 def _index(t, shape, index: int, what: str) -> int:
     """Address of a contiguous int32 tensor of this shape on CUDA device ``index``."""
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
@@ -528,8 +523,7 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
         None if lens is None else _index(lens, (n,), index, "lens"),
         None if tok_start is None else _index(tok_start, (n,), index, "tok_start"),
         s, most if max_new is None else min(int(max_new), most))
-    with _Device(index):
-        _check(lib().attn_kv_append(ctypes.byref(p), _stream(index)), "attn_kv_append")
+    _check(_on_device(index, lib().attn_kv_append, ctypes.byref(p)), "attn_kv_append")
 
 
 def kv_cache_copy_pages(k_cache, v_cache, k_scale, v_scale, src, dst):
@@ -544,9 +538,8 @@ def kv_cache_copy_pages(k_cache, v_cache, k_scale, v_scale, src, dst):
     a, b = _index(src, src.shape, index, "src"), _index(dst, src.shape, index, "dst")
     if src.shape[0] == 0:
         return
-    with _Device(index):
-        _check(lib().attn_kv_copy_pages(ctypes.byref(c), a, b, src.shape[0], _stream(index)),
-               "attn_kv_copy_pages")
+    _check(_on_device(index, lib().attn_kv_copy_pages, ctypes.byref(c), a, b, src.shape[0]),
+           "attn_kv_copy_pages")
 
 
 def _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
@@ -583,8 +576,8 @@ def workspace_bytes_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, se
     """Workspace bytes attn_decode needs for these shapes on q's device (0 if it rejects them)."""
     p, index, _, _ = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, -1, 0,
                                     None, None, None, False)
-    with _Device(index):
-        return int(lib().attn_decode_workspace_bytes(ctypes.byref(p)))
+    with torch.cuda.device(index):
+        return lib().attn_decode_workspace_bytes(ctypes.byref(p))
 
 
 def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
@@ -605,14 +598,15 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
     allocates its own)."""
     p, index, out, lse = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens,
                                         window_left, sink_tokens, scale, out, lse, out_fp32)
-    with _Device(index):
-        if workspace is None:
-            workspace = _workspace(lib().attn_decode_workspace_bytes(ctypes.byref(p)), q.device)
-        elif workspace.get_device() != index or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the call's device")
-        p.workspace = workspace.data_ptr()
-        p.workspace_bytes = workspace.nbytes
-        _check(lib().attn_decode(ctypes.byref(p), _stream(index)), "attn_decode")
+    ref = ctypes.byref(p)
+    if workspace is None:
+        need = _on_device(index, lambda r, _: lib().attn_decode_workspace_bytes(r), ref)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's device")
+    p.workspace = workspace.data_ptr()
+    p.workspace_bytes = workspace.nbytes
+    _check(_on_device(index, lib().attn_decode, ref), "attn_decode")
     return out, lse
 
 

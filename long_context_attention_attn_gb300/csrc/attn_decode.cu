@@ -6,7 +6,7 @@
 // group's query heads and the query tokens share each key read as the rows of
 // one small matrix product.
 //
-// Work is cut by keys, not by sequence: the 32-key blocks of all (sequence, kv
+// Work is cut by keys, not by sequence: the blocks of 32 (16) keys of all (sequence, kv
 // head, row tile) items form one list, and every CTA of a grid that fills the
 // GPU once takes an equal run of it, so ragged batches and single long
 // sequences load every SM alike.  A run that ends inside an item leaves a
@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlock = kDecodeBlock;  // keys per block
 constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum is raised only when a value exceeds it by more than this
 // (in powers of two), so P <= 256.
@@ -61,6 +60,28 @@ struct DecodeArgs {
   float scale_log2;
 };
 
+// How a kernel is cut.  A block of K and V is 8 KB (4 KB at d = 64): 32 keys, 16
+// at d = 256, whose accumulators leave no registers for two groups of 16.  Two
+// or three ring slots a warp keep 64 to 190 KB of copies in flight on an SM;
+// what counts more are warps to issue from, so the q fragments move to shared
+// memory where that makes room for another CTA.  On GB300 (64 sequences of 200
+// to 16384 tokens, Hkv 8, d 128): two CTAs per SM and three slots 179 us,
+// three CTAs and two slots 173 us (1.09 GB).
+template <int D, int NT>
+struct Tune {
+  static constexpr int kBlock = D == 256 ? 16 : 32;
+  static constexpr int kStages = (D == 128 && NT <= 2) || (D == 256 && NT == 1) ? 2 : 3;
+  static constexpr int kCtas = D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : D * NT <= 256 ? 3 : 2;
+  static constexpr bool kQRegs = D * NT <= 128 || D == 64;
+  // What the start and the end of an item (q, the first copies' latency, the
+  // fold of the warps) cost, in blocks: the runs are cut by blocks plus this.
+  // Without it the CTAs with many short sequences end last: 243 us for the
+  // batch above, 197 us with 16.
+  static constexpr int kItemCost = D * NT >= 512 ? 32 : 16;
+};
+// Shortest run: a shorter one would only add partials to fold.
+constexpr int kMinRun = 16;
+
 // The blocks of keys that some query of a sequence of length `len` may see:
 // first those of the kept tokens, then those from the window's start on.
 struct Span {
@@ -70,10 +91,13 @@ struct Span {
   int nb_sink;   // blocks taken before the window's first
   int first;     // the window's first block
   int count;     // blocks
+  int weight;    // what the item counts in the list: blocks and the cost of its start and end
   __device__ __forceinline__ int block(int t) const { return t < nb_sink ? t : first + t - nb_sink; }
 };
 
+template <typename T>
 __device__ __forceinline__ Span span_of(const DecodeArgs& a, int len) {
+  constexpr int kBlock = T::kBlock;
   Span s;
   const int cap = a.max_pages << a.page_shift;
   s.hi = max(min(len, cap), 0);
@@ -84,6 +108,7 @@ __device__ __forceinline__ Span span_of(const DecodeArgs& a, int len) {
   s.first = min(s.lo / kBlock, last);
   s.nb_sink = min((s.sink_hi + kBlock - 1) / kBlock, s.first);
   s.count = s.nb_sink + last - s.first;
+  s.weight = s.count ? s.count + T::kItemCost : 0;
   return s;
 }
 
@@ -95,32 +120,33 @@ struct Placement {
   int per;
 };
 
+template <typename T>
 __device__ __forceinline__ Placement place(const DecodeArgs& a, int64_t* before) {
   __shared__ int64_t warp_sum[kWarps];
   const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
   const int per = (a.n + kThreads - 1) / kThreads;
+  const bool mine = t < kThreads;  // (the combine kernel has more)
   int64_t sum = 0;
-  for (int i = t * per; i < min((t + 1) * per, a.n); ++i) sum += span_of(a, a.lens[i]).count;
+  for (int i = mine ? t * per : a.n; i < min((t + 1) * per, a.n); ++i) sum += span_of<T>(a, a.lens[i]).weight;
   int64_t incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t u = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += u;
   }
-  if (lane == 31) warp_sum[wid] = incl;
+  if (mine && lane == 31) warp_sum[wid] = incl;
   __syncthreads();
   int64_t base = 0;
-  for (int w = 0; w < wid; ++w) base += warp_sum[w];
-  before[t] = base + incl - sum;
+  for (int w = 0; w < min(wid, kWarps); ++w) base += warp_sum[w];
+  if (mine) before[t] = base + incl - sum;
   if (t == kThreads - 1) before[kThreads] = base + incl;
   __syncthreads();
   return Placement{before, per};
 }
 
-// Blocks per CTA: an equal share of the list, and no less than a block for
-// each warp (a shorter run would only add partials to fold).
+// Weight per CTA: an equal share of the list, and no less than kMinRun.
 __device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total) {
-  return max((total + a.grid - 1) / a.grid, (int64_t)kWarps);
+  return max((total + a.grid - 1) / a.grid, (int64_t)kMinRun);
 }
 
 // ---------------------------------------------------------------- primitives
@@ -210,13 +236,13 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
 // takes zeros for NaN codes; kOnlyNan turns o to NaN where a NaN code meets a
 // key whose value in pb (0 or 1) says that the row sees it.
 enum { kPlain, kNoNan, kOnlyNan };
-template <int D, int NT, int kMode>
+template <int D, int NT, int MT, int kMode>
 __device__ __forceinline__ void add_pv(float (&o)[D / 16][NT][4], const uint8_t* vt,
-                                       const uint32_t (&pb)[2][NT][2], int n8, int t4) {
+                                       const uint32_t (&pb)[MT][NT][2], int n8, int t4) {
   constexpr int kParts = D == 256 ? 2 : 1;  // 16-byte pieces of a key per thread
   constexpr int kWords = D == 64 ? 2 : 4;   // words per piece
 #pragma unroll
-  for (int mt = 0; mt < 2; ++mt) {
+  for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
     for (int hh = 0; hh < kParts; ++hh) {
       uint32_t w[4][kWords];  // keys t4, t4 + 4, t4 + 8, t4 + 12 of the group
@@ -269,7 +295,7 @@ __device__ __forceinline__ void add_pv(float (&o)[D / 16][NT][4], const uint8_t*
 }
 
 // Whether a block's V tile holds the e4m3 NaN (0x7f or 0xff) anywhere.
-template <int D>
+template <int D, int kBlock>
 __device__ __forceinline__ bool holds_nan(const uint8_t* vt, int lane) {
   bool nan = false;
 #pragma unroll 2
@@ -294,11 +320,12 @@ __device__ __forceinline__ uint32_t copy_offset(uint32_t lane_off, int u) {
 template <int D, int NT>
 struct Cfg {
   static constexpr int R = NT * 8;                  // rows per tile
+  static constexpr int kBlock = Tune<D, NT>::kBlock;
   static constexpr int kTile = kBlock * D;          // bytes of a K or V tile
   static constexpr int kStage = 2 * kTile;
-  static constexpr int kStages = D == 64 ? 4 : 3;
+  static constexpr int kStages = Tune<D, NT>::kStages;
   static constexpr int kKSteps = D / 16;
-  static constexpr bool kQRegs = D * NT <= 256;     // q fragments in registers
+  static constexpr bool kQRegs = Tune<D, NT>::kQRegs;  // q fragments in registers
   static constexpr int q_off = kWarps * kStages * kStage;          // uint4 [NT * kKSteps / 2][32]
   static constexpr int meta_off = q_off + NT * kKSteps / 2 * 512;  // per warp and stage: 8 words
   static constexpr int row_off = meta_off + kWarps * kStages * 32; // row factors, positions
@@ -316,15 +343,18 @@ struct Piece {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kernel(const DecodeArgs a) {
   using C = Cfg<D, NT>;
+  using T = Tune<D, NT>;
+  constexpr int kBlock = T::kBlock, kItemCost = T::kItemCost;
+  constexpr int MT = kBlock / 16;  // groups of 16 keys
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t before[kThreads + 1];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int n8 = lane >> 2, t4 = lane & 3;
 
-  const Placement pl = place(a, before);
+  const Placement pl = place<T>(a, before);
   const int items = a.h_kv * a.row_tiles;  // per sequence
   const int64_t total = before[kThreads] * items;
   const int64_t run = run_length(a, total);
@@ -344,7 +374,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
     seq = t * pl.per;
     seq_at = before[t] * items;
     for (;; ++seq) {
-      const int64_t c = (int64_t)span_of(a, a.lens[seq]).count * items;
+      const int64_t c = (int64_t)span_of<T>(a, a.lens[seq]).weight * items;
       if (at < seq_at + c) break;
       seq_at += c;
     }
@@ -362,22 +392,44 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
     Piece p;
     p.seq = seq;
     p.len = a.lens[seq];
-    p.span = span_of(a, p.len);
+    p.span = span_of<T>(a, p.len);
     if (p.span.count == 0) {
       ++seq;
       continue;
     }
+    // the piece [w0, w1) of the item's weight: its first kItemCost hold no block
     const int64_t in_seq = at - seq_at;
-    const int item = (int)(in_seq / p.span.count);
+    const int weight = p.span.weight;
+    const int item = (int)(in_seq / weight);
     p.kvh = item / a.row_tiles;
     p.rt = item % a.row_tiles;
-    p.t0 = (int)(in_seq - (int64_t)item * p.span.count);
-    p.t1 = (int)min((int64_t)p.span.count, p.t0 + (end - at));
-    at += p.t1 - p.t0;
-    const bool item_done = p.t1 == p.span.count;
+    const int w0 = (int)(in_seq - (int64_t)item * weight);
+    const int w1 = (int)min((int64_t)weight, w0 + (end - at));
+    p.t0 = max(w0 - kItemCost, 0);
+    p.t1 = max(w1 - kItemCost, 0);
+    at += w1 - w0;
+    const bool item_done = w1 == weight;
     if (item_done && item == items - 1) {
-      seq_at += (int64_t)p.span.count * items;
+      seq_at += (int64_t)weight * items;
       ++seq;
+    }
+    if (p.t1 == p.t0) continue;
+
+    // ---- the rows of q: their loads are in flight while the ring fills
+    constexpr int kE = D / 32;               // values of a row per lane, neighbours
+    constexpr int kRows = C::R / kWarps;     // rows per warp
+    uint32_t qw[kRows][kE / 2];
+    int qtok[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int row = p.rt * C::R + warp + i * kWarps;
+      const bool in = row < a.rows;
+      const int tok = in ? row / a.g : 0, head = p.kvh * a.g + (in ? row - tok * a.g : 0);
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(
+          a.q + (((int64_t)p.seq * a.s_q + tok) * a.h_q + head) * D + lane * kE);
+      qtok[i] = in ? tok : -1;
+#pragma unroll
+      for (int e = 0; e < kE / 2; ++e) qw[i][e] = in ? src[e] : 0u;
     }
 
     // ---- the asynchronous copies of one block into a ring slot
@@ -387,54 +439,54 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
       if (t < p.t1) {
         const int key0 = p.span.block(t) * kBlock;
         // the block's two groups of 16 keys lie on one page each
-        int pid[2];
-        bool ok[2];
+        int pid[MT];
+        bool ok[MT];
         pid[0] = table[key0 >> a.page_shift];
-        pid[1] = pid[0];
-        if (a.page_shift == 4) pid[1] = key0 + 16 < p.span.hi ? table[(key0 >> 4) + 1] : -1;
+        if constexpr (MT == 2) pid[1] = pid[0];
+        if (MT == 2 && a.page_shift == 4) pid[MT - 1] = key0 + 16 < p.span.hi ? table[(key0 >> 4) + 1] : -1;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < MT; ++u) {
           ok[u] = pid[u] >= 0 && pid[u] < a.num_pages;
           if (!ok[u]) pid[u] = 0;
         }
         // a group's rows are neighbours in memory, 32 lanes take 512 bytes at a time
         const uint32_t dst = ring_u + slot * C::kStage;
         constexpr int kPer = kBlock * D / 512;
-        const uint8_t *kp[2], *vp[2];
+        const uint8_t *kp[MT], *vp[MT];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < MT; ++u) {
           const int64_t src = (int64_t)pid[u] * a.page_stride +
                               (((int64_t)p.kvh << a.page_shift) + ((key0 + 16 * u) & page_mask)) * D + lane * 16;
           kp[u] = a.k + src;
           vp[u] = a.v + src;
         }
-        const bool whole = ok[0] && ok[1] && key0 + kBlock <= p.span.hi &&
+        const bool whole = ok[0] && ok[MT - 1] && key0 + kBlock <= p.span.hi &&
                            (key0 >= p.span.lo || key0 + kBlock <= p.span.sink_hi);
         if (whole) {
 #pragma unroll
           for (int u = 0; u < kPer; ++u) {
             const uint32_t off = copy_offset<D>(lane_off, u);
-            cp_async16(dst + off, kp[2 * u / kPer] + (u % (kPer / 2)) * 512);
-            cp_async16(dst + C::kTile + off, vp[2 * u / kPer] + (u % (kPer / 2)) * 512);
+            cp_async16(dst + off, kp[MT * u / kPer] + (u % (kPer / MT)) * 512);
+            cp_async16(dst + C::kTile + off, vp[MT * u / kPer] + (u % (kPer / MT)) * 512);
           }
         } else {
           // zeros for what no query sees
 #pragma unroll
           for (int u = 0; u < kPer; ++u) {
             const int key = key0 + u * (512 / D) + lane / (D / 16);
-            const bool take = ok[2 * u / kPer] && key < p.span.hi && (key >= p.span.lo || key < p.span.sink_hi);
+            const bool take = ok[MT * u / kPer] && key < p.span.hi && (key >= p.span.lo || key < p.span.sink_hi);
             const uint32_t off = copy_offset<D>(lane_off, u);
-            cp_async16_or_zero(dst + off, kp[2 * u / kPer] + (u % (kPer / 2)) * 512, take);
-            cp_async16_or_zero(dst + C::kTile + off, vp[2 * u / kPer] + (u % (kPer / 2)) * 512, take);
+            cp_async16_or_zero(dst + off, kp[MT * u / kPer] + (u % (kPer / MT)) * 512, take);
+            cp_async16_or_zero(dst + C::kTile + off, vp[MT * u / kPer] + (u % (kPer / MT)) * 512, take);
           }
         }
         // K and V scales of the two groups, and whether they have a page
-        if (lane < 4) {
-          const int u = lane & 1;
-          const float* sc = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)pid[u] * a.h_kv + p.kvh;
-          cp_async4(meta_u + slot * 32 + lane * 4, sc, ok[u]);
+        if (lane < 4 && (lane & 1) < MT) {
+          const bool second = MT == 2 && (lane & 1);
+          const float* sc = (lane < 2 ? a.k_scale : a.v_scale) + (int64_t)pid[second ? MT - 1 : 0] * a.h_kv + p.kvh;
+          cp_async4(meta_u + slot * 32 + lane * 4, sc, second ? ok[MT - 1] : ok[0]);
         }
-        if (lane == 0) meta[slot * 8 + 4] = (ok[0] ? 1u : 0u) | (ok[1] ? 2u : 0u);
+        if (lane == 0) meta[slot * 8 + 4] = (ok[0] ? 1u : 0u) | (ok[MT - 1] ? 2u : 0u);
       }
       cp_async_commit();
     };
@@ -446,20 +498,15 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
     }
 
     // ---- q of the item's rows as f16 fragments, row factors and positions
-    for (int r = warp; r < C::R; r += kWarps) {
-      const int row = p.rt * C::R + r;
-      const bool in = row < a.rows;
-      const int tok = in ? row / a.g : 0, head = p.kvh * a.g + (in ? row % a.g : 0);
-      const __nv_bfloat16* src = a.q + (((int64_t)p.seq * a.s_q + tok) * a.h_q + head) * D;
-      // lane holds D / 32 neighbouring values
-      constexpr int kE = D / 32;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = warp + i * kWarps;
       float x[kE];
       float amax = 0.f;
 #pragma unroll
       for (int e = 0; e < kE; e += 2) {
-        const uint32_t w = in ? reinterpret_cast<const uint32_t*>(src)[(lane * kE + e) / 2] : 0u;
-        x[e] = __uint_as_float(w << 16);
-        x[e + 1] = __uint_as_float(w & 0xffff0000u);
+        x[e] = __uint_as_float(qw[i][e / 2] << 16);
+        x[e + 1] = __uint_as_float(qw[i][e / 2] & 0xffff0000u);
       }
 #pragma unroll
       for (int e = 0; e < kE; ++e)
@@ -468,18 +515,20 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
       // the row's largest value goes to [2^14, 2^15)
       const int ex = bits ? max((int)(bits >> 23) - 127, -100) - 14 : 0;
       const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-      __half* sq = reinterpret_cast<__half*>(s_q);
+      // value e of the lane's is element (d & 3) of k step (d >> 6) * 4 + ((d & 15) >> 2)
+      // of lane (r & 7) * 4 + ((d >> 4) & 3), in pairs
+      uint32_t* sq = reinterpret_cast<uint32_t*>(s_q);
 #pragma unroll
-      for (int e = 0; e < kE; ++e) {
+      for (int e = 0; e < kE; e += 2) {
         const int d = lane * kE + e;
-        const int ks = (d >> 6) * 4 + ((d & 15) >> 2);  // k step
-        const int ln = (r & 7) * 4 + ((d >> 4) & 3);    // lane that owns it
-        const int idx = ((((r >> 3) * C::kKSteps + ks) >> 1) * 32 + ln) * 8 + (ks & 1) * 4 + (d & 3);
-        sq[idx] = __float2half_rn(x[e] * inv);
+        const int ks = (d >> 6) * 4 + ((d & 15) >> 2);
+        const int ln = (r & 7) * 4 + ((d >> 4) & 3);
+        sq[((((r >> 3) * C::kKSteps + ks) >> 1) * 32 + ln) * 4 + (ks & 1) * 2 + ((d & 3) >> 1)] =
+            pack_f16(x[e] * inv, x[e + 1] * inv);
       }
       if (lane == 0) {
-        s_fac[r] = in ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) : 0.f;
-        s_pos[r] = in ? p.len - a.s_q + tok : -1;
+        s_fac[r] = qtok[i] >= 0 ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) : 0.f;
+        s_pos[r] = qtok[i] >= 0 ? p.len - a.s_q + qtok[i] : -1;
       }
     }
     __syncthreads();
@@ -522,18 +571,18 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
       const int key0 = p.span.block(t) * kBlock;
 
       // S^T = K q^T
-      float s[2][NT][4];
+      float s[MT][NT][4];
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 4; ++c) s[mt][nt][c] = 0.f;
 #pragma unroll
       for (int cc = 0; cc < D / 64; ++cc) {
-        uint32_t w[2][2][4];  // [mt][key group of 8][4 words of 4 codes]
+        uint32_t w[MT][2][4];  // [mt][key group of 8][4 words of 4 codes]
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const uint4 x = *reinterpret_cast<const uint4*>(
@@ -545,9 +594,9 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
           }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t af[2][4];
+          uint32_t af[MT][4];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) {
+          for (int mt = 0; mt < MT; ++mt) {
             af[mt][0] = widen_lo(w[mt][0][j]);
             af[mt][1] = widen_lo(w[mt][1][j]);
             af[mt][2] = widen_hi(w[mt][0][j]);
@@ -564,22 +613,26 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
               f = s_q[qi * 32 + lane];
             const uint32_t b0 = (ks & 1) ? f.z : f.x, b1 = (ks & 1) ? f.w : f.y;
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) mma16816(s[mt][nt], af[mt], b0, b1);
+            for (int mt = 0; mt < MT; ++mt) mma16816(s[mt][nt], af[mt], b0, b1);
           }
         }
       }
 
       // scores in base 2; s[mt][nt][c]: key 16 mt + 8 (c >> 1) + key_of_row(n8),
       // row 8 nt + 2 t4 + (c & 1)
-      const float ks_[2] = {__uint_as_float(mw[0]), __uint_as_float(mw[1])};
-      const float lvs[2] = {lg2(__uint_as_float(mw[2])), lg2(__uint_as_float(mw[3]))};
+      float ks_[MT], lvs[MT];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        ks_[mt] = __uint_as_float(mw[mt]);
+        lvs[mt] = lg2(__uint_as_float(mw[2 + mt]));
+      }
       const bool all_seen = pages_ok == 3u && key0 + kBlock - 1 <= p_first &&
                             (a.window < 0 || p_last - key0 <= a.window || key0 + kBlock - 1 < a.sink);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         const float2 fac = *reinterpret_cast<const float2*>(s_fac + 8 * nt + 2 * t4);
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) s[mt][nt][c] *= ((c & 1) ? fac.y : fac.x) * ks_[mt];
         }
@@ -589,7 +642,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
         for (int nt = 0; nt < NT; ++nt) {
           const int2 pq = *reinterpret_cast<const int2*>(s_pos + 8 * nt + 2 * t4);
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               const int key = key0 + 16 * mt + 8 * (c >> 1) + key_of_row(n8);
@@ -608,9 +661,9 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const float x0 = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-          const float x1 = fmaxf(s[1][nt][c], s[1][nt][c + 2]);
+          const float x1 = fmaxf(s[MT - 1][nt][c], s[MT - 1][nt][c + 2]);
           raise |= fmaxf(x0, x1) > m[nt][c] + kRescale;
-          raise |= fmaxf(x0 + lvs[0], x1 + lvs[1]) > mo[nt][c] + kRescale;
+          raise |= fmaxf(x0 + lvs[0], x1 + lvs[MT - 1]) > mo[nt][c] + kRescale;
         }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
@@ -618,8 +671,8 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             const float x0 = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-            const float x1 = fmaxf(s[1][nt][c], s[1][nt][c + 2]);
-            float a0 = fmaxf(x0, x1), a1 = fmaxf(x0 + lvs[0], x1 + lvs[1]);
+            const float x1 = fmaxf(s[MT - 1][nt][c], s[MT - 1][nt][c + 2]);
+            float a0 = fmaxf(x0, x1), a1 = fmaxf(x0 + lvs[0], x1 + lvs[MT - 1]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
               a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, off));
@@ -642,19 +695,19 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
       }
 
       // P^T fragments: p = 2^(x - m) for the sum, p * 2^(lvs + m - mo) for O
-      uint32_t pb[2][NT][2];
+      uint32_t pb[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float sub[2], up[2][2];
+        float sub[2], up[MT][2];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           sub[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
           const float so = mo[nt][c] == -INFINITY ? 0.f : mo[nt][c];
 #pragma unroll
-          for (int mt = 0; mt < 2; ++mt) up[mt][c] = ex2(fminf(lvs[mt] + sub[c] - so, 120.f));
+          for (int mt = 0; mt < MT; ++mt) up[mt][c] = ex2(fminf(lvs[mt] + sub[c] - so, 120.f));
         }
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt) {
+        for (int mt = 0; mt < MT; ++mt) {
           float e[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -668,12 +721,12 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
       }
 
       // O^T += V^T P^T
-      if (a.s_q > 1 && !all_seen && holds_nan<D>(vt, lane)) {
+      if (a.s_q > 1 && !all_seen && holds_nan<D, kBlock>(vt, lane)) {
         // NaN among keys that not every query sees (0 * NaN is NaN): the product
         // without them, then NaN where a query sees one
-        uint32_t see[2][NT][2];
+        uint32_t see[MT][NT][2];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const int2 pq = *reinterpret_cast<const int2*>(s_pos + 8 * nt + 2 * t4);
@@ -685,10 +738,10 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
               see[mt][nt][hf] = transpose8x8(pack_f16(s0 ? 1.f : 0.f, s1 ? 1.f : 0.f));
             }
           }
-        add_pv<D, NT, kNoNan>(o, vt, pb, n8, t4);
-        add_pv<D, NT, kOnlyNan>(o, vt, see, n8, t4);
+        add_pv<D, NT, MT, kNoNan>(o, vt, pb, n8, t4);
+        add_pv<D, NT, MT, kOnlyNan>(o, vt, see, n8, t4);
       } else {
-        add_pv<D, NT, kPlain>(o, vt, pb, n8, t4);
+        add_pv<D, NT, MT, kPlain>(o, vt, pb, n8, t4);
       }
       slot = slot == C::kStages - 1 ? 0 : slot + 1;
     }
@@ -783,19 +836,22 @@ __global__ void __launch_bounds__(kThreads) attn_decode_kernel(const DecodeArgs 
 
 // One CTA per item: folds the partials of an item that several CTAs shared,
 // and writes the empty result of a sequence without keys.
-template <int D, int R>
-__global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const DecodeArgs a) {
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads * 2) attn_decode_combine_kernel(const DecodeArgs a) {
+  using T = Tune<D, NT>;
+  constexpr int R = NT * 8;
   __shared__ int64_t before[kThreads + 1];
-  const Placement pl = place(a, before);
+  const Placement pl = place<T>(a, before);
   const int items = a.h_kv * a.row_tiles;
   const int seq = blockIdx.x / items, item = blockIdx.x % items;
   const int64_t total = before[kThreads] * items;
   const int64_t run = run_length(a, total);
   const int t = seq / pl.per;
   int64_t seq_at = before[t];
-  for (int i = t * pl.per; i < seq; ++i) seq_at += span_of(a, a.lens[i]).count;
-  const int count = span_of(a, a.lens[seq]).count;
-  const int64_t s0 = seq_at * items + (int64_t)item * count;  // the item's blocks: [s0, s0 + count)
+  for (int i = t * pl.per; i < seq; ++i) seq_at += span_of<T>(a, a.lens[i]).weight;
+  const Span sp = span_of<T>(a, a.lens[seq]);
+  const int count = sp.count;
+  const int64_t s0 = seq_at * items + (int64_t)item * sp.weight + T::kItemCost;  // the item's blocks: [s0, s0 + count)
   const int64_t c0 = count ? s0 / run : 0, c1 = count ? (s0 + count - 1) / run : 0;
   // every CTA waits, so that this grid never ends before the one it depends on
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -806,7 +862,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const Dec
   constexpr int kMost = 32;
   __shared__ float s_w[kMost][R];
   __shared__ float s_ref[R], s_old[R];
-  constexpr int kVec = D / 4, kPer = R * kVec / kThreads;
+  constexpr int kVec = D / 4, kAll = 2 * kThreads, kPer = (R * kVec + kAll - 1) / kAll;
   float4 acc[kPer];
   float z[kPer];
 #pragma unroll
@@ -820,7 +876,7 @@ __global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const Dec
     const int np = (int)min((int64_t)kMost, c1 - b0 + 1);
     // only the first piece can be a CTA's last one (it starts at the item's start)
     auto slot = [&](int i) { return 2 * (b0 + i) + ((b0 + i) * run <= s0 ? 1 : 0); };
-    for (int u = threadIdx.x; u < np * R; u += kThreads) s_w[u / R][u % R] = a.part_lse[slot(u / R) * R + u % R];
+    for (int u = threadIdx.x; u < np * R; u += kAll) s_w[u / R][u % R] = a.part_lse[slot(u / R) * R + u % R];
     __syncthreads();
     if (threadIdx.x < R) {
       float top = s_ref[threadIdx.x];
@@ -831,14 +887,15 @@ __global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const Dec
     __syncthreads();
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-      const int u = x * kThreads + threadIdx.x, r = u / kVec, d4 = u % kVec;
+      const int u = x * kAll + threadIdx.x, r = u / kVec, d4 = u % kVec;
+      if (R * kVec < kAll && r >= R) break;
       const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
       z[x] *= old;
       acc[x].x *= old;
       acc[x].y *= old;
       acc[x].z *= old;
       acc[x].w *= old;
-#pragma unroll 4
+#pragma unroll 8
       for (int i = 0; i < np; ++i) {
         const float f = ex2(s_w[i][r] - ref);
         const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(i) * R + r) * D)[d4];
@@ -853,9 +910,9 @@ __global__ void __launch_bounds__(kThreads) attn_decode_combine_kernel(const Dec
   }
 #pragma unroll
   for (int x = 0; x < kPer; ++x) {
-    const int u = x * kThreads + threadIdx.x, r = u / kVec, d4 = u % kVec;
+    const int u = x * kAll + threadIdx.x, r = u / kVec, d4 = u % kVec;
     const int row = rt * R + r;
-    if (row >= a.rows) break;
+    if (r >= R || row >= a.rows) break;
     const float inv = z[x] == 0.f ? 0.f : 1.f / z[x];
     const int tok = row / a.g, head = kvh * a.g + row % a.g;
     const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
@@ -911,14 +968,14 @@ struct Kernel {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.h_kv * a.row_tiles));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(kThreads * 2);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel<D, C::R>, a);
+    return cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel<D, NT>, a);
   }
 };
 

@@ -207,7 +207,6 @@ cudaError_t launch_kv_copy(const attn_kv_cache& c, const int* src, const int* ds
                            cudaStream_t st);
 
 // ---- attn_decode.cu
-constexpr int kDecodeBlock = 32;  // keys per block of the decode kernel's work list
 cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes);
 cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st);
 
