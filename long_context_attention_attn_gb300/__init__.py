@@ -396,12 +396,13 @@ def attn_bwd(q, k, v, out, lse, dout, q_ids, q_pos, kv_ids=None, kv_pos=None, *,
 
 
 def workspace_bytes_bwd(q, k, q_ids, q_pos, window_left=-1, v=None,
-                        deterministic: bool = False) -> int:
+                        deterministic: bool = False, sink_tokens: int = 0) -> int:
     """Workspace bytes attn_bwd needs for these shapes (0 if it rejects them);
-    pass ``v`` when its head dim differs from k's."""
+    pass ``v`` when its head dim differs from k's, and the call's window and
+    ``sink_tokens`` (kept tokens take scratch of their own)."""
     p = BwdParams()
     p.fwd = _fwd_params(q, k, k if v is None else v, q_ids, q_pos, q_ids, q_pos, window_left,
-                        None, q, q, False)
+                        None, q, q, False, sink_tokens)
     p.deterministic = 1 if deterministic else 0
     return int(lib().attn_bwd_workspace_bytes(ctypes.byref(p)))
 

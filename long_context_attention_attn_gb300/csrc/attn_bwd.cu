@@ -40,8 +40,6 @@
 // element-wise warps' path costs latency per step.
 #include <cuda_bf16.h>
 
-#include <climits>
-
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -107,6 +105,7 @@ struct BwdArgs {
   float scale;
   float scale_log2;
   float c_shift;  // -ln(scale) / scale: added to c so that the exponent gives scale * P
+  KeyParts parts;  // KEEP only
 };
 
 template <int D>
@@ -173,7 +172,9 @@ struct StepIter {
   }
 };
 
-template <int D>
+// KEEP: first tokens stay visible behind the window (its own variant, so that the
+// other masks' code stays as it is); key tiles that hold some come in parts.
+template <int D, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -190,14 +191,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.status && *reinterpret_cast<volatile int*>(a.status) != kStatusOk) return;
 
   // ---- work unit: kv head slowest, then (b, kv tile) in the plan's work order
+  // (KEEP: the parts of all kv heads first)
   const int nunits = a.b * a.nk;
-  const int kvh = blockIdx.x / nunits;
-  const int rank = blockIdx.x % nunits;
-  const int e = a.order[rank];
+  const int nparts = KEEP ? a.parts.max_parts * a.hkv : 0;
+  const bool is_part = KEEP && (int)blockIdx.x < nparts;
+  const int part = is_part ? blockIdx.x / a.hkv : 0;
+  if (is_part && part >= a.parts.header->n_parts) return;
+  const int unit = blockIdx.x - nparts;
+  const int kvh = is_part ? blockIdx.x % a.hkv : unit / nunits;
+  const int e = is_part ? a.parts.parts[part].x : a.order[unit % nunits];
+  if (KEEP && !is_part && a.kweight[e] > a.parts.header->cap) return;  // done by its parts
   const int bi = e / a.nk;
   const int kt = e % a.nk;
-  const int2 rng = a.krange[e];
-  const int nsteps_total = a.kweight[e] * a.g;  // (non-SKIP query tile, head) steps
+  int2 rng = a.krange[e];
+  int ntiles = a.kweight[e];  // non-SKIP query tiles
+  if (is_part) {
+    rng = make_int2(a.parts.parts[part].y, a.parts.parts[part].z);
+    ntiles = 0;
+    for (int i0 = rng.x; i0 <= rng.y; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      ntiles += __syncthreads_count(i <= rng.y && a.cls[((size_t)bi * a.nq + i) * a.nk + kt] != kSkip);
+    }
+  }
+  const int nsteps_total = ntiles * a.g;  // (non-SKIP query tile, head) steps
   StepIter it0;
   it0.hh = 0;
   it0.i_first = rng.x;
@@ -496,8 +512,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
-    // farthest query that sees this key (no branch per pair: a warp's keys may differ)
-    const int reach = (a.window < 0 || pk < a.sink) ? INT_MAX : a.window;
+    // KEEP: the farthest query that sees this key (no branch per pair: a warp's keys differ)
+    const int reach = KEEP && pk < a.sink ? 0x7fffffff : a.window;
     const float sl2 = a.scale_log2;
     uint8_t* ds_smem = smem + L::ds_off + w * L::kChunk + kr * 128;
     constexpr int kHalf = D / 2;         // dQ columns read back by this half
@@ -541,8 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qa[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            const bool vis = (ia[u] == ik) & (ik != 0) & (pk <= qa[u]) & (qa[u] - pk <= reach);
-            p[4 * c + u] = vis ? p[4 * c + u] : 0.f;
+            bool vis = (ia[u] == ik) && (ik != 0) && (pk <= qa[u]);
+            if constexpr (KEEP)
+              vis = vis & (qa[u] - pk <= reach);
+            else if (a.window >= 0)
+              vis = vis && (qa[u] - pk <= a.window);
+            if (!vis) p[4 * c + u] = 0.f;
           }
         }
       }
@@ -642,6 +662,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0u;
         }
+        if constexpr (KEEP) {
+          if (is_part) {
+            float4* dst = reinterpret_cast<float4*>(
+                a.parts.buf + (((int64_t)part * a.hkv + kvh) * BN + kr) * (2 * D) + (w == 0 ? D : 0) + c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[u] = make_float4(__uint_as_float(o[4 * u]) * sc, __uint_as_float(o[4 * u + 1]) * sc,
+                                   __uint_as_float(o[4 * u + 2]) * sc, __uint_as_float(o[4 * u + 3]) * sc);
+            continue;
+          }
+        }
         if (!key_in) continue;
         if (a.accumulate) {
           float4* dst = reinterpret_cast<float4*>(static_cast<float*>(w == 0 ? a.dv : a.dk) +
@@ -679,12 +710,26 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+template <int D, bool KEEP>
+cudaError_t launch_bwd_d(const BwdArgs& a, const BwdLaunch& Lc, cudaStream_t st) {
+  const int64_t units = ((int64_t)a.b * a.nk + (KEEP ? a.parts.max_parts : 0)) * a.hkv;
+  if (units > 0x7fffffffll) return cudaErrorNotSupported;
+  const int smem = BLayout<D>::alloc;
+  static std::atomic<int> smem_set[kMaxDevices];
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_bwd_kernel<D, KEEP>), smem,
+                                    kLaunchRegs, smem_set);
+  if (e != cudaSuccess) return e;
+  attn_bwd_kernel<D, KEEP><<<(unsigned)units, kThreads, smem, st>>>(Lc.tm_q, Lc.tm_k, Lc.tm_v, Lc.tm_do,
+                                                                    Lc.tm_dq, a);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_attn_bwd(const BwdLaunch& Lc, cudaStream_t st) {
   const attn_bwd_params& p = *Lc.p;
   const attn_fwd_params& f = p.fwd;
-  BwdArgs a;
+  BwdArgs a = {};
   a.q_ids = f.q_segment_ids;
   a.q_pos = f.q_segment_pos;
   a.kv_ids = f.kv_segment_ids;
@@ -714,28 +759,11 @@ cudaError_t launch_attn_bwd(const BwdLaunch& Lc, cudaStream_t st) {
   a.scale = f.scale;
   a.scale_log2 = f.scale * kLog2e;
   a.c_shift = -logf(f.scale) / f.scale;
-  const int64_t units = f.b * Lc.nk * f.h_kv;
-  if (units == 0) return cudaSuccess;
-  if (f.d == 128) {
-    const int smem = BLayout<128>::alloc;
-    static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e =
-        ensure_smem_limit(reinterpret_cast<const void*>(attn_bwd_kernel<128>), smem,
-                          kLaunchRegs, smem_set);
-    if (e != cudaSuccess) return e;
-    attn_bwd_kernel<128><<<(unsigned)units, kThreads, smem, st>>>(Lc.tm_q, Lc.tm_k, Lc.tm_v,
-                                                                  Lc.tm_do, Lc.tm_dq, a);
-  } else {
-    const int smem = BLayout<64>::alloc;
-    static std::atomic<int> smem_set[kMaxDevices];
-    cudaError_t e =
-        ensure_smem_limit(reinterpret_cast<const void*>(attn_bwd_kernel<64>), smem,
-                          kLaunchRegs, smem_set);
-    if (e != cudaSuccess) return e;
-    attn_bwd_kernel<64><<<(unsigned)units, kThreads, smem, st>>>(Lc.tm_q, Lc.tm_k, Lc.tm_v,
-                                                                 Lc.tm_do, Lc.tm_dq, a);
+  if (keeps_tokens(f)) {
+    a.parts = Lc.parts;
+    return f.d == 128 ? launch_bwd_d<128, true>(a, Lc, st) : launch_bwd_d<64, true>(a, Lc, st);
   }
-  return cudaGetLastError();
+  return f.d == 128 ? launch_bwd_d<128, false>(a, Lc, st) : launch_bwd_d<64, false>(a, Lc, st);
 }
 
 }  // namespace gb300

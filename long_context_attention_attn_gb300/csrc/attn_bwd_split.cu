@@ -35,8 +35,6 @@
 // latency every step.
 #include <cuda_bf16.h>
 
-#include <climits>
-
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -91,14 +89,20 @@ struct SplitArgs {
   float scale;
   float scale_log2;
   float c_shift;     // -ln(scale) / scale
+  KeyParts parts;    // dK / dV kernel with KEEP only
 };
 
-// reach: how far behind a query the key at pk may lie (key_reach below)
-__device__ __forceinline__ bool visible(int iq, int pq, int ik, int pk, int reach) {
-  return (iq == ik) & (iq != 0) & (pk <= pq) & (pq - pk <= reach);
-}
-__device__ __forceinline__ int key_reach(int pk, int window, int sink) {
-  return (window < 0 || pk < sink) ? INT_MAX : window;
+// KEEP: first tokens stay visible behind the window (its own variant of the
+// kernels, so that the other masks' code stays as it is; no branch per pair,
+// because the keys or rows of a warp differ)
+template <bool KEEP>
+__device__ __forceinline__ bool visible(int iq, int pq, int ik, int pk, int window, int sink) {
+  bool v = (iq == ik) && (iq != 0) && (pk <= pq);
+  if constexpr (KEEP)
+    v = v & ((pq - pk <= window) | (pk < sink));
+  else if (window >= 0)
+    v = v && (pq - pk <= window);
+  return v;
 }
 
 // ============================================================== dK / dV
@@ -191,7 +195,7 @@ struct AStepIter {
   __device__ int row0() const { return i * 128 + sub * BM; }
 };
 
-template <int DK, int DV, int BM, int NSPLIT, int NQ, int NO, bool KT, bool VT>
+template <int DK, int DV, int BM, int NSPLIT, int NQ, int NO, bool KT, bool VT, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -209,15 +213,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (a.status && *reinterpret_cast<volatile int*>(a.status) != kStatusOk) return;
 
   // ---- work unit: kv head slowest, then (b, kv tile) in work order, then slice
+  // (KEEP: the parts of all kv heads first)
   const int nunits = a.b * a.nk;
-  const int kvh = blockIdx.x / (nunits * NSPLIT);
-  const int rem = blockIdx.x % (nunits * NSPLIT);
-  const int ks = rem % NSPLIT;
-  const int e = a.order[rem / NSPLIT];
+  const int nparts = KEEP ? a.parts.max_parts * a.hkv * NSPLIT : 0;
+  const bool is_part = KEEP && (int)blockIdx.x < nparts;
+  const int part = is_part ? blockIdx.x / (a.hkv * NSPLIT) : 0;
+  if (is_part && part >= a.parts.header->n_parts) return;
+  const int unit = blockIdx.x - nparts;
+  const int kvh = is_part ? (blockIdx.x / NSPLIT) % a.hkv : unit / (nunits * NSPLIT);
+  const int rem = unit % (nunits * NSPLIT);
+  const int ks = is_part ? blockIdx.x % NSPLIT : rem % NSPLIT;
+  const int e = is_part ? a.parts.parts[part].x : a.order[rem / NSPLIT];
+  if (KEEP && !is_part && a.weight[e] > a.parts.header->cap) return;  // done by its parts
   const int bi = e / a.nk;
   const int kt = e % a.nk;
-  const int2 rng = a.range[e];
-  const int nsteps_total = a.weight[e] * a.g * AStepIter<BM>::kSub;
+  int2 rng = a.range[e];
+  int ntiles = a.weight[e];  // non-SKIP query tiles
+  if (is_part) {
+    rng = make_int2(a.parts.parts[part].y, a.parts.parts[part].z);
+    ntiles = 0;
+    for (int i0 = rng.x; i0 <= rng.y; i0 += kThreads) {
+      const int i = i0 + threadIdx.x;
+      ntiles += __syncthreads_count(i <= rng.y && a.cls[((size_t)bi * a.nq + i) * a.nk + kt] != kSkip);
+    }
+  }
+  const int nsteps_total = ntiles * a.g * AStepIter<BM>::kSub;
   AStepIter<BM> it0;
   it0.hh = 0;
   it0.i_first = rng.x;
@@ -529,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
-    const int reach = key_reach(pk, a.window, a.sink);  // this key's
     const float sl2 = a.scale_log2;
     if constexpr (KT || VT) {
       // this thread's key (KT) and value (VT) rows into TMEM as bf16 pairs
@@ -598,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qa[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            p[4 * c + u] = visible(ia[u], qa[u], ik, pk, reach) ? p[4 * c + u] : 0.f;
+            if (!visible<KEEP>(ia[u], qa[u], ik, pk, a.window, a.sink)) p[4 * c + u] = 0.f;
         }
       }
       uint32_t pk2[kHB / 2];
@@ -657,6 +676,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
 #pragma unroll
           for (int u = 0; u < 32; ++u) o[u] = 0u;
+        }
+        if constexpr (KEEP) {
+          if (is_part) {
+            float4* dst = reinterpret_cast<float4*>(
+                a.parts.buf + (((int64_t)part * a.hkv + kvh) * 128 + kr) * (DK + DV) +
+                (w == 0 ? DK + ks * L::DVS : ks * L::DKS) + c);
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              dst[u] = make_float4(__uint_as_float(o[4 * u]) * sc, __uint_as_float(o[4 * u + 1]) * sc,
+                                   __uint_as_float(o[4 * u + 2]) * sc, __uint_as_float(o[4 * u + 3]) * sc);
+            continue;
+          }
         }
         if (!key_in) continue;
         if (a.accumulate) {
@@ -747,7 +778,7 @@ struct QTBars {
 };
 static_assert(sizeof(QTBars) <= 512, "barrier block too large");
 
-template <int DK, int DV, int BN_, int NKV_, bool OT>
+template <int DK, int DV, int BN_, int NKV_, bool OT, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq_tmem_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v,
@@ -1046,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int ka[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            p[4 * c + u] = visible(iq, pq, ia[u], ka[u], key_reach(ka[u], a.window, a.sink)) ? p[4 * c + u] : 0.f;
+            if (!visible<KEEP>(iq, pq, ia[u], ka[u], a.window, a.sink)) p[4 * c + u] = 0.f;
         }
       }
       mbar_arrive(&bars->id_empty[en]);
@@ -1125,13 +1156,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int DK, int DV, int BN, int NKV, bool OT>
+template <int DK, int DV, int BN, int NKV, bool OT, bool KEEP>
 cudaError_t launch_dq_tmem(const SplitArgs& a, const SplitLaunch& Lc, cudaStream_t st) {
   using L = QTLayout<DK, DV, BN, NKV, OT>;
   const int64_t units = (int64_t)a.b * a.nq * a.hq;
   if (units == 0) return cudaSuccess;
   static std::atomic<int> smem_set[kMaxDevices];
-  auto kern = attn_bwd_dq_tmem_kernel<DK, DV, BN, NKV, OT>;
+  auto kern = attn_bwd_dq_tmem_kernel<DK, DV, BN, NKV, OT, KEEP>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::alloc, kLaunchRegs,
                                     smem_set);
   if (e != cudaSuccess) return e;
@@ -1142,18 +1173,38 @@ cudaError_t launch_dq_tmem(const SplitArgs& a, const SplitLaunch& Lc, cudaStream
   return cudaGetLastError();
 }
 
-template <int DK, int DV, int BM, int NSPLIT, int NQ, int NO, bool KT = false, bool VT = false>
+template <bool KEEP, int DK, int DV, int BM, int NSPLIT, int NQ, int NO, bool KT = false, bool VT = false>
 cudaError_t launch_dkdv(const SplitArgs& a, const SplitLaunch& Lc, cudaStream_t st) {
   using L = ALayout<DK, DV, BM, NSPLIT, NQ, NO, KT, VT>;
-  const int64_t units = (int64_t)a.b * a.nk * a.hkv * NSPLIT;
+  const int64_t units = ((int64_t)a.b * a.nk + (KEEP ? a.parts.max_parts : 0)) * a.hkv * NSPLIT;
   if (units == 0) return cudaSuccess;
+  if (units > 0x7fffffffll) return cudaErrorNotSupported;
   static std::atomic<int> smem_set[kMaxDevices];
-  auto kern = attn_bwd_dkdv_kernel<DK, DV, BM, NSPLIT, NQ, NO, KT, VT>;
+  auto kern = attn_bwd_dkdv_kernel<DK, DV, BM, NSPLIT, NQ, NO, KT, VT, KEEP>;
   cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), L::alloc, kLaunchRegs,
                                     smem_set);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)units, kThreads, L::alloc, st>>>(Lc.tm_q_a, Lc.tm_k, Lc.tm_v, Lc.tm_do_a, a);
   return cudaGetLastError();
+}
+
+// The dK / dV kernel, then the dQ kernel.
+template <bool KEEP>
+cudaError_t launch_pair(const SplitArgs& ak, const SplitArgs& aq, const SplitLaunch& Lc,
+                        cudaStream_t st) {
+  const attn_fwd_params& f = Lc.p->fwd;
+  const int64_t dv = f.d_v > 0 ? f.d_v : f.d;
+  cudaError_t e;
+  if (f.d == 128 && dv == 128) e = launch_dkdv<KEEP, 128, 128, 128, 1, 2, 2>(ak, Lc, st);
+  else if (f.d == 64 && dv == 64) e = launch_dkdv<KEEP, 64, 64, 128, 1, 2, 2>(ak, Lc, st);
+  else if (f.d == 192 && dv == 128) e = launch_dkdv<KEEP, 192, 128, 64, 1, 2, 2, false, true>(ak, Lc, st);
+  else if (f.d == 256 && dv == 256) e = launch_dkdv<KEEP, 256, 256, 64, 2, 2, 2, true>(ak, Lc, st);
+  else return cudaErrorNotSupported;
+  if (e != cudaSuccess) return e;
+  if (f.d == 128) return launch_dq_tmem<128, 128, 128, 6, true, KEEP>(aq, Lc, st);
+  if (f.d == 64) return launch_dq_tmem<64, 64, 128, 6, true, KEEP>(aq, Lc, st);
+  if (f.d == 192) return launch_dq_tmem<192, 128, 64, 6, true, KEEP>(aq, Lc, st);
+  return launch_dq_tmem<256, 256, 64, 4, false, KEEP>(aq, Lc, st);
 }
 
 }  // namespace
@@ -1172,7 +1223,7 @@ cudaError_t launch_attn_bwd_split(const SplitLaunch& Lc, cudaStream_t st) {
   const attn_bwd_params& p = *Lc.p;
   const attn_fwd_params& f = p.fwd;
   const int64_t dv = f.d_v > 0 ? f.d_v : f.d;
-  SplitArgs a;
+  SplitArgs a = {};
   a.k = static_cast<const __nv_bfloat16*>(f.k);
   a.v = static_cast<const __nv_bfloat16*>(f.v);
   a.q_ids = f.q_segment_ids;
@@ -1207,22 +1258,13 @@ cudaError_t launch_attn_bwd_split(const SplitLaunch& Lc, cudaStream_t st) {
   ak.range = Lc.plan.kv_range;
   ak.weight = Lc.plan.kv_weight;
   ak.order = Lc.plan.kv_order;
-  cudaError_t e;
-  if (f.d == 128 && dv == 128) e = launch_dkdv<128, 128, 128, 1, 2, 2>(ak, Lc, st);
-  else if (f.d == 64 && dv == 64) e = launch_dkdv<64, 64, 128, 1, 2, 2>(ak, Lc, st);
-  else if (f.d == 192 && dv == 128) e = launch_dkdv<192, 128, 64, 1, 2, 2, false, true>(ak, Lc, st);
-  else if (f.d == 256 && dv == 256) e = launch_dkdv<256, 256, 64, 2, 2, 2, true>(ak, Lc, st);
-  else return cudaErrorNotSupported;
-  if (e != cudaSuccess) return e;
+  ak.parts = Lc.parts;
   // dQ: q side of the plan
   SplitArgs aq = a;
   aq.range = Lc.plan.q_range;
   aq.weight = Lc.plan.q_weight;
   aq.order = Lc.plan.q_order;
-  if (f.d == 128) return launch_dq_tmem<128, 128, 128, 6, true>(aq, Lc, st);
-  if (f.d == 64) return launch_dq_tmem<64, 64, 128, 6, true>(aq, Lc, st);
-  if (f.d == 192) return launch_dq_tmem<192, 128, 64, 6, true>(aq, Lc, st);
-  return launch_dq_tmem<256, 256, 64, 4, false>(aq, Lc, st);
+  return keeps_tokens(f) ? launch_pair<true>(ak, aq, Lc, st) : launch_pair<false>(ak, aq, Lc, st);
 }
 
 }  // namespace gb300

@@ -35,8 +35,6 @@
 // reference m.
 #include <cuda_bf16.h>
 
-#include <climits>
-
 #include "internal.h"
 #include "merge_math.cuh"
 #include "ptx.cuh"
@@ -142,7 +140,9 @@ __device__ __forceinline__ int next_live_tile(const uint8_t* cls_row, int j, int
   return last + 1;
 }
 
-template <int DK, int DV>
+// KEEP: first tokens stay visible behind the window (its own variant, so that the
+// other masks' code stays as it is)
+template <int DK, int DV, bool KEEP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const FwdArgs a) {
@@ -448,7 +448,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         const int kind = s_ids[en * kIdEntry + 2 * BN];
         if (kind == kPartial) {
-          const int reach = a.window < 0 ? INT_MAX : a.window;
           const int4* ids4 = reinterpret_cast<const int4*>(s_ids + en * kIdEntry);
           const int4* pos4 = reinterpret_cast<const int4*>(s_ids + en * kIdEntry + BN);
 #pragma unroll
@@ -459,10 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pka[4] = {pk4.x, pk4.y, pk4.z, pk4.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              // (no branch per pair: the rows of a warp may differ)
-              const bool vis = (ika[u] == iq) & (iq != 0) & (pka[u] <= pq) &
-                               ((pq - pka[u] <= reach) | (pka[u] < a.sink));
-              sr[4 * c + u] = vis ? sr[4 * c + u] : __float_as_uint(-INFINITY);
+              bool vis = (ika[u] == iq) && (iq != 0) && (pka[u] <= pq);
+              if constexpr (KEEP)  // (no branch per pair: the rows of a warp differ)
+                vis = vis & ((pq - pka[u] <= a.window) | (pka[u] < a.sink));
+              else if (a.window >= 0)
+                vis = vis && (pq - pka[u] <= a.window);
+              if (!vis) sr[4 * c + u] = __float_as_uint(-INFINITY);
             }
           }
         }
@@ -642,15 +643,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int DK, int DV>
-cudaError_t launch_fwd_d(const FwdArgs& a, const FwdLaunch& Lc, int64_t units, cudaStream_t st) {
+template <int DK, int DV, bool KEEP>
+cudaError_t launch_fwd_k(const FwdArgs& a, const FwdLaunch& Lc, int64_t units, cudaStream_t st) {
   const int smem = Layout<DK, DV>::alloc;
   static std::atomic<int> smem_set[kMaxDevices];
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_fwd_kernel<DK, DV>), smem,
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(attn_fwd_kernel<DK, DV, KEEP>), smem,
                                     kLaunchRegs, smem_set);
   if (e != cudaSuccess) return e;
-  attn_fwd_kernel<DK, DV><<<(unsigned)units, kThreads, smem, st>>>(Lc.tm_q, Lc.tm_k, Lc.tm_v, a);
+  attn_fwd_kernel<DK, DV, KEEP><<<(unsigned)units, kThreads, smem, st>>>(Lc.tm_q, Lc.tm_k, Lc.tm_v, a);
   return cudaGetLastError();
+}
+
+template <int DK, int DV>
+cudaError_t launch_fwd_d(const FwdArgs& a, const FwdLaunch& Lc, int64_t units, cudaStream_t st) {
+  return keeps_tokens(*Lc.p) ? launch_fwd_k<DK, DV, true>(a, Lc, units, st)
+                             : launch_fwd_k<DK, DV, false>(a, Lc, units, st);
 }
 
 }  // namespace

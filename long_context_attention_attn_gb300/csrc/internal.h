@@ -134,6 +134,47 @@ inline PlanPtrs plan_ptrs(void* ws, const PlanLayout& L) {
                   L.sort_buckets};
 }
 
+// Whether the mask keeps first tokens visible behind the window.
+inline bool keeps_tokens(const attn_fwd_params& p) { return p.window_left >= 0 && p.sink_tokens > 0; }
+
+// ---- attn_bwd_parts.cu
+// Kept tokens make a key tile that holds some see every later query tile of
+// its segment, many times the work of the other key tiles: the kernels that
+// own a key tile per CTA then cut such a tile into parts of its query tiles,
+// one CTA each, whose fp32 dK / dV are folded in order afterwards.
+struct PartHeader {
+  int cap;      // key tiles with more (live) query tiles than this are cut
+  int n_parts;  // entries of parts
+  int n_tiles;  // entries of tiles
+  int reserved;
+};
+struct KeyParts {
+  PartHeader* header;
+  int4* parts;  // (b, key tile) index, first and last query tile, 0
+  int4* tiles;  // (b, key tile) index, its first part, its parts, 0
+  float* buf;   // [max_parts, h_kv, 128, d + d_v] fp32: dK, then dV
+  int max_parts;
+};
+// Parts over all kv heads, at most: three for each SM, so that a part is no
+// more than two thirds of an SM's share of the launch.
+constexpr int kPartsTotal = 3 * 152;
+inline int64_t max_key_parts(int64_t h_kv) { return (kPartsTotal + h_kv - 1) / h_kv; }
+inline size_t key_parts_bytes(int64_t h_kv, int64_t d, int64_t dv) {
+  const size_t n = (size_t)max_key_parts(h_kv);
+  return align_up(256 + 2 * n * sizeof(int4), 256) + align_up(n * h_kv * 128 * (d + dv) * 4, 256);
+}
+inline KeyParts key_parts(void* ws, int64_t h_kv) {
+  char* c = static_cast<char*>(ws);
+  const size_t n = (size_t)max_key_parts(h_kv);
+  return KeyParts{reinterpret_cast<PartHeader*>(c), reinterpret_cast<int4*>(c + 256),
+                  reinterpret_cast<int4*>(c + 256) + n,
+                  reinterpret_cast<float*>(c + align_up(256 + 2 * n * sizeof(int4), 256)), (int)n};
+}
+cudaError_t launch_key_parts(const attn_fwd_params& f, const PlanPtrs& pp, int64_t nk,
+                             const KeyParts& kp, cudaStream_t st);
+cudaError_t launch_fold_parts(const attn_bwd_params& p, int64_t nk, const KeyParts& kp,
+                              cudaStream_t st);
+
 // ---- kernels_misc.cu
 int sm_count();  // SMs of the current device
 // q_ctas / kv_ctas: CTAs the kernel that takes the query / key side's work
@@ -180,6 +221,7 @@ struct BwdLaunch {
   float* dq_acc;  // [b, s_q, hq, d]
   CUtensorMap tm_q, tm_k, tm_v, tm_do;
   CUtensorMap tm_dq;  // fp32 dQ accumulator, 32 d x 128 rows boxes, 128B swizzle
+  KeyParts parts;     // with kept tokens only
 };
 cudaError_t launch_attn_bwd(const BwdLaunch& L, cudaStream_t st);
 
@@ -194,6 +236,7 @@ struct SplitLaunch {
   CUtensorMap tm_q_a, tm_do_a;   // split_bwd_query_rows()-row boxes (dK / dV kernel)
   CUtensorMap tm_k, tm_v;        // 128-row boxes (dK / dV kernel)
   CUtensorMap tm_kb, tm_vb;      // split_bwd_key_rows()-row boxes (dQ kernel)
+  KeyParts parts;                // with kept tokens only
 };
 int split_bwd_query_rows(int64_t d, int64_t dv);
 int split_bwd_key_rows(int64_t d, int64_t dv);

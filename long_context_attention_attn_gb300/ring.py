@@ -229,7 +229,8 @@ def ring_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *, window_lef
     lse_sh = torch.empty(R, hq, n, dtype=torch.float32, device=dev)
     ws = torch.empty(workspace_bytes_bwd(qr[:1, :n], kr[:1, :n], idr[:1, :n], posr[:1, :n],
                                          window_left, v=vr[:1, :n],
-                                         deterministic=deterministic),
+                                         deterministic=deterministic,
+                                         sink_tokens=sink_tokens),
                      dtype=torch.uint8, device=dev)
     log = _StatusLog(b * R * R, dev) if check_status else None
     for bi in range(b):
@@ -291,7 +292,8 @@ def allgather_attn_bwd(q, k, v, out, lse, dout, ids, pos, cp_size: int, *,
     dv = torch.zeros(b, s, k.shape[2], v.shape[3], dtype=torch.float32, device=dev)
     lse_sh = torch.empty(R, hq, n, dtype=torch.float32, device=dev)
     ws = torch.empty(workspace_bytes_bwd(qr[:1, :n], kr[:1], idr[:1, :n], posr[:1, :n],
-                                         window_left, v=vr[:1], deterministic=deterministic),
+                                         window_left, v=vr[:1], deterministic=deterministic,
+                                         sink_tokens=sink_tokens),
                      dtype=torch.uint8, device=dev)
     log = _StatusLog(b * R, dev) if check_status else None
     for bi in range(b):
@@ -404,7 +406,8 @@ def _ring_bwd_batched(qr, kr, vr, outr, dor, idr, posr, lse, R, window_left, sca
     dk_held = torch.zeros(b, s, hkv, d, dtype=torch.float32, device=dev)
     dv_held = torch.zeros(b, s, hkv, dv, dtype=torch.float32, device=dev)
     ws = torch.empty(workspace_bytes_bwd(qa, kr.view(B, n, hkv, d), ida, pa, window_left,
-                                         v=vr.view(B, n, hkv, dv), deterministic=deterministic),
+                                         v=vr.view(B, n, hkv, dv), deterministic=deterministic,
+                                         sink_tokens=sink_tokens),
                      dtype=torch.uint8, device=dev)
     log = _StatusLog(R, dev) if check_status else None
     for t in range(R):
