@@ -957,12 +957,21 @@ struct Kernel {
     if (cached) cache[dev].store(*n, std::memory_order_release);
     return cudaSuccess;
   }
-  static cudaError_t launch(DecodeArgs& a, cudaStream_t st) {
-    int n = 0;
-    cudaError_t e = grid(&n);
-    if (e != cudaSuccess) return e;
+  // CTAs of a launch: no more than shortest runs of the longest sequences that the
+  // page table can hold
+  static cudaError_t grid_for(const attn_decode_params& p, int64_t row_tiles, int* n) {
+    const cudaError_t e = grid(n);
+    using T = Tune<D, NT>;
+    const int64_t blocks = (p.max_pages * p.cache.page_size + T::kBlock - 1) / T::kBlock + T::kItemCost;
+    const int64_t items = p.n * p.cache.h_kv * row_tiles;
+    const int64_t most = (blocks * items + kMinRun - 1) / kMinRun;
+    if (most < *n) *n = (int)most;
+    return e;
+  }
+  static cudaError_t launch(DecodeArgs& a, int n, cudaStream_t st) {
     a.grid = n;
     a.part_lse = a.part_o + (int64_t)2 * n * C::R * D;
+    cudaError_t e;
     attn_decode_kernel<D, NT><<<n, kThreads, C::bytes, st>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -1002,7 +1011,7 @@ cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes) {
   const int nt = n_tiles(d, rows);
   return dispatch(d, nt, [&](auto k) {
     int n = 0;
-    const cudaError_t e = k.grid(&n);
+    const cudaError_t e = k.grid_for(p, (rows + nt * 8 - 1) / (nt * 8), &n);
     *bytes = align_up((size_t)2 * n * nt * 8 * (d + 1) * 4, 256);
     return e;
   });
@@ -1037,7 +1046,11 @@ cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
   a.sink = (int)p.sink_tokens;
   a.out_fp32 = p.out_fp32 ? 1 : 0;
   a.scale_log2 = p.scale * 1.4426950408889634f;
-  return dispatch(c.d, nt, [&](auto k) { return k.launch(a, st); });
+  return dispatch(c.d, nt, [&](auto k) {
+    int n = 0;
+    const cudaError_t e = k.grid_for(p, a.row_tiles, &n);
+    return e == cudaSuccess ? k.launch(a, n, st) : e;
+  });
 }
 
 }  // namespace gb300

@@ -58,6 +58,12 @@ __device__ __forceinline__ float amax_finite(float m, uint32_t w) {
   return m;
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 // Exponent k of the smallest power of two with amax <= 448 * 2^k (448 = 1.75 *
 // 2^8, so the exponent less 8, and one more above a mantissa of 1.75), no less
 // than -126.
@@ -98,12 +104,14 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv_append_kernel(const Appe
   // the slots [lo, hi) of this page that get new tokens
   const int64_t page_first = (int64_t)entry * a.page_size;
   const int64_t end = (int64_t)start + len;
-  const int lo = (int)max((int64_t)start - page_first, (int64_t)0);
-  const int hi = (int)min(end - page_first, (int64_t)a.page_size);
-  if (hi <= lo) return;
+  // slot t takes token row at0 + t, of the rows that there are
+  const int64_t at0 = row0 + (page_first - start);
+  const int64_t lo64 = max(max((int64_t)start - page_first, (int64_t)0), -at0);
+  const int64_t hi64 = min(min(end - page_first, (int64_t)a.page_size), a.tokens - at0);
+  if (hi64 <= lo64) return;
+  const int lo = (int)lo64, hi = (int)hi64;  // 0 <= lo < hi <= page_size
   const int pid = a.table[i * a.max_pages + entry];
   if (pid < 0 || pid >= a.num_pages) return;
-  const int64_t src0 = row0 + (page_first + lo - start);  // token row of slot lo
 
   const __nv_bfloat16* x = (is_v ? a.v : a.k) + (int64_t)h * D;
   uint8_t* page = (is_v ? a.vc : a.kc) + pid * a.page_stride + (int64_t)h * a.page_size * D;
@@ -111,28 +119,42 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv_append_kernel(const Appe
   const float old = lo > 0 ? *scale : 0.f;
 
   const int chunks = (hi - lo) * kRowChunks;
+  const uint4* src = reinterpret_cast<const uint4*>(x + (at0 + lo + tid / kRowChunks) * a.token_stride) +
+                     2 * (tid % kRowChunks);
+  const int64_t step = (int64_t)(T / kRowChunks) * a.token_stride / 8;  // T % kRowChunks == 0
   uint4 r[kChunksPerThread][2];
-  float amax = 0.f;
 #pragma unroll
   for (int u = 0; u < kChunksPerThread; ++u) {
-    const int c = u * T + tid;
-    const int64_t row = src0 + c / kRowChunks;
     r[u][0] = r[u][1] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < chunks && row >= 0 && row < a.tokens) {
-      const uint4* p = reinterpret_cast<const uint4*>(x + row * a.token_stride) + 2 * (c % kRowChunks);
-      r[u][0] = __ldcs(p);
-      r[u][1] = __ldcs(p + 1);
+    if (u * T + tid < chunks) {
+      r[u][0] = __ldcs(src + u * step);
+      r[u][1] = __ldcs(src + u * step + 1);
     }
   }
+  // magnitudes of bf16 order like their bits, two in a word
+  uint32_t top = 0;
 #pragma unroll
   for (int u = 0; u < kChunksPerThread; ++u)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      amax = amax_finite(amax, r[u][e].x);
-      amax = amax_finite(amax, r[u][e].y);
-      amax = amax_finite(amax, r[u][e].z);
-      amax = amax_finite(amax, r[u][e].w);
+      top = max_u16x2(top, r[u][e].x & 0x7fff7fffu);
+      top = max_u16x2(top, r[u][e].y & 0x7fff7fffu);
+      top = max_u16x2(top, r[u][e].z & 0x7fff7fffu);
+      top = max_u16x2(top, r[u][e].w & 0x7fff7fffu);
     }
+  float amax = __uint_as_float(max(top << 16, top & 0xffff0000u));
+  if (!(amax < INFINITY)) {  // infinities or NaN: only what is finite counts
+    amax = 0.f;
+#pragma unroll
+    for (int u = 0; u < kChunksPerThread; ++u)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        amax = amax_finite(amax, r[u][e].x);
+        amax = amax_finite(amax, r[u][e].y);
+        amax = amax_finite(amax, r[u][e].z);
+        amax = amax_finite(amax, r[u][e].w);
+      }
+  }
   // non-negative floats order like their bits
   uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
   if constexpr (T > 32) {
@@ -163,11 +185,10 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv_append_kernel(const Appe
       *p = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
+  uint4* dst = reinterpret_cast<uint4*>(page) + lo * kRowChunks + tid;
 #pragma unroll
   for (int u = 0; u < kChunksPerThread; ++u) {
-    const int c = u * T + tid;
-    const int64_t row = src0 + c / kRowChunks;
-    if (c < chunks && row >= 0 && row < a.tokens) {
+    if (u * T + tid < chunks) {
       uint32_t o[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -178,7 +199,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv_append_kernel(const Appe
           o[2 * e + q] = to_e4m3x2(f0.x * inv, f0.y * inv) | (to_e4m3x2(f1.x * inv, f1.y * inv) << 16);
         }
       }
-      reinterpret_cast<uint4*>(page)[lo * kRowChunks + c] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[u * T] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
   // every thread read the old scale before the barrier of the maximum

@@ -84,6 +84,21 @@ def test_append_packed_prompts_and_dropped_tokens(ga):
     _same(cache, want)
 
 
+def test_append_token_rows_outside_the_tensor(ga):
+    """Rows before the first and behind the last are dropped, however far: what stays of a
+    page's new tokens counts, and the slots before them are the page's older tokens."""
+    size, h, d = 16, 1, 64
+    tok = [-3, -(1 << 31), (1 << 31) - 1, 25, -40, 20]
+    start, lens = [5, 0, 0, 3, 9, 30], [30, 40, 40, 40, 40, 2]
+    cache = _cache(20, h, size, d, seed=8)
+    table = _tables(6, 3, 20, seed=8)
+    k, v = _new(1, 30, h, d, seed=8)
+    want = _expect(k, v, cache, table, start, lens, tok)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    ga.kv_cache_append(k, v, *cache, table.to(DEV), i32(start), lens=i32(lens), tok_start=i32(tok), max_new=40)
+    _same(cache, want)
+
+
 @pytest.mark.parametrize("fill", ["zero", "inf", "nan", "tiny", "huge", "border"])
 def test_append_values_at_the_borders(ga, fill):
     size, h, d = 32, 1, 64
