@@ -556,7 +556,7 @@ def _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, w
     n, s_q, h_q, _ = q.shape
     kind = torch.float32 if out_fp32 else torch.bfloat16
     if out is None:
-        out = torch.empty_like(q, dtype=kind)
+        out = torch.empty_like(q, dtype=kind) if out_fp32 else torch.empty_like(q)
     elif (out.shape != q.shape or out.dtype != kind or not out.is_contiguous()
           or out.get_device() != index):
         raise ValueError("out must be a contiguous [n, s_q, h_q, d] tensor, bf16 (fp32 with out_fp32)")
@@ -601,7 +601,11 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
                                         window_left, sink_tokens, scale, out, lse, out_fp32)
     ref = ctypes.byref(p)
     if workspace is None:
-        need = _on_device(index, lambda r, _: lib().attn_decode_workspace_bytes(r), ref)
+        if torch._C._cuda_getDevice() == index:
+            need = lib().attn_decode_workspace_bytes(ref)
+        else:
+            with torch.cuda.device(index):
+                need = lib().attn_decode_workspace_bytes(ref)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the call's device")

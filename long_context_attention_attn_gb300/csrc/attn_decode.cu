@@ -834,12 +834,17 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
   }
 }
 
-// One CTA per item: folds the partials of an item that several CTAs shared,
-// and writes the empty result of a sequence without keys.
+// Folds the partials of an item that several CTAs shared, and writes the empty
+// result of a sequence without keys: one thread per four values, the rows of an
+// item over blockIdx.y.
+constexpr int kFoldThreads = 2 * kThreads;
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads * 2) attn_decode_combine_kernel(const DecodeArgs a) {
+constexpr int kFoldRows = NT * 8 * (D / 4) < kFoldThreads ? NT * 8 : kFoldThreads / (D / 4);
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFoldThreads) attn_decode_combine_kernel(const DecodeArgs a) {
   using T = Tune<D, NT>;
-  constexpr int R = NT * 8;
+  constexpr int R = NT * 8, RP = kFoldRows<D, NT>, kVec = D / 4;
   __shared__ int64_t before[kThreads + 1];
   const Placement pl = place<T>(a, before);
   const int items = a.h_kv * a.row_tiles;
@@ -860,71 +865,62 @@ __global__ void __launch_bounds__(kThreads * 2) attn_decode_combine_kernel(const
   // The weights of up to kMost pieces at a time through shared memory, then
   // their rows, several loads in flight; later batches of pieces rescale.
   constexpr int kMost = 32;
-  __shared__ float s_w[kMost][R];
-  __shared__ float s_ref[R], s_old[R];
-  constexpr int kVec = D / 4, kAll = 2 * kThreads, kPer = (R * kVec + kAll - 1) / kAll;
-  float4 acc[kPer];
-  float z[kPer];
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) {
-    acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
-    z[x] = 0.f;
-  }
-  if (threadIdx.x < R) s_ref[threadIdx.x] = -INFINITY;
+  __shared__ float s_w[kMost][RP];
+  __shared__ float s_ref[RP], s_old[RP];
+  const int r = threadIdx.x / kVec, d4 = threadIdx.x % kVec;  // this thread's row and values
+  const int r0 = blockIdx.y * RP;                             // the CTA's first row
+  const bool mine = r < RP;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float z = 0.f;
+  if (threadIdx.x < RP) s_ref[threadIdx.x] = -INFINITY;
   __syncthreads();
   for (int64_t b0 = c0; count && b0 <= c1; b0 += kMost) {
     const int np = (int)min((int64_t)kMost, c1 - b0 + 1);
     // only the first piece can be a CTA's last one (it starts at the item's start)
     auto slot = [&](int i) { return 2 * (b0 + i) + ((b0 + i) * run <= s0 ? 1 : 0); };
-    for (int u = threadIdx.x; u < np * R; u += kAll) s_w[u / R][u % R] = a.part_lse[slot(u / R) * R + u % R];
+    for (int u = threadIdx.x; u < np * RP; u += kFoldThreads)
+      s_w[u / RP][u % RP] = a.part_lse[slot(u / RP) * R + r0 + u % RP];
     __syncthreads();
-    if (threadIdx.x < R) {
+    if (threadIdx.x < RP) {
       float top = s_ref[threadIdx.x];
       for (int i = 0; i < np; ++i) top = fmaxf(top, s_w[i][threadIdx.x]);
       s_old[threadIdx.x] = top == -INFINITY ? 0.f : ex2(s_ref[threadIdx.x] - top);
       s_ref[threadIdx.x] = top;
     }
     __syncthreads();
-#pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int u = x * kAll + threadIdx.x, r = u / kVec, d4 = u % kVec;
-      if (R * kVec < kAll && r >= R) break;
+    if (mine) {
       const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
-      z[x] *= old;
-      acc[x].x *= old;
-      acc[x].y *= old;
-      acc[x].z *= old;
-      acc[x].w *= old;
+      z *= old;
+      acc.x *= old;
+      acc.y *= old;
+      acc.z *= old;
+      acc.w *= old;
 #pragma unroll 8
       for (int i = 0; i < np; ++i) {
         const float f = ex2(s_w[i][r] - ref);
-        const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(i) * R + r) * D)[d4];
-        z[x] += f;
-        acc[x].x += v.x * f;
-        acc[x].y += v.y * f;
-        acc[x].z += v.z * f;
-        acc[x].w += v.w * f;
+        const float4 v = reinterpret_cast<const float4*>(a.part_o + (slot(i) * R + r0 + r) * D)[d4];
+        z += f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
       }
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int x = 0; x < kPer; ++x) {
-    const int u = x * kAll + threadIdx.x, r = u / kVec, d4 = u % kVec;
-    const int row = rt * R + r;
-    if (r >= R || row >= a.rows) break;
-    const float inv = z[x] == 0.f ? 0.f : 1.f / z[x];
-    const int tok = row / a.g, head = kvh * a.g + row % a.g;
-    const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
-    const float4 o = make_float4(acc[x].x * inv, acc[x].y * inv, acc[x].z * inv, acc[x].w * inv);
-    if (a.out_fp32)
-      reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = o;
-    else
-      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
-          make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-    if (d4 == 0)
-      a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z[x] == 0.f ? -INFINITY : (s_ref[r] + log2f(z[x])) * kLn2;
-  }
+  const int row = rt * R + r0 + r;
+  if (!mine || row >= a.rows) return;
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  const int tok = row / a.g, head = kvh * a.g + row % a.g;
+  const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
+  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  if (a.out_fp32)
+    reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = o;
+  else
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
+        make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+  if (d4 == 0)
+    a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (s_ref[r] + log2f(z)) * kLn2;
 }
 
 // N tiles of 8 rows per CTA: the fewest that hold the rows, up to what the
@@ -976,8 +972,8 @@ struct Kernel {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.h_kv * a.row_tiles));
-    cfg.blockDim = dim3(kThreads * 2);
+    cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.h_kv * a.row_tiles), C::R / kFoldRows<D, NT>);
+    cfg.blockDim = dim3(kFoldThreads);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
