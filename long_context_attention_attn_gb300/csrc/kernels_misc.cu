@@ -57,20 +57,14 @@ __device__ __forceinline__ TileSummary warp_tile_summary(const int* __restrict__
   return r;
 }
 
-// One warp per tile: the query side's tiles, then the key side's.
-__global__ void tile_summary_kernel(const int* __restrict__ q_ids, const int* __restrict__ q_pos,
-                                    const int* __restrict__ kv_ids, const int* __restrict__ kv_pos,
-                                    int64_t b, int64_t s_q, int64_t s_kv, int64_t nq, int64_t nk,
-                                    TileSummary* __restrict__ q_out, TileSummary* __restrict__ kv_out) {
-  int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
+__global__ void tile_summary_kernel(const int* __restrict__ ids, const int* __restrict__ pos,
+                                    int64_t b, int64_t s, int64_t ntile,
+                                    TileSummary* __restrict__ out) {
+  const int64_t w = (int64_t)blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   const int lane = threadIdx.x & 31;
-  if (w >= b * (nq + nk)) return;
-  const bool qside = w < b * nq;
-  if (!qside) w -= b * nq;
-  const int64_t nt = qside ? nq : nk;
-  const TileSummary r = qside ? warp_tile_summary(q_ids, q_pos, s_q, w / nt, w % nt, lane)
-                              : warp_tile_summary(kv_ids, kv_pos, s_kv, w / nt, w % nt, lane);
-  if (lane == 0) (qside ? q_out : kv_out)[w] = r;
+  if (w >= b * ntile) return;
+  const TileSummary r = warp_tile_summary(ids, pos, s, w / ntile, w % ntile, lane);
+  if (lane == 0) out[w] = r;
 }
 
 // sink: keys at positions below it stay visible behind the window.
@@ -580,9 +574,10 @@ cudaError_t launch_tile_plan(const attn_fwd_params& p, const PlanPtrs& pp, int64
     return cudaGetLastError();
   }
   const int wpb = 8;
-  tile_summary_kernel<<<(unsigned)((p.b * (nq + nk) + wpb - 1) / wpb), wpb * 32, 0, st>>>(
-      p.q_segment_ids, p.q_segment_pos, p.kv_segment_ids, p.kv_segment_pos, p.b, p.s_q, p.s_kv, nq,
-      nk, pp.q_sum, pp.kv_sum);
+  tile_summary_kernel<<<(unsigned)((p.b * nq + wpb - 1) / wpb), wpb * 32, 0, st>>>(
+      p.q_segment_ids, p.q_segment_pos, p.b, p.s_q, nq, pp.q_sum);
+  tile_summary_kernel<<<(unsigned)((p.b * nk + wpb - 1) / wpb), wpb * 32, 0, st>>>(
+      p.kv_segment_ids, p.kv_segment_pos, p.b, p.s_kv, nk, pp.kv_sum);
   tile_class_kernel<<<dim3((unsigned)nq, (unsigned)p.b), 256, 0, st>>>(
       pp.q_sum, pp.kv_sum, nq, nk, p.window_left, (int)p.sink_tokens, pp.classes, pp.q_range,
       pp.q_weight);
