@@ -222,8 +222,7 @@ size_t attn_bwd_workspace_bytes(const attn_bwd_params* p) {
   if (!p || check_fwd(&p->fwd) != ATTN_OK) return 0;
   const PlanLayout L = fwd_layout(&p->fwd);
   const size_t d_bytes = align_up((size_t)(p->fwd.b * p->fwd.h_q * p->fwd.s_q) * 4, 256);
-  const size_t part_bytes =
-      keeps_tokens(p->fwd) ? key_parts_bytes(p->fwd.h_kv, p->fwd.d, fwd_dv(&p->fwd)) : 0;
+  const size_t part_bytes = key_parts_bytes(p->fwd);
   if (use_split_bwd(p)) return L.end + d_bytes + part_bytes;
   const size_t dq_bytes = align_up((size_t)(p->fwd.b * p->fwd.s_q * p->fwd.h_q * p->fwd.d) * 4, 256);
   return L.end + d_bytes + part_bytes + dq_bytes;
@@ -284,10 +283,9 @@ int attn_bwd(const attn_bwd_params* p, attn_stream_t stream) {
                : cudaSuccess;
   };
   // after D: the parts of key tiles that hold kept tokens
-  const bool keep = keeps_tokens(*f);
   const size_t parts_at = L.end + align_up((size_t)(f->b * f->h_q * f->s_q) * 4, 256);
-  KeyParts parts = {};
-  if (keep) parts = key_parts(static_cast<char*>(f->workspace) + parts_at, f->h_kv);
+  const KeyParts parts = key_parts(static_cast<char*>(f->workspace) + parts_at, *f);
+  const bool cut = parts.max_parts > 0;
   if (use_split_bwd(p)) {
     SplitLaunch sl;
     sl.parts = parts;
@@ -312,14 +310,14 @@ int attn_bwd(const attn_bwd_params* p, attn_stream_t stream) {
     if (e == cudaSuccess)
       e = launch_tile_plan(*f, sl.plan, sl.nq, sl.nk, true, f->h_q,
                            f->h_kv * split_bwd_col_slices(f->d, dv), st);
-    if (e == cudaSuccess && keep) e = launch_key_parts(*f, sl.plan, sl.nk, parts, st);
+    if (e == cudaSuccess && cut) e = launch_key_parts(*f, sl.plan, sl.nk, parts, st);
     if (e == cudaSuccess)
       e = launch_bwd_preprocess(f->out, p->dout, sl.D, nullptr, sl.plan.q_weight, f->b, f->s_q,
                                 f->h_q, dv, st);
     if (e == cudaSuccess) e = mark(0);
     if (e == cudaSuccess) e = launch_attn_bwd_split(sl, st);
     if (e == cudaSuccess) e = mark(1);
-    if (e == cudaSuccess && keep) e = launch_fold_parts(*p, sl.nk, parts, st);
+    if (e == cudaSuccess && cut) e = launch_fold_parts(*p, sl.nk, parts, st);
     if (e == cudaErrorNotSupported) return ATTN_ERR_UNSUPPORTED;
     return cuda_status(e);
   }
@@ -336,7 +334,7 @@ int attn_bwd(const attn_bwd_params* p, attn_stream_t stream) {
   // accumulate mode: the dQ reduce-adds go straight into the caller's fp32 dq
   bl.dq_acc = acc ? static_cast<float*>(p->dq)
                   : reinterpret_cast<float*>(
-                        ws + parts_at + (keep ? key_parts_bytes(f->h_kv, f->d, dv) : 0));
+                        ws + parts_at + key_parts_bytes(*f));
   if (!encode_qkv_map(&bl.tm_q, f->q, f->b, f->s_q, f->h_q, f->d, 0) ||
       !encode_qkv_map(&bl.tm_k, f->k, f->b, f->s_kv, f->h_kv, f->d, f->kv_token_stride) ||
       !encode_qkv_map(&bl.tm_v, f->v, f->b, f->s_kv, f->h_kv, f->d, f->kv_token_stride) ||
@@ -346,7 +344,7 @@ int attn_bwd(const attn_bwd_params* p, attn_stream_t stream) {
   cudaError_t e = cudaMemsetAsync(bl.plan.status, 0, sizeof(int), st);
   if (e == cudaSuccess)
     e = launch_tile_plan(*f, bl.plan, bl.nq, bl.nk, true, f->h_q, f->h_kv, st);
-  if (e == cudaSuccess && keep) e = launch_key_parts(*f, bl.plan, bl.nk, parts, st);
+  if (e == cudaSuccess && cut) e = launch_key_parts(*f, bl.plan, bl.nk, parts, st);
   // the D pre-pass also zeroes the workspace's fp32 dQ accumulator (not the
   // caller's accumulator in accumulate mode)
   if (e == cudaSuccess)
@@ -355,7 +353,7 @@ int attn_bwd(const attn_bwd_params* p, attn_stream_t stream) {
   if (e == cudaSuccess) e = mark(0);
   if (e == cudaSuccess) e = launch_attn_bwd(bl, st);
   if (e == cudaSuccess) e = mark(1);
-  if (e == cudaSuccess && keep) e = launch_fold_parts(*p, bl.nk, parts, st);
+  if (e == cudaSuccess && cut) e = launch_fold_parts(*p, bl.nk, parts, st);
   if (e == cudaErrorNotSupported) return ATTN_ERR_UNSUPPORTED;
   if (e == cudaSuccess && !acc)
     e = launch_dq_finalize(bl.dq_acc, p->dq, bl.plan.q_weight, f->b, f->s_q, f->h_q, f->d, st);

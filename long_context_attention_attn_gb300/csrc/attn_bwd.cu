@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int unit = blockIdx.x - nparts;
   const int kvh = is_part ? blockIdx.x % a.hkv : unit / nunits;
   const int e = is_part ? a.parts.parts[part].x : a.order[unit % nunits];
-  if (KEEP && !is_part && a.kweight[e] > a.parts.header->cap) return;  // done by its parts
+  if (nparts > 0 && !is_part && a.kweight[e] > a.parts.header->cap) return;  // done by its parts
   const int bi = e / a.nk;
   const int kt = e % a.nk;
   int2 rng = a.krange[e];

@@ -111,8 +111,8 @@ __global__ void __launch_bounds__(kFoldThreads)
 
 cudaError_t launch_key_parts(const attn_fwd_params& f, const PlanPtrs& pp, int64_t nk,
                              const KeyParts& kp, cudaStream_t st) {
-  const int64_t least = f.window_left / kTile + 2;
-  key_parts_kernel<<<1, kListThreads, 0, st>>>(pp.kv_weight, pp.kv_range, (int)(f.b * nk), (int)least, kp);
+  key_parts_kernel<<<1, kListThreads, 0, st>>>(pp.kv_weight, pp.kv_range, (int)(f.b * nk), (int)least_cut(f),
+                                           kp);
   return cudaGetLastError();
 }
 

@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int rem = unit % (nunits * NSPLIT);
   const int ks = is_part ? blockIdx.x % NSPLIT : rem % NSPLIT;
   const int e = is_part ? a.parts.parts[part].x : a.order[rem / NSPLIT];
-  if (KEEP && !is_part && a.weight[e] > a.parts.header->cap) return;  // done by its parts
+  if (nparts > 0 && !is_part && a.weight[e] > a.parts.header->cap) return;  // done by its parts
   const int bi = e / a.nk;
   const int kt = e % a.nk;
   int2 rng = a.range[e];

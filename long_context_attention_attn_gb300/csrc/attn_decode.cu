@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     // (entries behind the last sequence repeat the total, which is above `at`)
     seq = t * pl.per;
     seq_at = before[t] * items;
-    for (;; ++seq) {
+    for (; seq < a.n - 1; ++seq) {
       const int64_t c = (int64_t)span_of<T>(a, a.lens[seq]).weight * items;
       if (at < seq_at + c) break;
       seq_at += c;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
   const uint32_t ring_u = smem_u32(ring), meta_u = smem_u32(meta);
   const uint32_t lane_off = tile_offset<D>(lane / (D / 16), lane % (D / 16));
 
-  while (at < end) {
+  while (at < end && seq < a.n) {
     Piece p;
     p.seq = seq;
     p.len = a.lens[seq];

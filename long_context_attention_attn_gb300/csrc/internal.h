@@ -158,14 +158,29 @@ struct KeyParts {
 // Parts over all kv heads, at most: three for each SM, so that a part is no
 // more than two thirds of an SM's share of the launch.
 constexpr int kPartsTotal = 3 * 152;
-inline int64_t max_key_parts(int64_t h_kv) { return (kPartsTotal + h_kv - 1) / h_kv; }
-inline size_t key_parts_bytes(int64_t h_kv, int64_t d, int64_t dv) {
-  const size_t n = (size_t)max_key_parts(h_kv);
-  return align_up(256 + 2 * n * sizeof(int4), 256) + align_up(n * h_kv * 128 * (d + dv) * 4, 256);
+// Query tiles that any key tile may see without being cut: what it sees
+// through the window where positions are in order.
+inline int64_t least_cut(const attn_fwd_params& f) { return f.window_left / kTile + 2; }
+// Parts of a problem, at most (0: none are needed or there are too many heads
+// for them to matter).
+inline int64_t max_key_parts(const attn_fwd_params& f) {
+  if (!keeps_tokens(f)) return 0;
+  const int64_t nq = (f.s_q + kTile - 1) / kTile, nk = (f.s_kv + kTile - 1) / kTile;
+  if (nq <= least_cut(f)) return 0;
+  int64_t n = (kPartsTotal + f.h_kv - 1) / f.h_kv;
+  const int64_t most = 2 * f.b * nk * nq / least_cut(f);  // no tile over the cap takes more
+  if (most < n) n = most;
+  return n < 2 ? 0 : n;
 }
-inline KeyParts key_parts(void* ws, int64_t h_kv) {
+inline size_t key_parts_bytes(const attn_fwd_params& f) {
+  const size_t n = (size_t)max_key_parts(f), dv = (size_t)(f.d_v > 0 ? f.d_v : f.d);
+  if (n == 0) return 0;
+  return align_up(256 + 2 * n * sizeof(int4), 256) + align_up(n * f.h_kv * 128 * (f.d + dv) * 4, 256);
+}
+inline KeyParts key_parts(void* ws, const attn_fwd_params& f) {
   char* c = static_cast<char*>(ws);
-  const size_t n = (size_t)max_key_parts(h_kv);
+  const size_t n = (size_t)max_key_parts(f);
+  if (n == 0) return KeyParts{};
   return KeyParts{reinterpret_cast<PartHeader*>(c), reinterpret_cast<int4*>(c + 256),
                   reinterpret_cast<int4*>(c + 256) + n,
                   reinterpret_cast<float*>(c + align_up(256 + 2 * n * sizeof(int4), 256)), (int)n};

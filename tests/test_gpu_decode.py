@@ -289,3 +289,71 @@ def test_prompt_fork_and_decode_together(ga):
         want = paged.decode(paged.np64(qs), *(paged.raw(x) for x in cache[:2]), *(x.cpu().numpy() for x in cache[2:]),
                             table.cpu().numpy(), n, window, sink, 0.09)
         _check(res, want, False)
+
+
+def test_partials_of_many_ctas_with_nan_and_empty_rows(ga):
+    """One long sequence over many CTAs: a NaN key reaches the row's whole result, and a
+    query before the sequence's first token stays empty beside it."""
+    c = _case(2, 2, 4, 1, 64, 64, [5000, 1], seed=12)
+    ro, rl, mag = _want(c, -1, 0, 0.125)
+    out, lse = _run(ga, c, -1, 0, 0.125, out_fp32=True)
+    _check((out, lse), (ro, rl, mag), False)
+    c["k"][int(c["table"][0, 40]), 0, 3, 7] = 0x7f
+    out, lse = _run(ga, c, -1, 0, 0.125, out_fp32=True)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    _check((out[1:], lse[1:]), (ro[1:], rl[1:], mag[1:]), False)
+
+
+def test_tensors_in_place_of_allocations(ga):
+    c = _case(3, 1, 8, 2, 128, 32, [70, 0, 900], seed=13)
+    want = _want(c, -1, 0, 0.09)
+    out = torch.full((3, 1, 8, 128), float("nan"), device=DEV)
+    lse = torch.full((3, 8, 1), float("nan"), device=DEV)
+    f8 = torch.float8_e4m3fn
+    args = [c["q"].to(DEV), c["k"].to(DEV).view(f8), c["v"].to(DEV).view(f8), c["ks"].to(DEV), c["vs"].to(DEV),
+            c["table"].to(DEV), c["lens"].to(DEV)]
+    need = ga.workspace_bytes_decode(*args)
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)
+    got = ga.attn_decode(*args, scale=0.09, out=out, lse=lse, out_fp32=True, workspace=ws)
+    assert got[0] is out and got[1] is lse
+    _check(got, want, False)
+    with pytest.raises(ga.AttnError):
+        ga.attn_decode(*args, scale=0.09, workspace=ws[:need - 256])
+
+
+def test_binding_refusals(ga):
+    f8 = torch.float8_e4m3fn
+    c = _case(2, 1, 8, 2, 64, 16, [40, 3], seed=14)
+    good = dict(q=c["q"].to(DEV), k_cache=c["k"].to(DEV).view(f8), v_cache=c["v"].to(DEV).view(f8),
+                k_scale=c["ks"].to(DEV), v_scale=c["vs"].to(DEV), page_table=c["table"].to(DEV),
+                seqlens=c["lens"].to(DEV))
+    ga.attn_decode(**good)
+    bad = [dict(q=good["q"].half()), dict(q=good["q"][..., :32].contiguous()), dict(q=good["q"].transpose(1, 2)),
+           dict(k_cache=good["k_cache"].view(torch.uint8).short()), dict(v_cache=good["v_cache"][:-1]),
+           dict(k_cache=good["k_cache"].view(torch.uint8).transpose(1, 2).view(f8)),
+           dict(k_scale=good["k_scale"].double()), dict(v_scale=good["v_scale"][:, :1]),
+           dict(page_table=good["page_table"].long()), dict(page_table=good["page_table"][:1]),
+           dict(page_table=good["page_table"][:, ::2]), dict(seqlens=good["seqlens"][:1]),
+           dict(seqlens=good["seqlens"].cpu()), dict(q=good["q"].cpu()), dict(v_scale=good["v_scale"].cpu())]
+    for kw in bad:
+        with pytest.raises((ValueError, RuntimeError)):
+            ga.attn_decode(**{**good, **kw})
+    for kw, code in ((dict(window_left=-2), 1), (dict(sink_tokens=-1), 1), (dict(scale=-1.0), 1)):
+        with pytest.raises(ga.AttnError) as err:
+            ga.attn_decode(**good, **kw)
+        assert err.value.code == code
+    cache = [good[n] for n in ("k_cache", "v_cache", "k_scale", "v_scale")]
+    kv = torch.zeros(2, 1, 2, 64, dtype=torch.bfloat16, device=DEV)
+    start = torch.zeros(2, **INT)
+    before = [t.clone() for t in cache]
+    for args, kw in (((kv.float(), kv), {}), ((kv, kv[:1]), {}), ((kv[:, :, :1], kv[:, :, :1]), {}),
+                     ((kv, kv), dict(start=start[:1])), ((kv, kv), dict(lens=start.long())),
+                     ((kv[:1], kv[:1]), {}), ((kv, kv), dict(tok_start=start.cpu()))):
+        with pytest.raises((ValueError, RuntimeError)):
+            ga.kv_cache_append(*args, *cache, good["page_table"], **{"start": start, **kw})
+    with pytest.raises((ValueError, RuntimeError)):
+        ga.kv_cache_copy_pages(*cache, start, start[:1])
+    torch.cuda.synchronize()
+    for t, u in zip(cache, before):
+        assert torch.equal(t.view(torch.uint8) if t.dtype == f8 else t.nan_to_num(9),
+                           u.view(torch.uint8) if u.dtype == f8 else u.nan_to_num(9))

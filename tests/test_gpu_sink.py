@@ -126,6 +126,19 @@ def test_key_tiles_in_parts_of_packed_kv():
         check_grad(x.cpu(), r, name)
 
 
+def test_many_kv_heads_take_no_parts():
+    """With as many kv heads as parts in all, no key tile is cut."""
+    import long_context_attention_attn_gb300 as ga
+    x = _inputs(1, 400, 460, 460, 64, 64, "one", seed=6)
+    out, lse, grads = _gpu(ga, x, 16, 3, 0.125)
+    ro, _ = A.attn_fwd(x["q"], x["k"], x["v"], x["ids"], x["pos"], x["ids"], x["pos"], 16, 0.125, sink_tokens=3)
+    check_out(out.cpu(), ro)
+    ref = A.attn_bwd(x["q"], x["k"], x["v"], x["dout"], x["ids"], x["pos"], x["ids"], x["pos"], 16, 0.125,
+                     sink_tokens=3)
+    for name, got, want in zip(("dq", "dk", "dv"), grads, ref):
+        check_grad(got.cpu(), want, name)
+
+
 @pytest.mark.parametrize("s,window,sink,packing", [(1500, 100, 4, "one"), (1500, 100, 300, "one"),
                                                    (1300, 20, 5, "packed"), (9000, 1000, 140, "one")])
 def test_tile_plan_covers_the_mask(s, window, sink, packing):
