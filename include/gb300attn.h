@@ -437,7 +437,7 @@ GB300ATTN_API int attn_kv_copy_pages(const attn_kv_cache* cache, const int32_t* 
  *             [n, h_q, s_q]: finished partials that attn_merge_partial takes
  *  workspace  >= attn_decode_workspace_bytes() bytes, 256-byte aligned; no
  *             initialisation needed.  Calls that overlap on the GPU need one
- *             each.
+ *             each.  Where that size is 256 no scratch is used and NULL will do.
  * Results are bit-identical from run to run. */
 typedef struct attn_decode_params {
   attn_kv_cache cache;

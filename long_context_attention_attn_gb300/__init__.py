@@ -606,11 +606,13 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
         else:
             with torch.cuda.device(index):
                 need = lib().attn_decode_workspace_bytes(ref)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        if need > 256:  # (256: the call uses none)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the call's device")
-    p.workspace = workspace.data_ptr()
-    p.workspace_bytes = workspace.nbytes
+    if workspace is not None:
+        p.workspace = workspace.data_ptr()
+        p.workspace_bytes = workspace.nbytes
     _check(_on_device(index, lib().attn_decode, ref), "attn_decode")
     return out, lse
 

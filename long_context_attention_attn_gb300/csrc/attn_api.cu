@@ -521,17 +521,17 @@ static int check_decode(const attn_decode_params* p) {
 size_t attn_decode_workspace_bytes(const attn_decode_params* p) {
   size_t n = 0;
   if (check_decode(p) != ATTN_OK || decode_workspace(*p, &n) != cudaSuccess) return 0;
-  return n;
+  return n > 0 ? n : 256;
 }
 
 int attn_decode(const attn_decode_params* p, attn_stream_t stream) {
   const int rc = check_decode(p);
   if (rc != ATTN_OK) return rc;
   size_t need = 0;
-  if (!p->workspace || !aligned(p->workspace, 256)) return ATTN_ERR_INVALID_ARG;
-  cudaError_t e = decode_workspace(*p, &need);
+  if (!aligned(p->workspace, 256)) return ATTN_ERR_INVALID_ARG;
+  const cudaError_t e = decode_workspace(*p, &need);
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
-  if (p->workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+  if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
   return cuda_status(launch_attn_decode(*p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

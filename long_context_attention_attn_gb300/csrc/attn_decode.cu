@@ -6,12 +6,14 @@
 // group's query heads and the query tokens share each key read as the rows of
 // one small matrix product.
 //
-// Work is cut by keys, not by sequence: the blocks of 32 (16) keys of all (sequence, kv
-// head, row tile) items form one list, and every CTA of a grid that fills the
-// GPU once takes an equal run of it, so ragged batches and single long
-// sequences load every SM alike.  A run that ends inside an item leaves a
-// finished partial (O, lse) in the workspace, and the combine kernel folds an
-// item's partials in their order (the result does not depend on timing).
+// An item is a sequence, a kv head and a tile of its rows.  Small problems give
+// each item a cluster of CTAs that fold their results through shared memory, in
+// one launch.  Others are cut by keys, not by sequence: the blocks of 32 (16)
+// keys of all items form one list, and every CTA of a grid that fills the GPU
+// once takes an equal run of it, so ragged batches and single long sequences
+// load every SM alike.  A run that ends inside an item leaves a finished
+// partial (O, lse) in the workspace, and the combine kernel folds an item's
+// partials in their order (the result does not depend on timing).
 //
 // A CTA's four warps take the blocks of a piece in turn, each with a ring of
 // its own in shared memory, filled by 16-byte asynchronous copies, so that no
@@ -56,7 +58,9 @@ struct DecodeArgs {
   float* part_lse;  // [2 * grid, R] (base 2)
   int64_t page_stride;
   int n, s_q, h_q, h_kv, g, rows, row_tiles, max_pages, page_shift, num_pages;
-  int window, sink, out_fp32, grid;
+  int window, sink, out_fp32;
+  int grid;     // CTAs that share the list
+  int cluster;  // CTAs per item (0: by the list)
   float scale_log2;
 };
 
@@ -78,9 +82,18 @@ struct Tune {
   // Without it the CTAs with many short sequences end last: 243 us for the
   // batch above, 197 us with 16.
   static constexpr int kItemCost = D * NT >= 512 ? 32 : 16;
+  // Most blocks per warp for which an item gets a cluster of its own (up to 8
+  // CTAs, all items at once on the GPU, by the longest sequence that the page
+  // table can hold).  That saves the list, the scratch and the second launch;
+  // the list balances unlike lengths and uses the SMs that clusters leave.  One
+  // sequence, Hkv 8 d 128, us by list / by cluster: Hq 32 at 512 tokens 8.7 /
+  // 6.3, 4096 11.5 / 8.9, 16384 19.6 / 18.5, 32768 29.3 / 31.5; Hq 128 at 4096
+  // 15.1 / 12.8, 8192 16.8 / 16.4, 16384 23.2 / 25.2.
+  static constexpr int kClusterBlocks = (NT == 1 ? 16 : 8) * (D == 64 ? 2 : 1);
 };
 // Shortest run: a shorter one would only add partials to fold.
 constexpr int kMinRun = 16;
+constexpr int kMaxCluster = 8;  // CTAs per item, at most (a size every GPU takes)
 
 // The blocks of keys that some query of a sequence of length `len` may see:
 // first those of the kept tokens, then those from the window's start on.
@@ -201,6 +214,29 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
+}
+
+// Clusters: a barrier of all threads, and loads from another CTA's shared memory.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float load_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 load_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
@@ -332,7 +368,9 @@ struct Cfg {
   static constexpr int bytes = row_off + 2 * R * 4;
   // the ring's room holds the four warps' results at the end of a piece
   static constexpr int kMergeRow = D + 4;
-  static_assert(kWarps * R * (kMergeRow + 3) * 4 <= q_off, "merge buffer");
+  // behind them, with a cluster per item, the CTA's own: [R][D], then [R]
+  static constexpr int fin_off = kWarps * R * (kMergeRow + 3) * 4;
+  static_assert(fin_off % 16 == 0 && fin_off + R * (D + 1) * 4 <= q_off, "merge buffer");
 };
 
 // One piece of work: blocks [t0, t1) of an item.
@@ -342,30 +380,35 @@ struct Piece {
   int len;
 };
 
-template <int D, int NT>
+// CL: one cluster per item, its CTAs taking equal shares of the item's blocks
+// and folding their results through each other's shared memory (no list, no
+// scratch, no second launch); else each CTA takes a run of the list.
+template <int D, int NT, bool CL>
 __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kernel(const DecodeArgs a) {
   using C = Cfg<D, NT>;
   using T = Tune<D, NT>;
   constexpr int kBlock = T::kBlock, kItemCost = T::kItemCost;
   constexpr int MT = kBlock / 16;  // groups of 16 keys
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t before[kThreads + 1];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int n8 = lane >> 2, t4 = lane & 3;
-
-  const Placement pl = place<T>(a, before);
   const int items = a.h_kv * a.row_tiles;  // per sequence
-  const int64_t total = before[kThreads] * items;
-  const int64_t run = run_length(a, total);
-  int64_t at = blockIdx.x * run;
-  const int64_t end = min(at + run, total);
-  if (at >= end) return;
 
-  // the sequence of the run's first block
+  int64_t at = 0, end = 1;  // the run of the list; with CL a single turn
   int seq;
-  int64_t seq_at;  // where it starts in the list
-  {
+  int64_t seq_at = 0;  // where the sequence starts in the list
+  if constexpr (CL) {
+    seq = (int)(blockIdx.x / a.cluster) / items;
+  } else {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ int64_t before[kThreads + 1];
+    const Placement pl = place<T>(a, before);
+    const int64_t total = before[kThreads] * items;
+    const int64_t run = run_length(a, total);
+    at = blockIdx.x * run;
+    end = min(at + run, total);
+    if (at >= end) return;
+    // the sequence of the run's first block
     int t = 0;
 #pragma unroll
     for (int step = kThreads / 2; step > 0; step >>= 1)
@@ -393,6 +436,15 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     p.seq = seq;
     p.len = a.lens[seq];
     p.span = span_of<T>(a, p.len);
+    bool item_done = true;
+    if constexpr (CL) {
+      const int item = (int)(blockIdx.x / a.cluster) % items, rank = blockIdx.x % a.cluster;
+      p.kvh = item / a.row_tiles;
+      p.rt = item % a.row_tiles;
+      p.t0 = (int)((int64_t)p.span.count * rank / a.cluster);
+      p.t1 = (int)((int64_t)p.span.count * (rank + 1) / a.cluster);
+      at = end;
+    } else {
     if (p.span.count == 0) {
       ++seq;
       continue;
@@ -408,12 +460,13 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     p.t0 = max(w0 - kItemCost, 0);
     p.t1 = max(w1 - kItemCost, 0);
     at += w1 - w0;
-    const bool item_done = w1 == weight;
+    item_done = w1 == weight;
     if (item_done && item == items - 1) {
       seq_at += (int64_t)weight * items;
       ++seq;
     }
     if (p.t1 == p.t0) continue;
+    }
 
     // ---- the rows of q: their loads are in flight while the ring fills
     constexpr int kE = D / 32;               // values of a row per lane, neighbours
@@ -815,6 +868,11 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         acc.z *= inv;
         acc.w *= inv;
         const float lse2 = z == 0.f ? -INFINITY : ref + log2f(z);
+        if constexpr (CL) {
+          *reinterpret_cast<float4*>(smem + C::fin_off + (r * D + 4 * d4) * 4) = acc;
+          if (d4 == 0) reinterpret_cast<float*>(smem + C::fin_off + C::R * D * 4)[r] = lse2;
+          continue;
+        }
         if (whole) {
           const int tok = row / a.g, head = p.kvh * a.g + row % a.g;
           const int64_t orow = ((int64_t)p.seq * a.s_q + tok) * a.h_q + head;
@@ -830,7 +888,52 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         }
       }
     }
-    __syncthreads();  // the ring, q and the row values are free again
+    if constexpr (CL) {
+      // every CTA folds its share of the rows from all of the cluster
+      cluster_barrier();
+      const uint32_t fin = smem_u32(smem) + C::fin_off;
+      constexpr int kVec = D / 4;
+      for (int u = (int)(blockIdx.x % a.cluster) * kThreads + threadIdx.x; u < C::R * kVec;
+           u += a.cluster * kThreads) {
+        const int r = u / kVec, d4 = u % kVec;
+        const int row = p.rt * C::R + r;
+        if (row >= a.rows) break;
+        float lses[kMaxCluster], top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          lses[c] = c < a.cluster ? load_cluster(cluster_address(fin + (C::R * D + r) * 4, c)) : -INFINITY;
+          top = fmaxf(top, lses[c]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top;
+        float z = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) {
+          if (c >= a.cluster) break;
+          const float f = ex2(lses[c] - ref);
+          const float4 v = load_cluster4(cluster_address(fin + (r * D + 4 * d4) * 4, c));
+          z += f;
+          acc.x += v.x * f;
+          acc.y += v.y * f;
+          acc.z += v.z * f;
+          acc.w += v.w * f;
+        }
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+        const int tok = row / a.g, head = p.kvh * a.g + row % a.g;
+        const int64_t orow = ((int64_t)p.seq * a.s_q + tok) * a.h_q + head;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (a.out_fp32)
+          reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = acc;
+        else
+          reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
+              make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
+        if (d4 == 0)
+          a.lse[((int64_t)p.seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (ref + log2f(z)) * kLn2;
+      }
+      cluster_barrier();  // nobody leaves while its results are read
+    } else {
+      __syncthreads();  // the ring, q and the row values are free again
+    }
   }
 }
 
@@ -931,11 +1034,18 @@ int n_tiles(int64_t d, int64_t rows) {
   return need < most ? need : most;
 }
 
+// How a problem is launched: a cluster of `cluster` CTAs per item, or (0) `grid`
+// CTAs over the list.
+struct Shape {
+  int grid, cluster;
+};
+
 template <int D, int NT>
 struct Kernel {
   using C = Cfg<D, NT>;
+  using T = Tune<D, NT>;
   // CTAs that fill the device once
-  static cudaError_t grid(int* n) {
+  static cudaError_t resident(int* n) {
     static std::atomic<int> cache[kMaxDevices];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -943,43 +1053,70 @@ struct Kernel {
     const bool cached = dev >= 0 && dev < kMaxDevices;
     *n = cached ? cache[dev].load(std::memory_order_acquire) : 0;
     if (*n > 0) return cudaSuccess;
-    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes);
+    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::bytes);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::bytes);
     int per_sm = 0;
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_decode_kernel<D, NT>, kThreads, C::bytes);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_decode_kernel<D, NT, false>, kThreads,
+                                                        C::bytes);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     *n = per_sm * sm_count();
     if (cached) cache[dev].store(*n, std::memory_order_release);
     return cudaSuccess;
   }
-  // CTAs of a launch: no more than shortest runs of the longest sequences that the
-  // page table can hold
-  static cudaError_t grid_for(const attn_decode_params& p, int64_t row_tiles, int* n) {
-    const cudaError_t e = grid(n);
-    using T = Tune<D, NT>;
-    const int64_t blocks = (p.max_pages * p.cache.page_size + T::kBlock - 1) / T::kBlock + T::kItemCost;
-    const int64_t items = p.n * p.cache.h_kv * row_tiles;
-    const int64_t most = (blocks * items + kMinRun - 1) / kMinRun;
-    if (most < *n) *n = (int)most;
-    return e;
-  }
-  static cudaError_t launch(DecodeArgs& a, int n, cudaStream_t st) {
-    a.grid = n;
-    a.part_lse = a.part_o + (int64_t)2 * n * C::R * D;
-    cudaError_t e;
-    attn_decode_kernel<D, NT><<<n, kThreads, C::bytes, st>>>(a);
-    e = cudaGetLastError();
+  static cudaError_t shape(const attn_decode_params& p, int64_t row_tiles, Shape* s) {
+    int n = 0;
+    const cudaError_t e = resident(&n);
     if (e != cudaSuccess) return e;
+    // blocks of the longest sequence that the page table can hold, as far as the
+    // window and the kept tokens reach (which may begin and end inside blocks)
+    int64_t blocks = (p.max_pages * p.cache.page_size + T::kBlock - 1) / T::kBlock;
+    if (p.window_left >= 0) {
+      const int64_t seen = (p.window_left + p.s_q) / T::kBlock + 2 + (p.sink_tokens + T::kBlock - 1) / T::kBlock;
+      if (seen < blocks) blocks = seen;
+    }
+    const int64_t items = p.n * p.cache.h_kv * row_tiles;
+    s->cluster = 0;
+    for (int c = kMaxCluster; c > 1; c /= 2)
+      if (items * c <= n && blocks <= (int64_t)c * kWarps * T::kClusterBlocks) {
+        s->cluster = c;
+        break;
+      }
+    // no more than shortest runs
+    const int64_t most = ((blocks + T::kItemCost) * items + kMinRun - 1) / kMinRun;
+    s->grid = most < n ? (int)most : n;
+    return cudaSuccess;
+  }
+  static cudaError_t launch(DecodeArgs& a, const Shape& sh, cudaStream_t st) {
+    a.grid = sh.grid;
+    a.cluster = sh.cluster;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.n * a.h_kv * a.row_tiles), C::R / kFoldRows<D, NT>);
-    cfg.blockDim = dim3(kFoldThreads);
-    cfg.stream = st;
     cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    const int64_t items = (int64_t)a.n * a.h_kv * a.row_tiles;
+    if (sh.cluster) {
+      cfg.gridDim = dim3((unsigned)(items * sh.cluster));
+      cfg.blockDim = dim3(kThreads);
+      cfg.dynamicSmemBytes = C::bytes;
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = sh.cluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NT, true>, a);
+    }
+    a.part_lse = a.part_o + (int64_t)2 * sh.grid * C::R * D;
+    attn_decode_kernel<D, NT, false><<<sh.grid, kThreads, C::bytes, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3((unsigned)items, C::R / kFoldRows<D, NT>);
+    cfg.blockDim = dim3(kFoldThreads);
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, attn_decode_combine_kernel<D, NT>, a);
   }
 };
@@ -1006,9 +1143,9 @@ cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes) {
   const int64_t d = p.cache.d, rows = p.s_q * (p.h_q / p.cache.h_kv);
   const int nt = n_tiles(d, rows);
   return dispatch(d, nt, [&](auto k) {
-    int n = 0;
-    const cudaError_t e = k.grid_for(p, (rows + nt * 8 - 1) / (nt * 8), &n);
-    *bytes = align_up((size_t)2 * n * nt * 8 * (d + 1) * 4, 256);
+    Shape sh;
+    const cudaError_t e = k.shape(p, (rows + nt * 8 - 1) / (nt * 8), &sh);
+    *bytes = sh.cluster ? 0 : align_up((size_t)2 * sh.grid * nt * 8 * (d + 1) * 4, 256);
     return e;
   });
 }
@@ -1043,9 +1180,9 @@ cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
   a.out_fp32 = p.out_fp32 ? 1 : 0;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   return dispatch(c.d, nt, [&](auto k) {
-    int n = 0;
-    const cudaError_t e = k.grid_for(p, a.row_tiles, &n);
-    return e == cudaSuccess ? k.launch(a, n, st) : e;
+    Shape sh;
+    const cudaError_t e = k.shape(p, a.row_tiles, &sh);
+    return e == cudaSuccess ? k.launch(a, sh, st) : e;
   });
 }
 

@@ -94,20 +94,29 @@ CASES = [
 ]
 
 
+def _wide(c, size, keys=1 << 18):
+    """The same with a table for 256k tokens: the work is then cut by the list of blocks, not
+    given to a cluster of CTAs per item."""
+    more = torch.full((c["table"].shape[0], keys // size - c["table"].shape[1]), -1, dtype=torch.int32)
+    return dict(c, table=torch.cat([c["table"], more], 1))
+
+
 @pytest.mark.parametrize("n,sq,hq,hkv,d,size,lens,window,sink", CASES)
-@pytest.mark.parametrize("bf16", [False, True])
-def test_decode(ga, n, sq, hq, hkv, d, size, lens, window, sink, bf16):
+@pytest.mark.parametrize("bf16,wide", [(False, False), (True, False), (False, True)])
+def test_decode(ga, n, sq, hq, hkv, d, size, lens, window, sink, bf16, wide):
     c = _case(n, sq, hq, hkv, d, size, lens, seed=d + sq)
-    got = _run(ga, c, window, sink, d ** -0.5, out_fp32=not bf16)
+    got = _run(ga, _wide(c, size) if wide else c, window, sink, d ** -0.5, out_fp32=not bf16)
     _check(got, _want(c, window, sink, d ** -0.5), bf16)
 
 
-def test_pages_that_are_none(ga):
+@pytest.mark.parametrize("wide", [False, True])
+def test_pages_that_are_none(ga, wide):
     """Entries outside the pool hide their tokens, whole sequences among them."""
     c = _case(3, 2, 4, 2, 64, 32, [300, 200, 64], seed=1)
     c["table"][0, 1], c["table"][0, 4], c["table"][0, 9] = -1, 1 << 30, -(1 << 31)
     c["table"][2, :] = 10 ** 6
-    _check(_run(ga, c, -1, 0, 0.125, out_fp32=True), _want(c, -1, 0, 0.125), False)
+    want = _want(c, -1, 0, 0.125)
+    _check(_run(ga, _wide(c, 32) if wide else c, -1, 0, 0.125, out_fp32=True), want, False)
 
 
 def test_pages_behind_the_window_are_not_needed(ga):
@@ -126,28 +135,31 @@ def test_length_behind_the_table(ga):
     _check(_run(ga, c, 50, 3, 0.125, out_fp32=True), _want(c, 50, 3, 0.125), False)
 
 
-def test_nan_of_a_later_token_stays_there(ga):
+@pytest.mark.parametrize("wide", [False, True])
+def test_nan_of_a_later_token_stays_there(ga, wide):
     """A NaN in a drafted token's V reaches the queries that see it and no others."""
     c = _case(1, 4, 4, 1, 128, 64, [200], seed=4)
     want = _want(c, -1, 0, 0.1)
     pid = int(c["table"][0, 198 // 64])
     c["v"][pid, 0, 198 % 64, 5] = 0x7f
     c["k"][int(c["table"][0, 199 // 64]), 0, 199 % 64, 3] = 0xff
-    out, lse = _run(ga, c, -1, 0, 0.1, out_fp32=True)
+    out, lse = _run(ga, _wide(c, 64) if wide else c, -1, 0, 0.1, out_fp32=True)
     ro, rl, mag = want
     _check((out[:, :2], lse[:, :, :2]), (ro[:, :2], rl[:, :, :2], mag[:, :2]), False)
     assert torch.isnan(out[:, 2, :, 5]).all() and not torch.isnan(out[:, 2, :, 6]).any()
     assert torch.isnan(out[:, 3]).all() and torch.isnan(lse[:, :, 3]).all()
 
 
-def test_scales_far_apart(ga):
+@pytest.mark.parametrize("wide", [False, True])
+def test_scales_far_apart(ga, wide):
     """Pages of V from 2^-40 to 2^40 and of K that raise the maximum late."""
     c = _case(1, 1, 8, 1, 128, 16, [600], seed=5)
     n = 600 // 16 + 1
     ids = c["table"][0, :n].long()
     c["vs"][ids, 0] = torch.exp2(torch.linspace(-40, 40, n).round())
     c["ks"][ids, 0] *= torch.exp2(torch.linspace(-3, 2, n).round())
-    _check(_run(ga, c, -1, 0, 0.088, out_fp32=True), _want(c, -1, 0, 0.088), False)
+    want = _want(c, -1, 0, 0.088)
+    _check(_run(ga, _wide(c, 16) if wide else c, -1, 0, 0.088, out_fp32=True), want, False)
 
 
 def test_zero_scales_and_large_queries(ga):
@@ -291,11 +303,13 @@ def test_prompt_fork_and_decode_together(ga):
         _check(res, want, False)
 
 
-def test_partials_of_many_ctas_with_nan_and_empty_rows(ga):
+@pytest.mark.parametrize("wide", [False, True])
+def test_partials_of_many_ctas_with_nan_and_empty_rows(ga, wide):
     """One long sequence over many CTAs: a NaN key reaches the row's whole result, and a
     query before the sequence's first token stays empty beside it."""
     c = _case(2, 2, 4, 1, 64, 64, [5000, 1], seed=12)
     ro, rl, mag = _want(c, -1, 0, 0.125)
+    c = _wide(c, 64) if wide else c
     out, lse = _run(ga, c, -1, 0, 0.125, out_fp32=True)
     _check((out, lse), (ro, rl, mag), False)
     c["k"][int(c["table"][0, 40]), 0, 3, 7] = 0x7f
@@ -307,6 +321,7 @@ def test_partials_of_many_ctas_with_nan_and_empty_rows(ga):
 def test_tensors_in_place_of_allocations(ga):
     c = _case(3, 1, 8, 2, 128, 32, [70, 0, 900], seed=13)
     want = _want(c, -1, 0, 0.09)
+    c = _wide(c, 32)  # (small problems take no scratch)
     out = torch.full((3, 1, 8, 128), float("nan"), device=DEV)
     lse = torch.full((3, 8, 1), float("nan"), device=DEV)
     f8 = torch.float8_e4m3fn
@@ -317,6 +332,7 @@ def test_tensors_in_place_of_allocations(ga):
     got = ga.attn_decode(*args, scale=0.09, out=out, lse=lse, out_fp32=True, workspace=ws)
     assert got[0] is out and got[1] is lse
     _check(got, want, False)
+    assert need > 256
     with pytest.raises(ga.AttnError):
         ga.attn_decode(*args, scale=0.09, workspace=ws[:need - 256])
 

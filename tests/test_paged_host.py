@@ -90,7 +90,7 @@ def test_append_refusals(ga, kw, code):
     (dict(q=A + 8), 1), (dict(out=A + 8), 1), (dict(n=0), 1), (dict(n=65536), 2), (dict(s_q=0), 1), (dict(h_q=7), 1),
     (dict(h_q=0), 1), (dict(window_left=-2), 1), (dict(sink_tokens=-1), 1), (dict(sink_tokens=1 << 31), 2),
     (dict(scale=0.0), 1), (dict(scale=float("inf")), 1), (dict(s_q=300), 2), (dict(s_q=1025, h_q=2), 2),
-    (dict(max_pages=(1 << 24) + 1), 2), (dict(workspace=None), 1), (dict(workspace=10 * A + 128), 1),
+    (dict(max_pages=(1 << 24) + 1), 2), (dict(workspace=10 * A + 128), 1),
 ])
 def test_decode_refusals(ga, kw, code):
     assert _decode(ga, **kw) == code
