@@ -54,12 +54,12 @@ struct DecodeArgs {
   const int* lens;
   void* out;
   float* lse;
-  float* part_o;    // [2 * grid, R, D]
-  float* part_lse;  // [2 * grid, R] (base 2)
+  float* part_o;    // [2 * runs * row_tiles, R, D]
+  float* part_lse;  // [2 * runs * row_tiles, R] (base 2)
   int64_t page_stride;
   int n, s_q, h_q, h_kv, g, rows, row_tiles, max_pages, page_shift, num_pages;
   int window, sink, out_fp32;
-  int grid;     // CTAs that share the list
+  int runs;     // of the list; row_tiles CTAs take each
   int cluster;  // CTAs per item (0: by the list)
   float scale_log2;
 };
@@ -89,7 +89,7 @@ struct Tune {
   // sequence, Hkv 8 d 128, us by list / by cluster: Hq 32 at 512 tokens 8.7 /
   // 6.3, 4096 11.5 / 8.9, 16384 19.6 / 18.5, 32768 29.3 / 31.5; Hq 128 at 4096
   // 15.1 / 12.8, 8192 16.8 / 16.4, 16384 23.2 / 25.2.
-  static constexpr int kClusterBlocks = (NT == 1 ? 16 : 8) * (D == 64 ? 2 : 1);
+  static constexpr int kClusterBlocks = (NT == 1 ? 16 : NT == 2 ? 8 : 0) * (D == 64 ? 2 : 1);
 };
 // Shortest run: a shorter one would only add partials to fold.
 constexpr int kMinRun = 16;
@@ -159,7 +159,7 @@ __device__ __forceinline__ Placement place(const DecodeArgs& a, int64_t* before)
 
 // Weight per CTA: an equal share of the list, and no less than kMinRun.
 __device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total) {
-  return max((total + a.grid - 1) / a.grid, (int64_t)kMinRun);
+  return max((total + a.runs - 1) / a.runs, (int64_t)kMinRun);
 }
 
 // ---------------------------------------------------------------- primitives
@@ -392,32 +392,31 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
   const int n8 = lane >> 2, t4 = lane & 3;
-  const int items = a.h_kv * a.row_tiles;  // per sequence
 
   int64_t at = 0, end = 1;  // the run of the list; with CL a single turn
   int seq;
   int64_t seq_at = 0;  // where the sequence starts in the list
   if constexpr (CL) {
-    seq = (int)(blockIdx.x / a.cluster) / items;
+    seq = (int)(blockIdx.x / a.cluster) / (a.h_kv * a.row_tiles);
   } else {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __shared__ int64_t before[kThreads + 1];
     const Placement pl = place<T>(a, before);
-    const int64_t total = before[kThreads] * items;
+    const int64_t total = before[kThreads] * a.h_kv;
     const int64_t run = run_length(a, total);
-    at = blockIdx.x * run;
+    at = blockIdx.x / a.row_tiles * run;
     end = min(at + run, total);
     if (at >= end) return;
     // the sequence of the run's first block
     int t = 0;
 #pragma unroll
     for (int step = kThreads / 2; step > 0; step >>= 1)
-      if (before[t + step] * items <= at) t += step;
+      if (before[t + step] * a.h_kv <= at) t += step;
     // (entries behind the last sequence repeat the total, which is above `at`)
     seq = t * pl.per;
-    seq_at = before[t] * items;
+    seq_at = before[t] * a.h_kv;
     for (; seq < a.n - 1; ++seq) {
-      const int64_t c = (int64_t)span_of<T>(a, a.lens[seq]).weight * items;
+      const int64_t c = (int64_t)span_of<T>(a, a.lens[seq]).weight * a.h_kv;
       if (at < seq_at + c) break;
       seq_at += c;
     }
@@ -438,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     p.span = span_of<T>(a, p.len);
     bool item_done = true;
     if constexpr (CL) {
-      const int item = (int)(blockIdx.x / a.cluster) % items, rank = blockIdx.x % a.cluster;
+      const int item = (int)(blockIdx.x / a.cluster) % (a.h_kv * a.row_tiles), rank = blockIdx.x % a.cluster;
       p.kvh = item / a.row_tiles;
       p.rt = item % a.row_tiles;
       p.t0 = (int)((int64_t)p.span.count * rank / a.cluster);
@@ -452,17 +451,16 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     // the piece [w0, w1) of the item's weight: its first kItemCost hold no block
     const int64_t in_seq = at - seq_at;
     const int weight = p.span.weight;
-    const int item = (int)(in_seq / weight);
-    p.kvh = item / a.row_tiles;
-    p.rt = item % a.row_tiles;
-    const int w0 = (int)(in_seq - (int64_t)item * weight);
+    p.kvh = (int)(in_seq / weight);
+    p.rt = blockIdx.x % a.row_tiles;
+    const int w0 = (int)(in_seq - (int64_t)p.kvh * weight);
     const int w1 = (int)min((int64_t)weight, w0 + (end - at));
     p.t0 = max(w0 - kItemCost, 0);
     p.t1 = max(w1 - kItemCost, 0);
     at += w1 - w0;
     item_done = w1 == weight;
-    if (item_done && item == items - 1) {
-      seq_at += (int64_t)weight * items;
+    if (item_done && p.kvh == a.h_kv - 1) {
+      seq_at += (int64_t)weight * a.h_kv;
       ++seq;
     }
     if (p.t1 == p.t0) continue;
@@ -950,21 +948,20 @@ __global__ void __launch_bounds__(kFoldThreads) attn_decode_combine_kernel(const
   constexpr int R = NT * 8, RP = kFoldRows<D, NT>, kVec = D / 4;
   __shared__ int64_t before[kThreads + 1];
   const Placement pl = place<T>(a, before);
-  const int items = a.h_kv * a.row_tiles;
-  const int seq = blockIdx.x / items, item = blockIdx.x % items;
-  const int64_t total = before[kThreads] * items;
+  const int rt = blockIdx.x % a.row_tiles, kvh = blockIdx.x / a.row_tiles % a.h_kv;
+  const int seq = blockIdx.x / (a.row_tiles * a.h_kv);
+  const int64_t total = before[kThreads] * a.h_kv;
   const int64_t run = run_length(a, total);
   const int t = seq / pl.per;
   int64_t seq_at = before[t];
   for (int i = t * pl.per; i < seq; ++i) seq_at += span_of<T>(a, a.lens[i]).weight;
   const Span sp = span_of<T>(a, a.lens[seq]);
   const int count = sp.count;
-  const int64_t s0 = seq_at * items + (int64_t)item * sp.weight + T::kItemCost;  // the item's blocks: [s0, s0 + count)
+  const int64_t s0 = seq_at * a.h_kv + (int64_t)kvh * sp.weight + T::kItemCost;  // the item's blocks: [s0, s0 + count)
   const int64_t c0 = count ? s0 / run : 0, c1 = count ? (s0 + count - 1) / run : 0;
   // every CTA waits, so that this grid never ends before the one it depends on
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (count && c0 == c1) return;  // written whole
-  const int kvh = item / a.row_tiles, rt = item % a.row_tiles;
   // The weights of up to kMost pieces at a time through shared memory, then
   // their rows, several loads in flight; later batches of pieces rescale.
   constexpr int kMost = 32;
@@ -980,7 +977,7 @@ __global__ void __launch_bounds__(kFoldThreads) attn_decode_combine_kernel(const
   for (int64_t b0 = c0; count && b0 <= c1; b0 += kMost) {
     const int np = (int)min((int64_t)kMost, c1 - b0 + 1);
     // only the first piece can be a CTA's last one (it starts at the item's start)
-    auto slot = [&](int i) { return 2 * (b0 + i) + ((b0 + i) * run <= s0 ? 1 : 0); };
+    auto slot = [&](int i) { return 2 * ((b0 + i) * a.row_tiles + rt) + ((b0 + i) * run <= s0 ? 1 : 0); };
     for (int u = threadIdx.x; u < np * RP; u += kFoldThreads)
       s_w[u / RP][u % RP] = a.part_lse[slot(u / RP) * R + r0 + u % RP];
     __syncthreads();
@@ -1026,18 +1023,10 @@ __global__ void __launch_bounds__(kFoldThreads) attn_decode_combine_kernel(const
     a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (s_ref[r] + log2f(z)) * kLn2;
 }
 
-// N tiles of 8 rows per CTA: the fewest that hold the rows, up to what the
-// registers allow for the accumulators (D * NT <= 512 values per row tile).
-int n_tiles(int64_t d, int64_t rows) {
-  const int most = d == 256 ? 2 : 4;
-  const int need = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-  return need < most ? need : most;
-}
-
-// How a problem is launched: a cluster of `cluster` CTAs per item, or (0) `grid`
-// CTAs over the list.
+// How a problem is launched: a cluster of `cluster` CTAs per item, or (0) `runs`
+// runs of the list.
 struct Shape {
-  int grid, cluster;
+  int row_tiles, runs, cluster;
 };
 
 template <int D, int NT>
@@ -1053,11 +1042,13 @@ struct Kernel {
     const bool cached = dev >= 0 && dev < kMaxDevices;
     *n = cached ? cache[dev].load(std::memory_order_acquire) : 0;
     if (*n > 0) return cudaSuccess;
-    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              C::bytes);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               C::bytes);
+    if constexpr (T::kClusterBlocks > 0) {
+      if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 C::bytes);
+    }
     int per_sm = 0;
     if (e == cudaSuccess)
       e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_decode_kernel<D, NT, false>, kThreads,
@@ -1068,7 +1059,9 @@ struct Kernel {
     if (cached) cache[dev].store(*n, std::memory_order_release);
     return cudaSuccess;
   }
-  static cudaError_t shape(const attn_decode_params& p, int64_t row_tiles, Shape* s) {
+  static cudaError_t shape(const attn_decode_params& p, Shape* s) {
+    const int64_t row_tiles = (p.s_q * (p.h_q / p.cache.h_kv) + C::R - 1) / C::R;
+    s->row_tiles = (int)row_tiles;
     int n = 0;
     const cudaError_t e = resident(&n);
     if (e != cudaSuccess) return e;
@@ -1087,12 +1080,14 @@ struct Kernel {
         break;
       }
     // no more than shortest runs
-    const int64_t most = ((blocks + T::kItemCost) * items + kMinRun - 1) / kMinRun;
-    s->grid = most < n ? (int)most : n;
+    const int64_t most = ((blocks + T::kItemCost) * p.n * p.cache.h_kv + kMinRun - 1) / kMinRun;
+    const int64_t runs = n / row_tiles > 1 ? n / row_tiles : 1;
+    s->runs = most < runs ? (int)most : (int)runs;
     return cudaSuccess;
   }
   static cudaError_t launch(DecodeArgs& a, const Shape& sh, cudaStream_t st) {
-    a.grid = sh.grid;
+    a.row_tiles = sh.row_tiles;
+    a.runs = sh.runs;
     a.cluster = sh.cluster;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute at[1];
@@ -1100,17 +1095,20 @@ struct Kernel {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     const int64_t items = (int64_t)a.n * a.h_kv * a.row_tiles;
-    if (sh.cluster) {
-      cfg.gridDim = dim3((unsigned)(items * sh.cluster));
-      cfg.blockDim = dim3(kThreads);
-      cfg.dynamicSmemBytes = C::bytes;
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = sh.cluster;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NT, true>, a);
+    if constexpr (T::kClusterBlocks > 0) {
+      if (sh.cluster) {
+        cfg.gridDim = dim3((unsigned)(items * sh.cluster));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = C::bytes;
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = sh.cluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        return cudaLaunchKernelEx(&cfg, attn_decode_kernel<D, NT, true>, a);
+      }
     }
-    a.part_lse = a.part_o + (int64_t)2 * sh.grid * C::R * D;
-    attn_decode_kernel<D, NT, false><<<sh.grid, kThreads, C::bytes, st>>>(a);
+    const int grid = sh.runs * a.row_tiles;
+    a.part_lse = a.part_o + (int64_t)2 * grid * C::R * D;
+    attn_decode_kernel<D, NT, false><<<grid, kThreads, C::bytes, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)items, C::R / kFoldRows<D, NT>);
@@ -1121,38 +1119,51 @@ struct Kernel {
   }
 };
 
+// f(kernel, shape) with 8 or 16 rows per CTA, and 32 where there are more rows
+// than 16 and the list cuts the work: a CTA then widens each code for twice the
+// rows (Hkv 8 d 128, 48 sequences of 100 to 12000 tokens, 64 rows: 301 us against
+// 332), while clusters do better with twice the CTAs (one sequence of 4096
+// tokens, 64 rows: 15.3 us against 20.2).  At d = 256 the registers end at 16.
+template <int D, typename F>
+cudaError_t with_rows(const attn_decode_params& p, F&& f) {
+  auto use = [&](auto k) {
+    Shape sh;
+    const cudaError_t e = k.shape(p, &sh);
+    return e == cudaSuccess ? f(k, sh) : e;
+  };
+  const int64_t rows = p.s_q * (p.h_q / p.cache.h_kv);
+  if (rows <= 8) return use(Kernel<D, 1>());
+  if constexpr (D < 256) {
+    if (rows > 16) {
+      Shape sh;
+      const cudaError_t e = Kernel<D, 2>::shape(p, &sh);
+      if (e != cudaSuccess) return e;
+      if (!sh.cluster) return use(Kernel<D, 4>());
+    }
+  }
+  return use(Kernel<D, 2>());
+}
+
 template <typename F>
-cudaError_t dispatch(int64_t d, int nt, F&& f) {
-  if (d == 64) {
-    if (nt == 1) return f(Kernel<64, 1>());
-    if (nt == 2) return f(Kernel<64, 2>());
-    return f(Kernel<64, 4>());
-  }
-  if (d == 128) {
-    if (nt == 1) return f(Kernel<128, 1>());
-    if (nt == 2) return f(Kernel<128, 2>());
-    return f(Kernel<128, 4>());
-  }
-  if (nt == 1) return f(Kernel<256, 1>());
-  return f(Kernel<256, 2>());
+cudaError_t dispatch(const attn_decode_params& p, F&& f) {
+  if (p.cache.d == 64) return with_rows<64>(p, f);
+  if (p.cache.d == 128) return with_rows<128>(p, f);
+  return with_rows<256>(p, f);
 }
 
 }  // namespace
 
 cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes) {
-  const int64_t d = p.cache.d, rows = p.s_q * (p.h_q / p.cache.h_kv);
-  const int nt = n_tiles(d, rows);
-  return dispatch(d, nt, [&](auto k) {
-    Shape sh;
-    const cudaError_t e = k.shape(p, (rows + nt * 8 - 1) / (nt * 8), &sh);
-    *bytes = sh.cluster ? 0 : align_up((size_t)2 * sh.grid * nt * 8 * (d + 1) * 4, 256);
-    return e;
+  return dispatch(p, [&](auto k, const Shape& sh) {
+    const size_t rows = (size_t)sh.runs * sh.row_tiles * decltype(k)::C::R;
+    *bytes = sh.cluster ? 0 : align_up(2 * rows * (p.cache.d + 1) * 4, 256);
+    return cudaSuccess;
   });
 }
 
 cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
   const attn_kv_cache& c = p.cache;
-  DecodeArgs a;
+  DecodeArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(p.q);
   a.k = static_cast<const uint8_t*>(c.k);
   a.v = static_cast<const uint8_t*>(c.v);
@@ -1170,8 +1181,6 @@ cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
   a.h_kv = (int)c.h_kv;
   a.g = (int)(p.h_q / c.h_kv);
   a.rows = a.s_q * a.g;
-  const int nt = n_tiles(c.d, a.rows);
-  a.row_tiles = (a.rows + nt * 8 - 1) / (nt * 8);
   a.max_pages = (int)p.max_pages;
   a.page_shift = c.page_size == 16 ? 4 : c.page_size == 32 ? 5 : c.page_size == 64 ? 6 : 7;
   a.num_pages = (int)c.num_pages;
@@ -1179,11 +1188,7 @@ cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
   a.sink = (int)p.sink_tokens;
   a.out_fp32 = p.out_fp32 ? 1 : 0;
   a.scale_log2 = p.scale * 1.4426950408889634f;
-  return dispatch(c.d, nt, [&](auto k) {
-    Shape sh;
-    const cudaError_t e = k.shape(p, a.row_tiles, &sh);
-    return e == cudaSuccess ? k.launch(a, sh, st) : e;
-  });
+  return dispatch(p, [&](auto k, const Shape& sh) { return k.launch(a, sh, st); });
 }
 
 }  // namespace gb300
