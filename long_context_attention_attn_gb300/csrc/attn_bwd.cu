@@ -512,8 +512,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_in = key < a.s_kv;
     const int ik = key_in ? a.kv_ids[(int64_t)bi * a.s_kv + key] : 0;
     const int pk = key_in ? a.kv_pos[(int64_t)bi * a.s_kv + key] : 0;
-    // KEEP: the farthest query that sees this key (no branch per pair: a warp's keys differ)
-    const int reach = KEEP && pk < a.sink ? 0x7fffffff : a.window;
+    // KEEP: how far behind a query this key may lie (no branch per pair: a warp's
+    // keys differ; a key behind its query, as an unsigned difference, is out of reach)
+    const uint32_t reach = KEEP && pk < a.sink ? 0x7fffffffu : (uint32_t)a.window;
+    const bool key_ok = ik != 0;
     const float sl2 = a.scale_log2;
     uint8_t* ds_smem = smem + L::ds_off + w * L::kChunk + kr * 128;
     constexpr int kHalf = D / 2;         // dQ columns read back by this half
@@ -557,11 +559,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int qa[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            bool vis = (ia[u] == ik) && (ik != 0) && (pk <= qa[u]);
-            if constexpr (KEEP)
-              vis = vis & (qa[u] - pk <= reach);
-            else if (a.window >= 0)
-              vis = vis && (qa[u] - pk <= a.window);
+            bool vis;
+            if constexpr (KEEP) {
+              vis = key_ok & (ia[u] == ik) & ((uint32_t)(qa[u] - pk) <= reach);
+            } else {
+              vis = (ia[u] == ik) && (ik != 0) && (pk <= qa[u]);
+              if (a.window >= 0) vis = vis && (qa[u] - pk <= a.window);
+            }
             if (!vis) p[4 * c + u] = 0.f;
           }
         }

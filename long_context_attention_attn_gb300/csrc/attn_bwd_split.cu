@@ -97,11 +97,13 @@ struct SplitArgs {
 // because the keys or rows of a warp differ)
 template <bool KEEP>
 __device__ __forceinline__ bool visible(int iq, int pq, int ik, int pk, int window, int sink) {
+  if constexpr (KEEP) {
+    // a key behind its query, as an unsigned difference, is out of reach
+    const uint32_t reach = pk < sink ? 0x7fffffffu : (uint32_t)window;
+    return (iq == ik) & (iq != 0) & ((uint32_t)(pq - pk) <= reach);
+  }
   bool v = (iq == ik) && (iq != 0) && (pk <= pq);
-  if constexpr (KEEP)
-    v = v & ((pq - pk <= window) | (pk < sink));
-  else if (window >= 0)
-    v = v && (pq - pk <= window);
+  if (window >= 0) v = v && (pq - pk <= window);
   return v;
 }
 

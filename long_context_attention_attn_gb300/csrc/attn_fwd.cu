@@ -458,11 +458,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int pka[4] = {pk4.x, pk4.y, pk4.z, pk4.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-              bool vis = (ika[u] == iq) && (iq != 0) && (pka[u] <= pq);
-              if constexpr (KEEP)  // (no branch per pair: the rows of a warp differ)
-                vis = vis & ((pq - pka[u] <= a.window) | (pka[u] < a.sink));
-              else if (a.window >= 0)
-                vis = vis && (pq - pka[u] <= a.window);
+              bool vis;
+              if constexpr (KEEP) {
+                // no branch per pair (the rows of a warp differ); a key behind its
+                // query, as an unsigned difference, is out of reach
+                const uint32_t reach = pka[u] < a.sink ? 0x7fffffffu : (uint32_t)a.window;
+                vis = (ika[u] == iq) & (iq != 0) & ((uint32_t)(pq - pka[u]) <= reach);
+              } else {
+                vis = (ika[u] == iq) && (iq != 0) && (pka[u] <= pq);
+                if (a.window >= 0) vis = vis && (pq - pka[u] <= a.window);
+              }
               if (!vis) sr[4 * c + u] = __float_as_uint(-INFINITY);
             }
           }
