@@ -354,8 +354,9 @@ GB300ATTN_API int attn_fwd_noalloc_status(attn_stream_t stream);
  *  k_scale, v_scale  fp32 [num_pages, h_kv], contiguous, finite and >= 0
  *  page_size  16, 32, 64 or 128;  d  64, 128 or 256
  *  page_stride  bytes between consecutive pages of k and of v, 0 = contiguous;
- *             else >= h_kv * page_size * d and a multiple of 16 (k and v may
- *             be the halves of one [num_pages, 2, h_kv, page_size, d] buffer)
+ *             else >= h_kv * page_size * d, a multiple of 16 and <= 2^32 (k and
+ *             v may be the halves of one [num_pages, 2, h_kv, page_size, d]
+ *             buffer)
  *  k, v 16-byte aligned, scales 4-byte aligned; num_pages <= 2^31 - 1.
  * A page table is int32 [n, max_pages]: entry (i, j) is the page that holds
  * tokens j * page_size .. of sequence i.  An entry outside [0, num_pages) is
@@ -389,8 +390,8 @@ typedef struct attn_kv_cache {
  *           max(old scale, need),
  *   the codes of the slots before the new tokens become
  *           e4m3(code * old scale / scale) where the scale grew,
- *   a new value x becomes e4m3(x / scale): round to nearest even, saturating
- *           at +-448 (infinities too); NaN stays NaN.
+ *   a new value x becomes e4m3(x * (1 / scale)): round to nearest even,
+ *           saturating at +-448 (infinities too); NaN stays NaN.
  * Slots behind the new tokens keep their bytes.  Powers of two make x / scale
  * and the rescaling exact, so a value is rounded once (again only where it
  * turns subnormal).  Each touched page has to belong to one sequence of the

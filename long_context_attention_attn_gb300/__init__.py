@@ -574,7 +574,8 @@ def _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, w
 
 
 def workspace_bytes_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens) -> int:
-    """Workspace bytes attn_decode needs for these shapes on q's device (0 if it rejects them)."""
+    """Workspace bytes attn_decode needs for these shapes on q's device, with any window (0 if it
+    rejects them; 256 where it uses none)."""
     p, index, _, _ = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, -1, 0,
                                     None, None, None, False)
     with torch.cuda.device(index):

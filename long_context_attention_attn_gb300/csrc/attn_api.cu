@@ -448,7 +448,7 @@ static int check_cache(const attn_kv_cache& c) {
   if (c.d != 64 && c.d != 128 && c.d != 256) return ATTN_ERR_UNSUPPORTED;
   if (c.page_stride != 0 &&
       (c.page_stride < c.h_kv * c.page_size * c.d || c.page_stride % 16 != 0 ||
-       c.page_stride > (1ll << 40)))
+       c.page_stride > (1ll << 32)))
     return ATTN_ERR_INVALID_ARG;
   return ATTN_OK;
 }
@@ -472,7 +472,7 @@ int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
   if (p->token_stride != 0 && (p->token_stride < c.h_kv * c.d || p->token_stride % 8 != 0 ||
                                p->token_stride > (1ll << 24)))
     return ATTN_ERR_INVALID_ARG;
-  if (p->tokens > (1ll << 40) || p->row_tokens > (1ll << 40) || p->max_new > (1ll << 30))
+  if (p->tokens > (1ll << 36) || p->row_tokens > (1ll << 40) || p->max_new > (1ll << 30))
     return ATTN_ERR_UNSUPPORTED;
   const int64_t ts = p->token_stride > 0 ? p->token_stride : c.h_kv * c.d;
   const uint64_t in_bytes = ((uint64_t)(p->tokens - 1) * ts + c.h_kv * c.d) * 2;

@@ -444,26 +444,26 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
       p.t1 = (int)((int64_t)p.span.count * (rank + 1) / a.cluster);
       at = end;
     } else {
-    if (p.span.count == 0) {
-      ++seq;
-      continue;
-    }
-    // the piece [w0, w1) of the item's weight: its first kItemCost hold no block
-    const int64_t in_seq = at - seq_at;
-    const int weight = p.span.weight;
-    p.kvh = (int)(in_seq / weight);
-    p.rt = blockIdx.x % a.row_tiles;
-    const int w0 = (int)(in_seq - (int64_t)p.kvh * weight);
-    const int w1 = (int)min((int64_t)weight, w0 + (end - at));
-    p.t0 = max(w0 - kItemCost, 0);
-    p.t1 = max(w1 - kItemCost, 0);
-    at += w1 - w0;
-    item_done = w1 == weight;
-    if (item_done && p.kvh == a.h_kv - 1) {
-      seq_at += (int64_t)weight * a.h_kv;
-      ++seq;
-    }
-    if (p.t1 == p.t0) continue;
+      if (p.span.count == 0) {
+        ++seq;
+        continue;
+      }
+      // the piece [w0, w1) of the item's weight: its first kItemCost hold no block
+      const int64_t in_seq = at - seq_at;
+      const int weight = p.span.weight;
+      p.kvh = (int)(in_seq / weight);
+      p.rt = blockIdx.x % a.row_tiles;
+      const int w0 = (int)(in_seq - (int64_t)p.kvh * weight);
+      const int w1 = (int)min((int64_t)weight, w0 + (end - at));
+      p.t0 = max(w0 - kItemCost, 0);
+      p.t1 = max(w1 - kItemCost, 0);
+      at += w1 - w0;
+      item_done = w1 == weight;
+      if (item_done && p.kvh == a.h_kv - 1) {
+        seq_at += (int64_t)weight * a.h_kv;
+        ++seq;
+      }
+      if (p.t1 == p.t0) continue;
     }
 
     // ---- the rows of q: their loads are in flight while the ring fills
