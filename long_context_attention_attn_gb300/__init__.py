@@ -163,12 +163,14 @@ def _ptr(t: Optional[torch.Tensor]):
 
 
 def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The current stream of a CUDA device (or device index) as a raw handle: torch's Stream
+    object would cost more than a launch."""
+    index = device if isinstance(device, int) else device.index
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(index))
 
 
 def _on_device(index: int, call, *args):
-    """call(*args, stream) on device ``index`` and its current stream (as a raw
-    handle: torch's Stream object would cost more than the launch it is for)."""
+    """call(*args, stream) on device ``index`` and its current stream."""
     here = torch._C._cuda_getDevice()
     if here == index:
         return call(*args, torch._C._cuda_getCurrentRawStream(index))
