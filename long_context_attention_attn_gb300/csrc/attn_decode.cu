@@ -91,6 +91,11 @@ struct Tune {
   // 15.1 / 12.8, 8192 16.8 / 16.4, 16384 23.2 / 25.2.
   static constexpr int kClusterBlocks = (NT == 1 ? 16 : NT == 2 ? 8 : 0) * (D == 64 ? 2 : 1);
 };
+// Most blocks per warp for which a CTA takes an item alone, however many items
+// there are (twice that where all fit on the GPU at once): 64 sequences of up to
+// 512 tokens (Hq 32 Hkv 8 d 128) 17.3 us by the list, 15.6 us so; of up to 2048
+// 31.8 and 32.9.
+constexpr int kAloneBlocks = 4;
 // Shortest run: a shorter one would only add partials to fold.
 constexpr int kMinRun = 16;
 constexpr int kMaxCluster = 8;  // CTAs per item, at most (a size every GPU takes)
@@ -1074,11 +1079,11 @@ struct Kernel {
     }
     const int64_t items = p.n * p.cache.h_kv * row_tiles;
     s->cluster = 0;
-    for (int c = kMaxCluster; c > 1; c /= 2)
-      if (items * c <= n && blocks <= (int64_t)c * kWarps * T::kClusterBlocks) {
-        s->cluster = c;
-        break;
-      }
+    if constexpr (T::kClusterBlocks > 0) {
+      for (int c = kMaxCluster; c > 1 && !s->cluster; c /= 2)
+        if (items * c <= n && blocks <= (int64_t)c * kWarps * T::kClusterBlocks) s->cluster = c;
+      if (!s->cluster && blocks <= kWarps * (items <= n ? 2 : 1) * kAloneBlocks) s->cluster = 1;
+    }
     // no more than shortest runs
     const int64_t most = ((blocks + T::kItemCost) * p.n * p.cache.h_kv + kMinRun - 1) / kMinRun;
     const int64_t runs = n / row_tiles > 1 ? n / row_tiles : 1;

@@ -219,6 +219,15 @@ def test_ragged_batch_is_repeatable_on_any_stream(ga):
     assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("n,hkv,lens_of", [(70, 8, lambda i: (i * 37) % 257), (40, 8, lambda i: (i * 131) % 513),
+                                           (25, 2, lambda i: (i * 331) % 4000)])
+def test_many_items(ga, n, hkv, lens_of):
+    """More items than the GPU holds CTAs (one CTA each), as many (one each, or a pair), and
+    few long ones (a cluster of eight)."""
+    c = _case(n, 1, 4 * hkv, hkv, 64, 32, [lens_of(i) for i in range(n)], seed=n)
+    _check(_run(ga, c, -1, 0, 0.125), _want(c, -1, 0, 0.125), True)
+
+
 def test_captured_steps_follow_the_lengths(ga):
     """A graph of append and decode, replayed step by step with lengths on the device."""
     n, hq, hkv, d, size = 3, 8, 2, 128, 32
