@@ -382,3 +382,22 @@ def test_binding_refusals(ga):
     for t, u in zip(cache, before):
         assert torch.equal(t.view(torch.uint8) if t.dtype == f8 else t.nan_to_num(9),
                            u.view(torch.uint8) if u.dtype == f8 else u.nan_to_num(9))
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_random_configurations(ga, seed):
+    """Any mix of lengths, query tokens, groups, page sizes, windows, kept tokens and missing pages,
+    by clusters and by the list."""
+    rng = np.random.default_rng(9000 + seed)
+    d, size = int(rng.choice([64, 128, 256])), int(rng.choice([16, 32, 64, 128]))
+    n, sq = int(rng.integers(1, 9)), int(rng.choice([1, 1, 2, 3, 5]))
+    hkv, g = int(rng.integers(1, 4)), int(rng.choice([1, 2, 3, 7, 8, 16, 20]))
+    lens = [int(m) for m in rng.integers(0, int(rng.choice([20, 200, 900])), n)]
+    window = -1 if rng.random() < 0.4 else int(rng.integers(0, 200))
+    sink = int(rng.choice([0, 1, 17, 40]))
+    c = _case(n, sq, hkv * g, hkv, d, size, lens, seed=seed)
+    if rng.random() < 0.5:
+        gone = torch.from_numpy(rng.random(c["table"].shape) < 0.2)
+        c["table"][gone] = int(rng.choice([-1, 1 << 20]))
+    want = _want(c, window, sink, d ** -0.5)
+    _check(_run(ga, _wide(c, size) if seed % 2 else c, window, sink, d ** -0.5, out_fp32=True), want, False)

@@ -154,3 +154,25 @@ def test_copy_no_pairs(ga):
     cache = _cache(3, 1, 16, 64, seed=0)
     none = torch.empty(0, dtype=torch.int32, device=DEV)
     ga.kv_cache_copy_pages(*cache, none, none)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_appends(ga, seed):
+    """Three calls in a row on one cache with any starts, lengths, page sizes and heads."""
+    rng = np.random.default_rng(8000 + seed)
+    d, size, h = int(rng.choice([64, 128, 256])), int(rng.choice([16, 32, 64, 128])), int(rng.integers(1, 4))
+    n, per = int(rng.integers(1, 5)), int(rng.integers(1, 5))
+    cache = _cache(n * per + 2, h, size, d, seed=seed, halves=bool(seed & 1))
+    table = _tables(n, per, n * per + 2, seed=seed)
+    if seed % 3 == 0:
+        table[rng.integers(0, n), rng.integers(0, per)] = -1
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    at = [int(x) for x in rng.integers(0, size, n)]
+    for call in range(3):
+        s = int(rng.choice([1, 2, 17, 40]))
+        k, v = _new(n, s, h, d, seed=100 * seed + call, packed=bool(seed & 2))
+        lens = [int(x) for x in rng.integers(0, s + 1, n)]
+        want = _expect(k, v, cache, table, at, lens, [i * s for i in range(n)])
+        ga.kv_cache_append(k, v, *cache, table.to(DEV), i32(at), lens=i32(lens))
+        _same(cache, want)
+        at = [a + m for a, m in zip(at, lens)]

@@ -180,3 +180,43 @@ def test_ring_and_allgather(batch_shards):
     for got3 in grads:
         for name, got, want in zip(("dq", "dk", "dv"), got3, ref):
             check_grad(got.cpu(), want, name)
+
+
+LENGTHS = [1, 2, 63, 64, 65, 127, 128, 129, 255, 257, 383, 640, 1000, 1500]
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_configurations(seed):
+    """Lengths around the tiles' edges, groups of one to five, any window and kept tokens, random
+    packings, and queries of one block against the keys of an earlier one."""
+    import long_context_attention_attn_gb300 as ga
+    rng = np.random.default_rng(7000 + seed)
+    d, dv = [(64, 64), (128, 128), (256, 256), (192, 128)][seed % 4]
+    b, hkv, g = int(rng.integers(1, 3)), int(rng.integers(1, 3)), int(rng.integers(1, 6))
+    s_q = int(rng.choice(LENGTHS))
+    cross = bool(rng.random() < 0.3)
+    s_kv = int(rng.choice(LENGTHS)) if cross else s_q
+    window = int(rng.integers(0, max(1, s_kv // int(rng.integers(1, 9)))))
+    sink = int(rng.choice([1, 2, 5, 64, 129, 400]))
+    q, _, _, dout = workload.qkv(b, s_q, hkv * g, hkv, d, seed=seed, with_dout=True, dv=dv)
+    _, k, v = workload.qkv(b, s_kv, hkv * g, hkv, d, seed=seed + 500, dv=dv)
+    ids, pos = workload.random_segments(b, s_q, seed=seed, max_segments=3, pad_prob=0.25)
+    kv_ids, kv_pos = ids, pos
+    if cross:
+        kv_ids = torch.ones(b, s_kv, dtype=torch.int32)
+        kv_pos = torch.arange(s_kv, dtype=torch.int32)[None].repeat(b, 1)
+        kv_ids[:, s_kv // 3: s_kv // 3 + s_kv // 7] = 0
+        ids = torch.ones(b, s_q, dtype=torch.int32)
+        pos = torch.arange(s_kv // 2, s_kv // 2 + s_q, dtype=torch.int32)[None].repeat(b, 1)
+    desc = (ids, pos, kv_ids, kv_pos)
+    scale = d ** -0.5
+    dev = [t.to(DEV) for t in (q, k, v, dout, *desc)]
+    kw = dict(window_left=window, sink_tokens=sink, scale=scale, check_status=True)
+    out, lse = ga.attn_fwd(*dev[:3], *dev[4:], **kw)
+    grads = ga.attn_bwd(*dev[:3], out, lse, dev[3], *dev[4:], deterministic=bool(seed & 4), **kw)
+    ro, rl = A.attn_fwd(q, k, v, *desc, window, scale, sink_tokens=sink)
+    check_out(out.cpu(), ro)
+    check_lse(lse.cpu(), rl)
+    for name, got, want in zip(("dq", "dk", "dv"), grads, A.attn_bwd(q, k, v, dout, *desc, window, scale,
+                                                                     sink_tokens=sink)):
+        check_grad(got.cpu(), want, name)
