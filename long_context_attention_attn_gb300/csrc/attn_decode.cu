@@ -30,6 +30,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
+
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -596,7 +598,9 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
 
     // ---- running state: thread (n8, t4) holds rows 8 nt + 2 t4 + {0, 1}
     float o[D / 16][NT][4];
-    float m[NT][2], mo[NT][2], l[NT][2];  // reference of P, of P * v_scale (base 2); sum of P
+    // the references of P and of P * v_scale (base 2, negated; at first below every
+    // score), and the sum of P
+    float nm[NT][2], nmo[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -605,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         for (int c = 0; c < 4; ++c) o[i][nt][c] = 0.f;
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        m[nt][c] = mo[nt][c] = -INFINITY;
+        nm[nt][c] = nmo[nt][c] = FLT_MAX;
         l[nt][c] = 0.f;
       }
     }
@@ -686,11 +690,13 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
                             (a.window < 0 || p_last - key0 <= a.window || key0 + kBlock - 1 < a.sink);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float2 fac = *reinterpret_cast<const float2*>(s_fac + 8 * nt + 2 * t4);
+        const float2 row = *reinterpret_cast<const float2*>(s_fac + 8 * nt + 2 * t4);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[mt][nt][c] *= ((c & 1) ? fac.y : fac.x) * ks_[mt];
+          float f0, f1;
+          mul_f32x2(f0, f1, row.x, row.y, ks_[mt], ks_[mt]);
+          mul_f32x2(s[mt][nt][0], s[mt][nt][1], s[mt][nt][0], s[mt][nt][1], f0, f1);
+          mul_f32x2(s[mt][nt][2], s[mt][nt][3], s[mt][nt][2], s[mt][nt][3], f0, f1);
         }
       }
       if (!all_seen) {
@@ -711,65 +717,77 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
       }
 
       // raise the references where a score passed them by more than kRescale
+      // (the largest score of this thread's keys, alone and with V's scale)
+      auto largest = [&](int nt, float (&x)[2], float (&xo)[2]) {
+        x[0] = x[1] = xo[0] = xo[1] = -INFINITY;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          float y0 = fmaxf(s[mt][nt][0], s[mt][nt][2]), y1 = fmaxf(s[mt][nt][1], s[mt][nt][3]);
+          x[0] = fmaxf(x[0], y0);
+          x[1] = fmaxf(x[1], y1);
+          add_f32x2(y0, y1, y0, y1, lvs[mt], lvs[mt]);
+          xo[0] = fmaxf(xo[0], y0);
+          xo[1] = fmaxf(xo[1], y1);
+        }
+      };
       bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const float x0 = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-          const float x1 = fmaxf(s[MT - 1][nt][c], s[MT - 1][nt][c + 2]);
-          raise |= fmaxf(x0, x1) > m[nt][c] + kRescale;
-          raise |= fmaxf(x0 + lvs[0], x1 + lvs[MT - 1]) > mo[nt][c] + kRescale;
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        float x[2], xo[2];
+        largest(nt, x, xo);
+        add_f32x2(x[0], x[1], x[0], x[1], nm[nt][0], nm[nt][1]);
+        add_f32x2(xo[0], xo[1], xo[0], xo[1], nmo[nt][0], nmo[nt][1]);
+        raise |= fmaxf(x[0], xo[0]) > kRescale;
+        raise |= fmaxf(x[1], xo[1]) > kRescale;
+      }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float x[2], xo[2];
+          largest(nt, x, xo);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float x0 = fmaxf(s[0][nt][c], s[0][nt][c + 2]);
-            const float x1 = fmaxf(s[MT - 1][nt][c], s[MT - 1][nt][c + 2]);
-            float a0 = fmaxf(x0, x1), a1 = fmaxf(x0 + lvs[0], x1 + lvs[MT - 1]);
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
-              a0 = fmaxf(a0, __shfl_xor_sync(0xffffffffu, a0, off));
-              a1 = fmaxf(a1, __shfl_xor_sync(0xffffffffu, a1, off));
+              x[c] = fmaxf(x[c], __shfl_xor_sync(0xffffffffu, x[c], off));
+              xo[c] = fmaxf(xo[c], __shfl_xor_sync(0xffffffffu, xo[c], off));
             }
-            if (a0 > m[nt][c]) {
-              l[nt][c] *= ex2(m[nt][c] - a0);
-              m[nt][c] = a0;
+            if (x[c] + nm[nt][c] > 0.f) {
+              l[nt][c] *= ex2(-nm[nt][c] - x[c]);
+              nm[nt][c] = -x[c];
             }
-            if (a1 > mo[nt][c]) {
-              const float f = ex2(mo[nt][c] - a1);
+            if (xo[c] + nmo[nt][c] > 0.f) {
+              const float f = ex2(-nmo[nt][c] - xo[c]);
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 o[i][nt][c] *= f;
                 o[i][nt][c + 2] *= f;
               }
-              mo[nt][c] = a1;
+              nmo[nt][c] = -xo[c];
             }
           }
+        }
       }
 
       // P^T fragments: p = 2^(x - m) for the sum, p * 2^(lvs + m - mo) for O
       uint32_t pb[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float sub[2], up[MT][2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          sub[c] = m[nt][c] == -INFINITY ? 0.f : m[nt][c];
-          const float so = mo[nt][c] == -INFINITY ? 0.f : mo[nt][c];
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) up[mt][c] = ex2(fminf(lvs[mt] + sub[c] - so, 120.f));
-        }
+        float b0, b1;  // m - mo
+        fma_f32x2(b0, b1, nm[nt][0], nm[nt][1], -1.f, -1.f, nmo[nt][0], nmo[nt][1]);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
-          float e[4];
+          float u0, u1, e[4];
+          add_f32x2(u0, u1, lvs[mt], lvs[mt], b0, b1);
+          u0 = ex2(fminf(u0, 120.f));
+          u1 = ex2(fminf(u1, 120.f));
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            e[c] = ex2(s[mt][nt][c] - sub[c & 1]);
-            l[nt][c & 1] += e[c];
-            e[c] *= up[mt][c & 1];
+          for (int c = 0; c < 4; c += 2) {
+            add_f32x2(e[c], e[c + 1], s[mt][nt][c], s[mt][nt][c + 1], nm[nt][0], nm[nt][1]);
+            e[c] = ex2(e[c]);
+            e[c + 1] = ex2(e[c + 1]);
+            add_f32x2(l[nt][0], l[nt][1], l[nt][0], l[nt][1], e[c], e[c + 1]);
+            mul_f32x2(e[c], e[c + 1], e[c], e[c + 1], u0, u1);
           }
           pb[mt][nt][0] = transpose8x8(pack_f16(e[0], e[1]));
           pb[mt][nt][1] = transpose8x8(pack_f16(e[2], e[3]));
@@ -832,8 +850,8 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         }
         if (n8 == 0) {
           float* x = st + (warp * C::R + r) * 3;
-          x[0] = m[nt][c];
-          x[1] = mo[nt][c];
+          x[0] = -nm[nt][c];
+          x[1] = -nmo[nt][c];
           x[2] = l[nt][c];
         }
       }
@@ -848,10 +866,9 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         const int r = u / kVec, d4 = u % kVec;
         const int row = p.rt * C::R + r;
         if (row >= a.rows) break;
-        float top = -INFINITY;
+        float ref = -FLT_MAX;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, st[(w * C::R + r) * 3]);
-        const float ref = top == -INFINITY ? 0.f : top;
+        for (int w = 0; w < kWarps; ++w) ref = fmaxf(ref, st[(w * C::R + r) * 3]);
         float z = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
