@@ -123,6 +123,21 @@ bool encode_acc_map(CUtensorMap* m, const float* base, int64_t b, int64_t s, int
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Pages of 8-bit codes viewed as (d, token, head, page); box = up to 128 d (64 or
+// 128 bytes, swizzled) x 16 tokens of one head, which lie on one page.
+bool encode_page_map(CUtensorMap* m, const void* base, int64_t pages, int64_t h, int64_t page_size, int64_t d,
+                     int64_t page_stride) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page_size, (cuuint64_t)h, (cuuint64_t)pages};
+  cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)(page_size * d), (cuuint64_t)page_stride};
+  cuuint32_t box[4] = {(cuuint32_t)(d < 128 ? d : 128), 16, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gb300
 
 extern "C" {

@@ -31,6 +31,7 @@
 #include <cuda_fp16.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -45,6 +46,10 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // The running maximum is raised only when a value exceeds it by more than this
 // (in powers of two), so P <= 256.
 constexpr float kRescale = 8.f;
+// P * v_scale is held 2^7 times larger (<= 2^15, f16 ends at 2^16): it keeps its 11
+// bits down to 2^-21 of the largest, where one key has nearly all the weight and a
+// zero code others decide the sum.
+constexpr float kShift = 7.f;
 
 struct DecodeArgs {
   const __nv_bfloat16* q;
@@ -75,6 +80,7 @@ struct DecodeArgs {
 // three CTAs and two slots 173 us (1.09 GB).
 template <int D, int NT>
 struct Tune {
+  static constexpr bool kTensor = false;
   static constexpr int kBlock = D == 256 ? 16 : 32;
   static constexpr int kStages = (D == 128 && NT <= 2) || (D == 256 && NT == 1) ? 2 : 3;
   static constexpr int kCtas = D == 64 ? (NT == 1 ? 4 : NT == 2 ? 3 : 2) : D * NT <= 256 ? 3 : 2;
@@ -92,6 +98,16 @@ struct Tune {
   // 6.3, 4096 11.5 / 8.9, 16384 19.6 / 18.5, 32768 29.3 / 31.5; Hq 128 at 4096
   // 15.1 / 12.8, 8192 16.8 / 16.4, 16384 23.2 / 25.2.
   static constexpr int kClusterBlocks = (NT == 1 ? 16 : NT == 2 ? 8 : 0) * (D == 64 ? 2 : 1);
+};
+// The kernel of 128 rows per CTA (attn_decode_tensor.cuh), one CTA per SM.
+constexpr int kTensorNT = 16;
+template <int D>
+struct Tune<D, kTensorNT> {
+  static constexpr bool kTensor = true;
+  static constexpr int kBlock = 32;
+  static constexpr int kStages = D == 64 ? 6 : 3;  // of 128 keys (64 at d = 256)
+  static constexpr int kItemCost = D == 256 ? 16 : 64;
+  static constexpr int kClusterBlocks = 0;
 };
 // Most blocks per warp for which a CTA takes an item alone, however many items
 // there are (twice that where all fit on the GPU at once): 64 sequences of up to
@@ -769,12 +785,13 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         }
       }
 
-      // P^T fragments: p = 2^(x - m) for the sum, p * 2^(lvs + m - mo) for O
+      // P^T fragments: p = 2^(x - m) for the sum, p * 2^(lvs + m - mo + kShift) for O
       uint32_t pb[MT][NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float b0, b1;  // m - mo
+        float b0, b1;  // m - mo + kShift
         fma_f32x2(b0, b1, nm[nt][0], nm[nt][1], -1.f, -1.f, nmo[nt][0], nmo[nt][1]);
+        add_f32x2(b0, b1, b0, b1, kShift, kShift);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float u0, u1, e[4];
@@ -851,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         if (n8 == 0) {
           float* x = st + (warp * C::R + r) * 3;
           x[0] = -nm[nt][c];
-          x[1] = -nmo[nt][c];
+          x[1] = -nmo[nt][c] - kShift;
           x[2] = l[nt][c];
         }
       }
@@ -1045,6 +1062,8 @@ __global__ void __launch_bounds__(kFoldThreads) attn_decode_combine_kernel(const
     a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (s_ref[r] + log2f(z)) * kLn2;
 }
 
+#include "attn_decode_tensor.cuh"
+
 // How a problem is launched: a cluster of `cluster` CTAs per item, or (0) `runs`
 // runs of the list.
 struct Shape {
@@ -1053,8 +1072,8 @@ struct Shape {
 
 template <int D, int NT>
 struct Kernel {
-  using C = Cfg<D, NT>;
   using T = Tune<D, NT>;
+  using C = std::conditional_t<T::kTensor, TensorCfg<D>, Cfg<D, NT>>;
   // CTAs that fill the device once
   static cudaError_t resident(int* n) {
     static std::atomic<int> cache[kMaxDevices];
@@ -1064,19 +1083,24 @@ struct Kernel {
     const bool cached = dev >= 0 && dev < kMaxDevices;
     *n = cached ? cache[dev].load(std::memory_order_acquire) : 0;
     if (*n > 0) return cudaSuccess;
-    e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::bytes);
-    if constexpr (T::kClusterBlocks > 0) {
+    int per_sm = 1;
+    if constexpr (T::kTensor) {
+      e = cudaFuncSetAttribute(attn_decode_tensor_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes);
+      if (e != cudaSuccess) return e;
+    } else {
+      e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               C::bytes);
+      if constexpr (T::kClusterBlocks > 0) {
+        if (e == cudaSuccess)
+          e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   C::bytes);
+      }
       if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 C::bytes);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_decode_kernel<D, NT, false>, kThreads,
+                                                          C::bytes);
+      if (e != cudaSuccess) return e;
+      if (per_sm < 1) return cudaErrorInvalidConfiguration;
     }
-    int per_sm = 0;
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attn_decode_kernel<D, NT, false>, kThreads,
-                                                        C::bytes);
-    if (e != cudaSuccess) return e;
-    if (per_sm < 1) return cudaErrorInvalidConfiguration;
     *n = per_sm * sm_count();
     if (cached) cache[dev].store(*n, std::memory_order_release);
     return cudaSuccess;
@@ -1130,7 +1154,15 @@ struct Kernel {
     }
     const int grid = sh.runs * a.row_tiles;
     a.part_lse = a.part_o + (int64_t)2 * grid * C::R * D;
-    attn_decode_kernel<D, NT, false><<<grid, kThreads, C::bytes, st>>>(a);
+    if constexpr (T::kTensor) {
+      CUtensorMap tm_k, tm_v;
+      if (!encode_page_map(&tm_k, a.k, a.num_pages, a.h_kv, 1 << a.page_shift, D, a.page_stride) ||
+          !encode_page_map(&tm_v, a.v, a.num_pages, a.h_kv, 1 << a.page_shift, D, a.page_stride))
+        return cudaErrorInvalidValue;
+      attn_decode_tensor_kernel<D><<<grid, C::kThreads, C::bytes, st>>>(a, tm_k, tm_v);
+    } else {
+      attn_decode_kernel<D, NT, false><<<grid, kThreads, C::bytes, st>>>(a);
+    }
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)items, C::R / kFoldRows<D, NT>);
@@ -1141,11 +1173,13 @@ struct Kernel {
   }
 };
 
-// f(kernel, shape) with 8 or 16 rows per CTA, and 32 where there are more rows
-// than 16 and the list cuts the work: a CTA then widens each code for twice the
-// rows (Hkv 8 d 128, 48 sequences of 100 to 12000 tokens, 64 rows: 301 us against
-// 332), while clusters do better with twice the CTAs (one sequence of 4096
-// tokens, 64 rows: 15.3 us against 20.2).  At d = 256 the registers end at 16.
+// f(kernel, shape) with 8 or 16 rows per CTA.  Above 16 rows clusters stay with
+// them (twice the CTAs: one sequence of 4096 tokens, Hkv 8 d 128, 64 rows 14.6 us),
+// and where the list cuts the work a CTA widens each code for more rows: 32 (at
+// d = 256 the registers end at 16), and from 65 rows on (49 at d = 256) 128 on the
+// tensor-memory path, whose time does not depend on the rows.  48 sequences of 100
+// to 12000 tokens, Hkv 8, us at 64 and 128 rows so, and by the tensor path: d 64 207
+// and 407, 236; d 128 294 and 567, 307; d 256 635 and 1252, 555.
 template <int D, typename F>
 cudaError_t with_rows(const attn_decode_params& p, F&& f) {
   auto use = [&](auto k) {
@@ -1155,12 +1189,13 @@ cudaError_t with_rows(const attn_decode_params& p, F&& f) {
   };
   const int64_t rows = p.s_q * (p.h_q / p.cache.h_kv);
   if (rows <= 8) return use(Kernel<D, 1>());
-  if constexpr (D < 256) {
-    if (rows > 16) {
-      Shape sh;
-      const cudaError_t e = Kernel<D, 2>::shape(p, &sh);
-      if (e != cudaSuccess) return e;
-      if (!sh.cluster) return use(Kernel<D, 4>());
+  if (rows > 16) {
+    Shape sh;
+    const cudaError_t e = Kernel<D, 2>::shape(p, &sh);
+    if (e != cudaSuccess) return e;
+    if (!sh.cluster) {
+      if (rows > (D == 256 ? 48 : 64)) return use(Kernel<D, kTensorNT>());
+      if constexpr (D < 256) return use(Kernel<D, 4>());
     }
   }
   return use(Kernel<D, 2>());

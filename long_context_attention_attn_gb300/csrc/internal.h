@@ -272,5 +272,7 @@ cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st);
 bool encode_qkv_map(CUtensorMap* m, const void* base, int64_t b, int64_t s, int64_t h, int64_t d,
                     int64_t token_stride, int box_rows = kTile);
 bool encode_acc_map(CUtensorMap* m, const float* base, int64_t b, int64_t s, int64_t h, int64_t d);
+bool encode_page_map(CUtensorMap* m, const void* base, int64_t pages, int64_t h, int64_t page_size, int64_t d,
+                     int64_t page_stride);
 
 }  // namespace gb300
