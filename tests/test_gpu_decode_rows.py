@@ -112,6 +112,35 @@ def test_strided_pages_beside_other_work(ga):
         assert torch.equal(there, alone) and torch.equal(here[0], ref[0]) and torch.equal(here[1], ref[1])
 
 
+def test_offsets_past_32_bits(ga):
+    """Pages whose bytes lie beyond 4 GB of the cache, and lengths behind the table."""
+    size, hkv, d, pages = 128, 8, 128, 36000  # of 128 KB
+    c = _case(2, 9, 64, hkv, d, size, [500, 130], seed=8)
+    k = torch.empty(pages, hkv, size, d, dtype=torch.uint8, device=DEV)
+    v = torch.empty(pages, hkv, size, d, dtype=torch.uint8, device=DEV)
+    ks = torch.empty(pages, hkv, device=DEV)
+    vs = torch.empty(pages, hkv, device=DEV)
+    at = torch.tensor([pages - 1 - 100 * i for i in range(c["k"].shape[0])])
+    for big, small in ((k, c["k"]), (v, c["v"]), (ks, c["ks"]), (vs, c["vs"])):
+        big[at.to(DEV)] = small.to(DEV)
+    want = _want(c, -1, 0, 0.09)
+    table = torch.where(c["table"] >= 0, at[c["table"].clamp_min(0).long()].int(), c["table"])
+    table = _wide(dict(table=table), size)["table"]
+    f8 = torch.float8_e4m3fn
+    got = ga.attn_decode(c["q"].to(DEV), k.view(f8), v.view(f8), ks, vs, table.to(DEV), c["lens"].to(DEV),
+                         scale=0.09, out_fp32=True)
+    _check(got, want, False)
+
+
+def test_length_behind_the_table(ga):
+    """Positions go by the length, keys end with the table (here all of its 4096 tokens hold)."""
+    c = _case(2, 9, 8, 1, 64, 16, [4096, 4096], seed=3)
+    c["table"] = c["table"][:, :256].contiguous()
+    c["lens"] = torch.tensor([4100, 2 ** 31 - 1], dtype=torch.int32)
+    for window, sink in ((-1, 0), (50, 3), (2 ** 31 - 1, 1)):
+        _check(_run(ga, c, window, sink, 0.125, out_fp32=True), _want(c, window, sink, 0.125), False)
+
+
 @pytest.mark.parametrize("seed", range(16))
 def test_random_configurations(ga, seed):
     rng = np.random.default_rng(7000 + seed)
