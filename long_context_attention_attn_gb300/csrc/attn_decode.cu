@@ -106,6 +106,8 @@ struct Tune<D, kTensorNT> {
   static constexpr bool kTensor = true;
   static constexpr int kBlock = 32;
   static constexpr int kStages = D == 64 ? 6 : 3;  // of 128 keys (64 at d = 256)
+  // (us of 48 sequences of 100 to 12000 tokens with 32 / 64: d 64 252 / 241, d 128
+  // 326 / 313; d 256 with 16 / 32: 563 / 572)
   static constexpr int kItemCost = D == 256 ? 16 : 64;
   static constexpr int kClusterBlocks = 0;
 };
@@ -1179,7 +1181,7 @@ struct Kernel {
 // d = 256 the registers end at 16), and from 65 rows on (49 at d = 256) 128 on the
 // tensor-memory path, whose time does not depend on the rows.  48 sequences of 100
 // to 12000 tokens, Hkv 8, us at 64 and 128 rows so, and by the tensor path: d 64 207
-// and 407, 236; d 128 294 and 567, 307; d 256 635 and 1252, 555.
+// and 407, 233; d 128 294 and 567, 305; d 256 635 and 1252, 544.
 template <int D, typename F>
 cudaError_t with_rows(const attn_decode_params& p, F&& f) {
   auto use = [&](auto k) {

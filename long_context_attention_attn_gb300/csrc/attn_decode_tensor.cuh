@@ -11,6 +11,14 @@
 //   products  one thread: S in two buffers, O behind P
 //   softmax   4 warps, a thread per row: q's row as f16 into tensor memory once a
 //             piece; scores out of it, P (f16) back in their place
+// The time is the softmax's: its 128 keys of a tile take a warp 2900 cycles (one warp
+// per scheduler, so latencies count: the e^x 1090, the sums, factors and packing
+// 1100, the maxima 440), where HBM would take 1410 at d = 128.  That does not depend
+// on the rows.  Tried, 128 rows at d = 128 (305 us for 48 sequences of 100 to 12000
+// tokens, Hkv 8): two softmax groups on tiles of 64 keys with an accumulator each 392;
+// 216 registers for the softmax and a thread each for S and O 374; keys on the M side
+// (a thread per key, P through shared memory, votes over threads) 495 with two CTAs
+// per SM, 541 by roles.
 #pragma once
 
 // One piece of work: blocks [t0, t1) of an item; whole: all of it.
@@ -113,7 +121,7 @@ template <int D>
 struct TensorCfg {
   using T = Tune<D, kTensorNT>;
   static constexpr int R = kTensorNT * 8;
-  static constexpr int kThreads = 32 * 16;  // K 4, V 4, softmax 4, loader, products, none
+  static constexpr int kThreads = 32 * 14;  // K 4, V 4, softmax 4, products, loader
   static constexpr int kKeys = D == 256 ? 64 : 128;  // per tile
   static constexpr int kBlocks = kKeys / 32;
   static constexpr int kStages = T::kStages;
@@ -200,15 +208,15 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     tmem_relinquish();
   }
   const Placement pl = place<T>(a, before);
-  // roles: 0 K, 1 V, 2 softmax, 3 products, 4 loader, 5 none
-  const int role = warp < 12 ? warp >> 2 : min(warp - 9, 5);
-  if (lane == 0 && (warp == 12 || warp == 13 || (warp < 12 && (warp & 3) == 0))) walks[role].begin(a, pl);
+  // roles: 0 K, 1 V, 2 softmax, 3 products, 4 loader
+  const int role = warp < 12 ? warp >> 2 : warp - 9;
+  if (lane == 0 && (warp >= 12 || (warp & 3) == 0)) walks[role].begin(a, pl);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const WaitCtx ctx{&s_abort, nullptr};
-  TensorWalk<T>& walk = walks[min(role, 4)];
+  TensorWalk<T>& walk = walks[role];
   auto warp_sync = [] { __syncwarp(); };
   auto group_sync = [&] { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + role) : "memory"); };
   // of piece number n
@@ -412,7 +420,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
       if (is_v) mbar_arrive(&bars.widened[n & 1]);
       ++n;
     }
-  } else if (role == 2) {
+  } else {
     // ======================================================== softmax
     const int wq = warp & 3, r = threadIdx.x & 127;  // the row of this thread
     const uint32_t my_tmem = tmem + ((uint32_t)(wq * 32) << 16), t_o = my_tmem + C::col_o;
