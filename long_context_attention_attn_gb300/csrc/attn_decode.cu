@@ -99,18 +99,21 @@ struct Tune {
   // 15.1 / 12.8, 8192 16.8 / 16.4, 16384 23.2 / 25.2.
   static constexpr int kClusterBlocks = (NT == 1 ? 16 : NT == 2 ? 8 : 0) * (D == 64 ? 2 : 1);
 };
-// The kernel of 128 rows per CTA (attn_decode_tensor.cuh), one CTA per SM.
-constexpr int kTensorNT = 16;
+// The kernel of 64 or 128 rows per CTA (attn_decode_tensor.cuh), one CTA per SM.
 template <int D>
-struct Tune<D, kTensorNT> {
+struct TensorTune {
   static constexpr bool kTensor = true;
   static constexpr int kBlock = 32;
-  static constexpr int kStages = D == 64 ? 6 : 3;  // of 128 keys (64 at d = 256)
+  static constexpr int kStages = D == 64 ? 8 : 3;  // tiles of codes: of 128 keys (64 at d = 256)
   // (us of 48 sequences of 100 to 12000 tokens with 32 / 64: d 64 252 / 241, d 128
   // 326 / 313; d 256 with 16 / 32: 563 / 572)
   static constexpr int kItemCost = D == 256 ? 16 : 64;
   static constexpr int kClusterBlocks = 0;
 };
+template <int D>
+struct Tune<D, 8> : TensorTune<D> {};
+template <int D>
+struct Tune<D, 16> : TensorTune<D> {};
 // Most blocks per warp for which a CTA takes an item alone, however many items
 // there are (twice that where all fit on the GPU at once): 64 sequences of up to
 // 512 tokens (Hq 32 Hkv 8 d 128) 17.3 us by the list, 15.6 us so; of up to 2048
@@ -1075,7 +1078,7 @@ struct Shape {
 template <int D, int NT>
 struct Kernel {
   using T = Tune<D, NT>;
-  using C = std::conditional_t<T::kTensor, TensorCfg<D>, Cfg<D, NT>>;
+  using C = std::conditional_t<T::kTensor, TensorCfg<D, NT>, Cfg<D, NT>>;
   // CTAs that fill the device once
   static cudaError_t resident(int* n) {
     static std::atomic<int> cache[kMaxDevices];
@@ -1087,7 +1090,7 @@ struct Kernel {
     if (*n > 0) return cudaSuccess;
     int per_sm = 1;
     if constexpr (T::kTensor) {
-      e = cudaFuncSetAttribute(attn_decode_tensor_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes);
+      e = cudaFuncSetAttribute(attn_decode_tensor_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::bytes);
       if (e != cudaSuccess) return e;
     } else {
       e = cudaFuncSetAttribute(attn_decode_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -1161,7 +1164,7 @@ struct Kernel {
       if (!encode_page_map(&tm_k, a.k, a.num_pages, a.h_kv, 1 << a.page_shift, D, a.page_stride) ||
           !encode_page_map(&tm_v, a.v, a.num_pages, a.h_kv, 1 << a.page_shift, D, a.page_stride))
         return cudaErrorInvalidValue;
-      attn_decode_tensor_kernel<D><<<grid, C::kThreads, C::bytes, st>>>(a, tm_k, tm_v);
+      attn_decode_tensor_kernel<D, NT><<<grid, C::kThreads, C::bytes, st>>>(a, tm_k, tm_v);
     } else {
       attn_decode_kernel<D, NT, false><<<grid, kThreads, C::bytes, st>>>(a);
     }
@@ -1177,11 +1180,11 @@ struct Kernel {
 
 // f(kernel, shape) with 8 or 16 rows per CTA.  Above 16 rows clusters stay with
 // them (twice the CTAs: one sequence of 4096 tokens, Hkv 8 d 128, 64 rows 14.6 us),
-// and where the list cuts the work a CTA widens each code for more rows: 32 (at
-// d = 256 the registers end at 16), and from 65 rows on (49 at d = 256) 128 on the
-// tensor-memory path, whose time does not depend on the rows.  48 sequences of 100
-// to 12000 tokens, Hkv 8, us at 64 and 128 rows so, and by the tensor path: d 64 207
-// and 407, 233; d 128 294 and 567, 305; d 256 635 and 1252, 544.
+// and where the list cuts the work a CTA widens each code for more rows: up to 32 rows
+// 32 (at d = 256 the registers end at 16), above 64 or 128 on the tensor-memory path.
+// 48 sequences of 100 to 12000 tokens, Hkv 8, us at 32 / 64 / 128 rows by the
+// warp-level kernel and by the other: d 64 109 / 208 / 407 and 157 / 165 / 271; d 128
+// 161 / 294 / 567 and 190 / 221 / 303; d 256 326 / 635 / 1252 and 364 / 438 / 453.
 template <int D, typename F>
 cudaError_t with_rows(const attn_decode_params& p, F&& f) {
   auto use = [&](auto k) {
@@ -1196,7 +1199,8 @@ cudaError_t with_rows(const attn_decode_params& p, F&& f) {
     const cudaError_t e = Kernel<D, 2>::shape(p, &sh);
     if (e != cudaSuccess) return e;
     if (!sh.cluster) {
-      if (rows > (D == 256 ? 48 : 64)) return use(Kernel<D, kTensorNT>());
+      if (rows > 64) return use(Kernel<D, 16>());
+      if (rows > 32) return use(Kernel<D, 8>());
       if constexpr (D < 256) return use(Kernel<D, 4>());
     }
   }

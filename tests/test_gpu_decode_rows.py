@@ -1,5 +1,5 @@
 """Decoding of many rows per kv head (query tokens times the group), which takes a kernel of
-its own from 65 rows on (49 at d = 256) where the list of blocks cuts the work.  Tolerances as
+its own from 33 rows on where the list of blocks cuts the work, with 64 or 128 rows per CTA.  Tolerances as
 in test_gpu_decode."""
 import numpy as np
 import pytest
@@ -21,6 +21,10 @@ CASES = [
     (1, 100, 8, 1, 128, 128, [2000], 1000, 10 ** 6),  # kept tokens: all
     (7, 10, 16, 2, 64, 16, [i * 97 for i in range(7)], 50, 40),
     (2, 1024, 1, 1, 128, 64, [1500, 300], -1, 0),     # the most rows
+    (3, 11, 6, 2, 128, 16, [11, 500, 77], -1, 0),     # 33 rows
+    (4, 4, 32, 2, 64, 64, [1, 130, 64, 2000], 100, 5),  # 64 rows
+    (2, 13, 8, 2, 256, 64, [700, 14], 0, 2),          # 52 rows
+    (2, 50, 1, 1, 128, 32, [2, 1000], 3, 10 ** 6),    # kept tokens: all
 ]
 
 
@@ -33,9 +37,10 @@ def test_many_rows(ga, n, sq, hq, hkv, d, size, lens, window, sink, bf16):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
-def test_nan_of_a_later_token_stays_there(ga, d):
+@pytest.mark.parametrize("g", [16, 6, 12])
+def test_nan_of_a_later_token_stays_there(ga, d, g):
     """A NaN in a token's V reaches the queries that see it and no others, in both row tiles."""
-    sq, g = 10, 16
+    sq = 10
     c = _case(2, sq, g, 1, d, 64, [200, 77], seed=4)
     ro, rl, mag = _want(c, -1, 0, 0.1)
     at = lambda i, key: (int(c["table"][i, key // 64]), 0, key % 64)
@@ -56,9 +61,10 @@ def test_nan_of_a_later_token_stays_there(ga, d):
 
 
 @pytest.mark.parametrize("top", [40, 110])
-def test_scales_far_apart(ga, top):
+@pytest.mark.parametrize("g,d", [(16, 128), (8, 128), (8, 64), (8, 256)])
+def test_scales_far_apart(ga, top, g, d):
     """Pages of V from 2^-top to 2^top, and of K that raise the maximum late."""
-    c = _case(1, 6, 16, 1, 128, 16, [900], seed=5)
+    c = _case(1, 6, g, 1, d, 16, [900], seed=5)
     n = 900 // 16 + 1
     ids = c["table"][0, :n].long()
     c["vs"][ids, 0] = torch.exp2(torch.linspace(-top, top, n).round())
@@ -148,6 +154,24 @@ def test_random_configurations(ga, seed):
     n, sq, hkv = int(rng.integers(1, 9)), int(rng.integers(7, 25)), int(rng.integers(1, 4))
     g = int(rng.choice([9, 10, 16, 20]))
     lens = [int(m) for m in rng.integers(0, int(rng.choice([20, 200, 900])), n)]
+    window = -1 if rng.random() < 0.4 else int(rng.integers(0, 200))
+    sink = int(rng.choice([0, 1, 17, 40]))
+    c = _case(n, sq, hkv * g, hkv, d, size, lens, seed=seed)
+    if rng.random() < 0.5:
+        gone = torch.from_numpy(rng.random(c["table"].shape) < 0.2)
+        c["table"][gone] = int(rng.choice([-1, 1 << 20]))
+    want = _want(c, window, sink, d ** -0.5)
+    _check(_run(ga, _wide(c, size), window, sink, d ** -0.5, out_fp32=True), want, False)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_configurations_of_fewer_rows(ga, seed):
+    """33 to 64 rows."""
+    rng = np.random.default_rng(8000 + seed)
+    d, size = int(rng.choice([64, 128, 256])), int(rng.choice([16, 32, 64, 128]))
+    n, hkv, g = int(rng.integers(1, 9)), int(rng.integers(1, 4)), int(rng.choice([1, 2, 5, 8, 16]))
+    sq = int(rng.integers(33 // g + 1, 64 // g + 1))
+    lens = [int(m) for m in rng.integers(0, int(rng.choice([20, 200, 1500])), n)]
     window = -1 if rng.random() < 0.4 else int(rng.integers(0, 200))
     sink = int(rng.choice([0, 1, 17, 40]))
     c = _case(n, sq, hkv * g, hkv, d, size, lens, seed=seed)
