@@ -230,10 +230,10 @@ __device__ __forceinline__ void mma16816(float* c, const uint32_t* a, uint32_t b
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Hardware base-2 logarithm (exact for powers of two); of 0 -inf.
+// Hardware base-2 logarithm (exact for powers of two, subnormal ones too); of 0 -inf.
 __device__ __forceinline__ float lg2(float x) {
   float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -897,12 +897,13 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
         for (int w = 0; w < kWarps; ++w) {
           const float* x = st + (w * C::R + r) * 3;
           z += x[2] * ex2(x[0] - ref);
-          const float f = ex2(x[1] - ref);
+          // (in two halves: for small V alone the factor is below fp32's normal numbers)
+          const float f = ex2(0.5f * (x[1] - ref));
           const float4 v = *reinterpret_cast<const float4*>(buf + (w * C::R + r) * C::kMergeRow + 4 * d4);
-          acc.x += v.x * f;
-          acc.y += v.y * f;
-          acc.z += v.z * f;
-          acc.w += v.w * f;
+          acc.x += v.x * f * f;
+          acc.y += v.y * f * f;
+          acc.z += v.z * f * f;
+          acc.w += v.w * f * f;
         }
         const float inv = z == 0.f ? 0.f : 1.f / z;
         acc.x *= inv;

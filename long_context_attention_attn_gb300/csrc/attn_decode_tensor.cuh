@@ -718,8 +718,10 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
 #pragma unroll
         for (int c = 0; c < C::kCopies; ++c) z += s_end[c][1][r] * ex2(-s_end[c][0][r] - ref);
       }
-      // of this copy's O: 2^(mo - ref) / z
-      const float w = (z == 0.f ? 0.f : 1.f / z) * ex2(-nmo - ref - kShift);
+      // of this copy's O: 2^(mo - ref) / z, as w * w2 (for small V alone the product is
+      // below fp32's normal numbers)
+      const float w2 = ex2(0.5f * (-nmo - ref - kShift));
+      const float w = (z == 0.f ? 0.f : 1.f / z) * w2;
       const float lse2 = z == 0.f ? -INFINITY : ref + log2f(z);
       if (mine && copy == 0) {
         if (p.whole)
@@ -735,7 +737,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           tmem_ld32(t_o + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] *= w;
+          for (int j = 0; j < 32; ++j) o[j] = o[j] * w * w2;
           if (nans) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -766,7 +768,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           tmem_ld32(t_o + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) buf[th * 33 + j] = o[j] * w;
+          for (int j = 0; j < 32; ++j) buf[th * 33 + j] = o[j] * w * w2;
           group_sync();
           for (int q = wq; q < rows; q += kWarps) {
             float x = 0.f;
