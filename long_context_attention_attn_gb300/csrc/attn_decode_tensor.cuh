@@ -589,11 +589,15 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
             for (int c = 0; c < W; c += CH) {
               float e[CH];
               tmem_ld32(t_s + col0 + c, reinterpret_cast<uint32_t*>(e));
-              float f[CH / 16], v[CH / 16];
+              // (b * v_scale may pass fp32's range, where keys are out of sight or of next to
+              // no weight: infinite it still tells below that a weight calls for a raise, but
+              // 0 * infinity is NaN, so P takes the largest finite value)
+              float f[CH / 16], v[CH / 16], v_all[CH / 16];
 #pragma unroll
               for (int h = 0; h < CH / 16; ++h) {
                 f[h] = fac * s_ks[m][(col0 + c) / 16 + h];
-                v[h] = b * s_vs[m][(col0 + c) / 16 + h];
+                v_all[h] = b * s_vs[m][(col0 + c) / 16 + h];
+                v[h] = fminf(v_all[h], FLT_MAX);
               }
               tmem_wait_ld();
 #pragma unroll
@@ -618,7 +622,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
                 }
                 const float most = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
                 top = fmaxf(top, most);
-                top_o = fmaxf(top_o, most * v[h]);
+                top_o = fmaxf(top_o, most * v_all[h]);  // (0 * infinity counts as nothing)
               }
 #pragma unroll
               for (int j = 0; j < CH; j += 2) {
