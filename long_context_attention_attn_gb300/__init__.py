@@ -470,6 +470,8 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale):
     page = h * size * d
     if (d > 1 and st[3] != 1) or (size > 1 and st[2] != d) or (h > 1 and st[1] != size * d):
         raise ValueError("k_cache / v_cache: each page must be contiguous")
+    if pages > 1 and st[0] < page:  # (0, as of an expanded tensor, would mean contiguous)
+        raise ValueError("k_cache / v_cache: pages must not overlap")
     if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32
             or k_scale.shape != (pages, h) or v_scale.shape != (pages, h)
             or not k_scale.is_contiguous() or not v_scale.is_contiguous()):
@@ -484,6 +486,8 @@ def _row_stride(x) -> int:
     step = st[1] if s > 1 else st[0] if b > 1 else h * d
     if (d > 1 and st[3] != 1) or (h > 1 and st[2] != d) or (s > 1 and b > 1 and st[0] != s * step):
         raise ValueError("k / v: heads must be contiguous and token rows evenly spaced")
+    if step < h * d:  # (0, as of an expanded tensor, would mean contiguous)
+        raise ValueError("k / v: token rows must not overlap")
     return step
 
 

@@ -1,0 +1,78 @@
+"""What the paged cache's binding makes of its tensors, on the CPU: the tensors pass for a GPU's and
+the library call is replaced by one that notes its parameters, so nothing is launched."""
+import ctypes
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    import __graft_entry__
+    __graft_entry__.build()
+    import long_context_attention_attn_gb300 as pkg
+    return pkg
+
+
+@pytest.fixture
+def ga(pkg, monkeypatch):
+    calls = []
+
+    def note(index, call, ref, *rest):
+        calls.append((call.__name__, ref._obj, rest))
+        return 0
+
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(pkg, "_on_device", note)
+    pkg.calls = calls
+    yield pkg
+    del pkg.calls
+
+
+def _cache(pages=4, h=2, size=16, d=64):
+    return ([torch.zeros(pages, h, size, d, dtype=torch.uint8) for _ in range(2)]
+            + [torch.zeros(pages, h) for _ in range(2)])
+
+
+def _i32(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+def _kv(b, s, h=2, d=64):
+    return torch.zeros(b, s, h, d, dtype=torch.bfloat16)
+
+
+def test_rows_of_stride_zero_are_refused(ga):
+    """One token (or row) broadcast to several has no stride that the library could take: 0 means
+    contiguous there, and rows behind the tensor's end would be read."""
+    table = torch.zeros(3, 2, dtype=torch.int32)
+    start = _i32(0, 0, 0)
+    for k in (_kv(1, 1).expand(3, 1, 2, 64), _kv(1, 1).expand(3, 5, 2, 64), _kv(3, 1).expand(3, 5, 2, 64)):
+        for pair in ((k, k), (k, k.contiguous()), (k.contiguous(), k)):
+            with pytest.raises(ValueError):
+                ga.kv_cache_append(*pair, *_cache(), table, start)
+    with pytest.raises(ValueError):
+        ga.kv_cache_append(_kv(1, 1).expand(1, 5, 2, 64), _kv(1, 1).expand(1, 5, 2, 64), *_cache(), table[:1], start[:1])
+    assert ga.calls == []
+    # rows of a larger tensor are taken as they lie, and sizes of one have no stride
+    kv = torch.zeros(3, 5, 2, 2, 64, dtype=torch.bfloat16)
+    ga.kv_cache_append(kv[:, :, 0], kv[:, :, 1], *_cache(), table, start)
+    ga.kv_cache_append(kv[:, 2:3, 0], kv[:, 2:3, 1], *_cache(), table, start)
+    one = _kv(1, 1).as_strided((1, 1, 2, 64), (0, 0, 64, 1))
+    ga.kv_cache_append(one, one, *_cache(), table[:1], start[:1])
+    assert [c[1].token_stride for c in ga.calls] == [2 * 2 * 64, 5 * 2 * 2 * 64, 2 * 64]
+
+
+def test_pages_of_stride_zero_are_refused(ga):
+    wide = [t[:1].expand(4, -1, -1, -1) for t in _cache()[:2]]
+    cache = (*wide, *_cache()[2:])
+    table, one = torch.zeros(1, 2, dtype=torch.int32), _i32(0)
+    with pytest.raises(ValueError):
+        ga.kv_cache_append(_kv(1, 1), _kv(1, 1), *cache, table, one)
+    with pytest.raises(ValueError):
+        ga.kv_cache_copy_pages(*cache, one, one)
+    with pytest.raises(ValueError):
+        ga.attn_decode(_kv(1, 1), *cache, table, one)
+    with pytest.raises(ValueError):
+        ga.workspace_bytes_decode(_kv(1, 1), *cache, table, one)
+    assert ga.calls == []
