@@ -464,6 +464,13 @@ typedef struct attn_decode_params {
 GB300ATTN_API size_t attn_decode_workspace_bytes(const attn_decode_params* p);
 GB300ATTN_API int attn_decode(const attn_decode_params* p, attn_stream_t stream);
 
+/* Test hook for the bounded waits of attn_decode: runs it with every copy of the
+ * cache withheld, so that the waits run out (about one second).  All results of
+ * sequences with keys are then NaN; the CUDA context stays usable.  Where the
+ * problem takes a kernel without such waits: ATTN_ERR_UNSUPPORTED, nothing is
+ * launched.  Not for production use. */
+GB300ATTN_API int attn_decode_test_timeout(const attn_decode_params* p, attn_stream_t stream);
+
 /* Static description of a status code. */
 GB300ATTN_API const char* attn_status_string(int status);
 

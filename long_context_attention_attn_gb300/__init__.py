@@ -28,7 +28,7 @@ EXPORTS = (
     "attn_read_device_status", "attn_status_string", "attn_fwd_noalloc",
     "attn_fwd_test_timeout", "attn_segments_from_seqlens", "attn_fwd_noalloc_status",
     "attn_tile_order", "attn_kv_append", "attn_kv_copy_pages", "attn_decode_workspace_bytes",
-    "attn_decode",
+    "attn_decode", "attn_decode_test_timeout",
 )
 
 
@@ -141,8 +141,10 @@ def lib() -> ctypes.CDLL:
         h.attn_kv_copy_pages.restype = c_int
         h.attn_decode_workspace_bytes.argtypes = [ctypes.POINTER(DecodeParams)]
         h.attn_decode_workspace_bytes.restype = ctypes.c_size_t
-        h.attn_decode.argtypes = [ctypes.POINTER(DecodeParams), vp]
-        h.attn_decode.restype = c_int
+        for name in ("attn_decode", "attn_decode_test_timeout"):
+            f = getattr(h, name)
+            f.argtypes = [ctypes.POINTER(DecodeParams), vp]
+            f.restype = c_int
         h.attn_status_string.argtypes = [c_int]
         h.attn_status_string.restype = ctypes.c_char_p
         _lib_handle = h

@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstring>
 
+#include "attn_decode.h"
 #include "internal.h"
 
 using namespace gb300;
@@ -539,7 +540,7 @@ size_t attn_decode_workspace_bytes(const attn_decode_params* p) {
   return n > 0 ? n : 256;
 }
 
-int attn_decode(const attn_decode_params* p, attn_stream_t stream) {
+static int decode_impl(const attn_decode_params* p, attn_stream_t stream, bool withhold) {
   const int rc = check_decode(p);
   if (rc != ATTN_OK) return rc;
   size_t need = 0;
@@ -547,7 +548,14 @@ int attn_decode(const attn_decode_params* p, attn_stream_t stream) {
   const cudaError_t e = decode_workspace(*p, &need);
   if (e != cudaSuccess) return ATTN_ERR_CUDA;
   if (need > 0 && (!p->workspace || p->workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
-  return cuda_status(launch_attn_decode(*p, reinterpret_cast<cudaStream_t>(stream)));
+  const cudaError_t l = launch_attn_decode(*p, withhold, reinterpret_cast<cudaStream_t>(stream));
+  return l == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : cuda_status(l);
+}
+
+int attn_decode(const attn_decode_params* p, attn_stream_t stream) { return decode_impl(p, stream, false); }
+
+int attn_decode_test_timeout(const attn_decode_params* p, attn_stream_t stream) {
+  return decode_impl(p, stream, true);
 }
 
 int attn_read_device_status(const void* workspace, attn_stream_t stream) {

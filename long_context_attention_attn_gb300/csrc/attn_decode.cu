@@ -33,6 +33,7 @@
 #include <cfloat>
 #include <type_traits>
 
+#include "attn_decode.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -66,6 +67,7 @@ struct DecodeArgs {
   int64_t page_stride;
   int n, s_q, h_q, h_kv, g, rows, row_tiles, max_pages, page_shift, num_pages;
   int window, sink, out_fp32;
+  int withhold;  // debug hook: copy nothing, so that every wait runs out (tensor memory only)
   int runs;     // of the list; row_tiles CTAs take each
   int cluster;  // CTAs per item (0: by the list)
   float scale_log2;
@@ -1138,6 +1140,7 @@ struct Kernel {
     return cudaSuccess;
   }
   static cudaError_t launch(DecodeArgs& a, const Shape& sh, cudaStream_t st) {
+    if (a.withhold && !T::kTensor) return cudaErrorNotSupported;
     a.row_tiles = sh.row_tiles;
     a.runs = sh.runs;
     a.cluster = sh.cluster;
@@ -1226,6 +1229,10 @@ cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes) {
 }
 
 cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
+  return launch_attn_decode(p, false, st);
+}
+
+cudaError_t launch_attn_decode(const attn_decode_params& p, bool withhold, cudaStream_t st) {
   const attn_kv_cache& c = p.cache;
   DecodeArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(p.q);
@@ -1251,6 +1258,7 @@ cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st) {
   a.window = p.window_left;
   a.sink = (int)p.sink_tokens;
   a.out_fp32 = p.out_fp32 ? 1 : 0;
+  a.withhold = withhold ? 1 : 0;
   a.scale_log2 = p.scale * 1.4426950408889634f;
   return dispatch(p, [&](auto k, const Shape& sh) { return k.launch(a, sh, st); });
 }

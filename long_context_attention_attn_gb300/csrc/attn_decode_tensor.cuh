@@ -17,6 +17,10 @@
 // an O of its own, put together at a piece's end: the softmax of a tile then takes a
 // warp half the time.
 //
+// Every wait ends: after a second it gives up and so do the CTA's others.  A thread that
+// gave up writes nothing that others read and arrives nowhere any more, so a softmax
+// thread that got through a piece has a right result, and the others' are NaN.
+//
 // HBM would take 1410 cycles per 128 keys at d = 128.  The softmax takes 2900 with
 // 128 rows and 1500 with 64 (one warp per scheduler, so latencies count), a thread's
 // eight products and their commit 700 to 800, the widening 1200; what a piece costs
@@ -280,7 +284,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     constexpr int kTurn = 16, kLanes = 2 * NB;  // blocks per turn, lanes per tile
     uint32_t i = 0;  // tiles so far
     bool ok = true;
-    while (walk.next(a, p, lane == 0, warp_sync)) {
+    while (!a.withhold && walk.next(a, p, lane == 0, warp_sync)) {
       const int* table = a.table + (int64_t)p.seq * a.max_pages;
       const int page_mask = (1 << a.page_shift) - 1;
       const int p_first = p.len - a.s_q, p_last = p.len - 1;  // query positions
@@ -344,7 +348,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     uint32_t i = 0, n = 0;
     bool ok = true;
     while (ok && walk.next(a, p, lane == 0, warp_sync)) {
-      ok = wait_on(&bars.q_full[n & 1], (n >> 1) & 1, ctx);
+      ok = __all_sync(0xffffffffu, wait_on(&bars.q_full[n & 1], (n >> 1) & 1, ctx));
       for (int t = p.t0; t < p.t1 && ok; t += NB, ++i) {
         const int buf = i % C::kKBufs;
         // its buffer holds S (or P) of two tiles before
@@ -406,14 +410,16 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     while (walk.next(a, p, (threadIdx.x & 127) == 0, group_sync)) {
       if (is_v) {
         if (ok && n > 1) ok = wait_on(&bars.done[n & 1], ((n >> 1) - 1) & 1, ctx);
-        if (a.s_q > 1)
+        if (ok && a.s_q > 1)
           for (int u = threadIdx.x & 127; u < D * 4; u += 128) s_nan(n)[u] = 0u;
-        if ((threadIdx.x & 127) == 0) s_any_nan[n & 1] = 0;
+        if (ok && (threadIdx.x & 127) == 0) s_any_nan[n & 1] = 0;
         group_sync();
         // ---- q's rows (a thread per row and copy) as f16, the largest value in [2^14,
         // 2^15), after the last S with the rows before them
         if (ok && i > 0) ok = wait_on(&bars.s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+      }
+      if (is_v && ok) {
         tc_fence_after();
         const int th = threadIdx.x & 127, row = p.rt * R + th % R;
         const bool mine = row < a.rows;
@@ -459,7 +465,8 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         if (wb >= NB) continue;
         const int slot = i % kStages;
         if (ok) ok = wait_on(&bars.full[slot], (i / kStages) & 1, ctx);
-        __syncwarp();
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) continue;
         const uint8_t* base = smem + slot * 2 * C::kCodes + (is_v ? C::kCodes : 0);
         const int k = wb * 32 + lane, m = i % C::kMeta;  // this thread's key of the tile
         uint32_t w[D / 4];
@@ -513,11 +520,12 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         mbar_arrive(&bars.free[slot]);
         // the f16 tile that was there has been multiplied
         if (is_v) {
-          if (ok && i >= C::kVBufs) ok = wait_on(&bars.o_done[i & 1], ((i >> 1) - 1) & 1, ctx);
-        } else if (ok && i >= C::kKBufs) {
+          if (i >= C::kVBufs) ok = wait_on(&bars.o_done[i & 1], ((i >> 1) - 1) & 1, ctx);
+        } else if (i >= C::kKBufs) {
           const uint32_t j = i - C::kKBufs;
           ok = wait_on(&bars.s_full[j & 1], (j >> 1) & 1, ctx);
         }
+        if (!ok) continue;
         uint8_t* dst = smem + (is_v ? C::v_off + i % C::kVBufs * C::kHalf : C::k_off + i % C::kKBufs * C::kHalf);
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {  // 8 d's
@@ -531,7 +539,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         fence_proxy_async_smem();
         mbar_arrive(is_v ? &bars.v_full[i % C::kVBufs] : &bars.k_full[i % C::kKBufs]);
       }
-      if (is_v) mbar_arrive(&bars.widened[n & 1]);
+      if (is_v && ok) mbar_arrive(&bars.widened[n & 1]);
       ++n;
     }
   } else {
@@ -676,7 +684,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         }
         if constexpr (C::kPBufs > 0) {
           tc_fence_before();
-          mbar_arrive(&bars.s_free[i & 1]);
+          if (ok) mbar_arrive(&bars.s_free[i & 1]);
           // P's place is free after its last O
           if (ok && i >= C::kPBufs) {
             const uint32_t j = i - C::kPBufs;
@@ -698,7 +706,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           tmem_wait_st();
         }
         tc_fence_before();
-        mbar_arrive(&bars.p_full[i & 1]);
+        if (ok) mbar_arrive(&bars.p_full[i & 1]);
       }
       if (ok) ok = wait_on(&bars.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
       if (ok) ok = wait_on(&bars.widened[n & 1], (n >> 1) & 1, ctx);
@@ -790,7 +798,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         }
       }
       tc_fence_before();
-      mbar_arrive(&bars.done[n & 1]);
+      if (ok) mbar_arrive(&bars.done[n & 1]);
       ++n;
     }
   }
