@@ -749,7 +749,10 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           tmem_ld32(t_o + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) o[j] = o[j] * w * w2;
+          for (int j = 0; j < 32; j += 2) {
+            mul_f32x2(o[j], o[j + 1], o[j], o[j + 1], w, w);
+            mul_f32x2(o[j], o[j + 1], o[j], o[j + 1], w2, w2);
+          }
           if (nans) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -780,7 +783,10 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           tmem_ld32(t_o + c, reinterpret_cast<uint32_t*>(o));
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) buf[th * 33 + j] = o[j] * w * w2;
+          for (int j = 0; j < 32; j += 2) {
+            mul_f32x2(o[j], o[j + 1], o[j], o[j + 1], w, w);
+            mul_f32x2(buf[th * 33 + j], buf[th * 33 + j + 1], o[j], o[j + 1], w2, w2);
+          }
           group_sync();
           for (int q = wq; q < rows; q += kWarps) {
             float x = 0.f;
