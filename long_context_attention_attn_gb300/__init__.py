@@ -504,8 +504,9 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
     Sequence i's new tokens are row i's first ``lens[i]`` (n = b; all s without
     ``lens``), or with ``tok_start`` int32 [n] the ``lens[i]`` tokens from flat
     token ``tok_start[i]`` of the b * s on (packed prompts).  ``max_new`` bounds
-    lens and sizes the launch (default: s, with ``tok_start`` b * s).  Each
-    page's scale is the smallest power of two that fits its values; where a
+    lens (without them it is every sequence's length) and sizes the launch: give
+    the longest of packed prompts (default: s, with ``tok_start`` b * s).  Several
+    sequences with ``tok_start`` need ``lens`` or ``max_new``.  Each page's scale is the smallest power of two that fits its values; where a
     page already holds tokens the larger of that and its scale is kept and
     grown scales requantise them.  Pages shared between sequences are copied
     first (:func:`kv_cache_copy_pages`)."""
@@ -524,6 +525,9 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
     n, max_pages = page_table.shape
     if tok_start is None and n != b:
         raise ValueError("page_table must have a row per row of k (or pass tok_start)")
+    if tok_start is not None and lens is None and max_new is None and n > 1:
+        # (each would take all tokens behind its first, those of the sequences after it too)
+        raise ValueError("tok_start for several sequences needs lens (or max_new)")
     most = s if tok_start is None else b * s
     p = KvAppendParams(
         cache, k.data_ptr(), v.data_ptr(), b * s, step,

@@ -76,3 +76,15 @@ def test_pages_of_stride_zero_are_refused(ga):
     with pytest.raises(ValueError):
         ga.workspace_bytes_decode(_kv(1, 1), *cache, table, one)
     assert ga.calls == []
+
+
+def test_packed_sequences_need_lengths(ga):
+    """Without lengths each sequence would take all tokens from its first on, other sequences' too."""
+    k, table, two = _kv(1, 40), torch.zeros(2, 2, dtype=torch.int32), _i32(0, 0)
+    with pytest.raises(ValueError, match="lens"):
+        ga.kv_cache_append(k, k, *_cache(), table, two, tok_start=_i32(0, 25))
+    assert ga.calls == []
+    ga.kv_cache_append(k, k, *_cache(), table, two, tok_start=_i32(0, 25), lens=_i32(25, 15))
+    ga.kv_cache_append(k, k, *_cache(), table, two, tok_start=_i32(0, 20), max_new=20)
+    ga.kv_cache_append(k, k, *_cache(), table[:1], two[:1], tok_start=_i32(5))  # the rest of the row
+    assert [(c[1].max_new, bool(c[1].lens)) for c in ga.calls] == [(40, True), (20, False), (40, False)]
