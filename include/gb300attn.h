@@ -374,8 +374,9 @@ typedef struct attn_kv_cache {
 
 /* Appends new tokens to the cache.
  *  k, v       bf16 [tokens, h_kv, d], token rows token_stride elements apart
- *             (0 = h_kv * d; else >= h_kv * d and a multiple of 8), 16-byte
- *             aligned; a packed [b, s, h_kv, d] tensor has tokens = b * s
+ *             (0 = h_kv * d; else >= h_kv * d and a multiple of 8, the last row
+ *             no more than 2^46 behind the first), 16-byte aligned; a packed
+ *             [b, s, h_kv, d] tensor has tokens = b * s
  *  start      int32 [n]: where sequence i's first new token goes (the tokens
  *             cached before it); a negative start appends nothing
  *  lens       int32 [n] new tokens of each sequence, clamped to [0, max_new];

@@ -485,12 +485,13 @@ int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
       !aligned(p->start, 4) || !aligned(p->lens, 4) || !aligned(p->tok_start, 4))
     return ATTN_ERR_INVALID_ARG;
   if (p->tokens < 1 || p->max_new < 1 || p->row_tokens < 0) return ATTN_ERR_INVALID_ARG;
-  if (p->token_stride != 0 && (p->token_stride < c.h_kv * c.d || p->token_stride % 8 != 0 ||
-                               p->token_stride > (1ll << 24)))
+  if (p->token_stride != 0 && (p->token_stride < c.h_kv * c.d || p->token_stride % 8 != 0))
     return ATTN_ERR_INVALID_ARG;
-  if (p->tokens > (1ll << 36) || p->row_tokens > (1ll << 40) || p->max_new > (1ll << 30))
-    return ATTN_ERR_UNSUPPORTED;
   const int64_t ts = p->token_stride > 0 ? p->token_stride : c.h_kv * c.d;
+  // (the last row's offset then fits 64 bits with room to spare)
+  if (p->tokens > (1ll << 36) || ts > (1ll << 40) || p->tokens - 1 > (1ll << 46) / ts ||
+      p->row_tokens > (1ll << 40) || p->max_new > (1ll << 30))
+    return ATTN_ERR_UNSUPPORTED;
   const uint64_t in_bytes = ((uint64_t)(p->tokens - 1) * ts + c.h_kv * c.d) * 2;
   const uint64_t sc_bytes = (uint64_t)c.num_pages * c.h_kv * 4;
   for (const void* in : {p->k, p->v})
