@@ -536,6 +536,8 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
         None if lens is None else _index(lens, (n,), index, "lens"),
         None if tok_start is None else _index(tok_start, (n,), index, "tok_start"),
         s, most if max_new is None else min(int(max_new), most))
+    if b * s == 0 or n == 0:
+        return
     _check(_on_device(index, lib().attn_kv_append, ctypes.byref(p)), "attn_kv_append")
 
 
@@ -612,6 +614,8 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
     allocates its own)."""
     p, index, out, lse = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens,
                                         window_left, sink_tokens, scale, out, lse, out_fp32)
+    if q.shape[0] == 0:
+        return out, lse
     ref = ctypes.byref(p)
     if workspace is None:
         if torch._C._cuda_getDevice() == index:

@@ -88,3 +88,21 @@ def test_packed_sequences_need_lengths(ga):
     ga.kv_cache_append(k, k, *_cache(), table, two, tok_start=_i32(0, 20), max_new=20)
     ga.kv_cache_append(k, k, *_cache(), table[:1], two[:1], tok_start=_i32(5))  # the rest of the row
     assert [(c[1].max_new, bool(c[1].lens)) for c in ga.calls] == [(40, True), (20, False), (40, False)]
+
+
+def test_no_tokens_and_no_sequences(ga):
+    """Nothing to append is no error, as no pairs to copy are none; neither is an empty batch."""
+    table, none = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(0, dtype=torch.int32)
+    ga.kv_cache_append(_kv(2, 0), _kv(2, 0), *_cache(), table, _i32(0, 0))
+    ga.kv_cache_append(_kv(0, 5), _kv(0, 5), *_cache(), table[:0], none)
+    ga.kv_cache_append(_kv(1, 0), _kv(1, 0), *_cache(), table, _i32(0, 0), lens=_i32(0, 0), tok_start=_i32(0, 0))
+    ga.kv_cache_append(_kv(1, 7), _kv(1, 7), *_cache(), table[:0], none, lens=none, tok_start=none)
+    for q in (torch.zeros(0, 1, 4, 64, dtype=torch.bfloat16), torch.zeros(0, 3, 4, 64, dtype=torch.bfloat16)):
+        out, lse = ga.attn_decode(q, *_cache(), table[:0], none)
+        assert out.shape == q.shape and lse.shape == (0, 4, q.shape[1])
+    assert ga.calls == []
+    for bad in (lambda: ga.kv_cache_append(_kv(2, 0), _kv(2, 0), *_cache(), table, _i32(0)),
+                lambda: ga.kv_cache_append(_kv(0, 5, d=128), _kv(0, 5, d=128), *_cache(), table[:0], none),
+                lambda: ga.attn_decode(torch.zeros(0, 1, 4, 64), *_cache(), table[:0], none)):
+        with pytest.raises(ValueError):
+            bad()
