@@ -211,6 +211,12 @@ def _kv_token_stride(*ts) -> int:
     return 0 if ts_ == h * d else int(ts_)
 
 
+def _clamp32(x) -> int:
+    """The nearest 32-bit integer: what a field of that size means for a value past it (ctypes would
+    take the value modulo 2^32)."""
+    return max(-(1 << 31), min(int(x), (1 << 31) - 1))
+
+
 def _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, lse, out_fp32,
                 sink_tokens=0):
     b, s_q, hq, d = q.shape
@@ -221,12 +227,12 @@ def _fwd_params(q, k, v, q_ids, q_pos, kv_ids, kv_pos, window_left, scale, out, 
     p.kv_segment_ids, p.kv_segment_pos = kv_ids.data_ptr(), kv_pos.data_ptr()
     p.b, p.s_q, p.s_kv, p.h_q, p.h_kv, p.d = b, s_q, s_kv, hq, hkv, d
     p.d_v = v.shape[3] if v.shape[3] != d else 0  # 0: V has the head dim of q and k
-    p.window_left, p.window_right = int(window_left), 0
+    p.window_left, p.window_right = _clamp32(window_left), 0
     p.scale = float(d ** -0.5 if scale is None else scale)
     p.out_fp32 = 1 if out_fp32 else 0
     p.out = out.data_ptr() if out is not None else None
     p.lse = lse.data_ptr() if lse is not None else None
-    p.sink_tokens = int(sink_tokens)
+    p.sink_tokens = _clamp32(sink_tokens)
     return p
 
 
@@ -582,8 +588,8 @@ def _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, w
     max_pages = page_table.shape[1]
     return DecodeParams(
         cache, q.data_ptr(), _index(page_table, (n, max_pages), index, "page_table"), n, max_pages,
-        _index(seqlens, (n,), index, "seqlens"), s_q, h_q, int(window_left), 1 if out_fp32 else 0,
-        int(sink_tokens), d ** -0.5 if scale is None else float(scale), out.data_ptr(),
+        _index(seqlens, (n,), index, "seqlens"), s_q, h_q, _clamp32(window_left), 1 if out_fp32 else 0,
+        _clamp32(sink_tokens), d ** -0.5 if scale is None else float(scale), out.data_ptr(),
         lse.data_ptr()), index, out, lse
 
 

@@ -106,3 +106,31 @@ def test_no_tokens_and_no_sequences(ga):
                 lambda: ga.attn_decode(torch.zeros(0, 1, 4, 64), *_cache(), table[:0], none)):
         with pytest.raises(ValueError):
             bad()
+
+
+@pytest.mark.parametrize("given,held", [(5, 5), (-1, -1), ((1 << 31) - 1, (1 << 31) - 1), (1 << 31, (1 << 31) - 1),
+                                        (1 << 32, (1 << 31) - 1), ((1 << 40) + 3, (1 << 31) - 1),
+                                        (-(1 << 32), -(1 << 31))])
+def test_windows_past_32_bits_do_not_wrap(ga, given, held):
+    """The C struct holds 32 bits: a window beyond them is as good as the largest (positions are
+    below it), and one far below zero stays a refusal."""
+    import workload
+    q, k, v = workload.qkv(1, 16, 2, 1, 64)
+    ids, pos = workload.segments(1, 16, None)
+    p = ga._fwd_params(q, k, v, ids, pos, ids, pos, given, 0.1, q, q, False)
+    assert p.window_left == held
+    dp, _, _, _ = ga._decode_params(_kv(1, 1), *_cache(), torch.zeros(1, 2, dtype=torch.int32), _i32(1), given, 0,
+                                    None, None, None, False)
+    assert dp.window_left == held
+
+
+@pytest.mark.parametrize("given,code", [(1 << 32, 2), ((1 << 64) + 5, 2), (-(1 << 32), 1), (-(1 << 64), 1)])
+def test_kept_tokens_past_the_field_are_refused(ga, given, code):
+    import workload
+    q, k, v = workload.qkv(1, 16, 2, 1, 64)
+    ids, pos = workload.segments(1, 16, None)
+    p = ga._fwd_params(q, k, v, ids, pos, ids, pos, 4, 0.1, q, q, False, given)
+    assert ga.lib().attn_fwd(ctypes.byref(p), None) == code
+    dp, _, _, _ = ga._decode_params(_kv(1, 1), *_cache(), torch.zeros(1, 2, dtype=torch.int32), _i32(1), 4, given,
+                                    None, None, None, False)
+    assert ga.lib().attn_decode(ctypes.byref(dp), None) == code
