@@ -8,7 +8,9 @@
  * ATTN_ERR_UNSUPPORTED without launching anything; otherwise it enqueues its
  * kernels asynchronously on `stream` and returns ATTN_OK (or ATTN_ERR_CUDA if
  * a launch failed).  Nothing synchronises implicitly except
- * attn_read_device_status.
+ * attn_read_device_status.  Clear a parameter struct (memset) before setting
+ * its fields: 0 is the default of every optional one, also of those that a
+ * later header adds in its padding.
  *
  * Notation (pages: "Context parallelism and ring attention", sections "The
  * attention problem", "Online softmax", "Causal attention", "Load balance";
@@ -126,10 +128,10 @@ typedef struct attn_fwd_params {
   void* workspace;
   size_t workspace_bytes;
   int32_t merge_into_out;
+  int32_t sink_tokens; /* (where padding was: no other field's place depends on it) */
   void* out_final;
   int64_t kv_token_stride;
   int64_t d_v;
-  int64_t sink_tokens;
 } attn_fwd_params;
 
 /* Backward parameters: gradient of sum(out * dout) with respect to q, k, v

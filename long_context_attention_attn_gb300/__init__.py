@@ -49,9 +49,8 @@ class FwdParams(ctypes.Structure):
         ("scale", ctypes.c_float), ("out_fp32", ctypes.c_int32),
         ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
-        ("merge_into_out", ctypes.c_int32), ("out_final", ctypes.c_void_p),
-        ("kv_token_stride", ctypes.c_int64), ("d_v", ctypes.c_int64),
-        ("sink_tokens", ctypes.c_int64),
+        ("merge_into_out", ctypes.c_int32), ("sink_tokens", ctypes.c_int32),
+        ("out_final", ctypes.c_void_p), ("kv_token_stride", ctypes.c_int64), ("d_v", ctypes.c_int64),
     ]
 
 

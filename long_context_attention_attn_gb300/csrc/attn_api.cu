@@ -2,6 +2,7 @@
 #include <cudaTypedefs.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstring>
 
 #include "attn_decode.h"
@@ -10,6 +11,11 @@
 using namespace gb300;
 
 namespace {
+
+// The embedded forward parameters fix the places of the backward's.
+static_assert(sizeof(attn_fwd_params) == 184 && offsetof(attn_fwd_params, out_final) == 160 &&
+                  offsetof(attn_bwd_params, dout) == 184,
+              "parameter layout");
 
 // cuTensorMapEncodeTiled from the driver, looked up once per process (a
 // function-local static: initialised exactly once even when several host
