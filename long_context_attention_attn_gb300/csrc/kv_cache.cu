@@ -163,6 +163,8 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv_append_kernel(const Appe
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < T / 32; ++w) bits = max(bits, s_max[w]);
+  } else {
+    __syncwarp();
   }
   const int k = scale_exponent(__uint_as_float(bits));
   const float need = pow2f(k);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) kv_append_kernel(const Appe
       dst[u * T] = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
-  // every thread read the old scale before the barrier of the maximum
+  // every thread read the old scale before the barrier behind the maximum
   if (tid == 0) *scale = now;
 }
 
