@@ -427,7 +427,8 @@ GB300ATTN_API int attn_kv_copy_pages(const attn_kv_cache* cache, const int32_t* 
 
 /* Attention of the last s_q tokens of each sequence over the cache.
  *  q          bf16 [n, s_q, h_q, d], contiguous, 16-byte aligned; h_q % h_kv
- *             == 0; s_q * (h_q / h_kv) <= 1024
+ *             == 0; s_q * (h_q / h_kv) <= 1024 (every 128 of these rows, or
+ *             fewer, read the cache again: attn_fwd is for long prompts)
  *  seqlens    int32 [n]: tokens of sequence i, the new ones (appended before
  *             this call) among them; query t sits at position
  *             seqlens[i] - s_q + t.  A query at a negative position (a shorter
@@ -436,6 +437,11 @@ GB300ATTN_API int attn_kv_copy_pages(const attn_kv_cache* cache, const int32_t* 
  *             table, and (window_left < 0 or p - j <= window_left or
  *             j < sink_tokens).  Pages without a visible key are not read, so
  *             those behind the window may be given back (table entry -1).
+ *  max_pages  the table's width.  With the window it is all that the host knows
+ *             of the lengths: it decides whether one launch or two do the work.
+ *             Tables no wider than the longest sequence needs are the fastest
+ *             (a sequence of 4096 tokens 8.9 us, with a table for 128k tokens
+ *             11.5 us).
  *  scale      softmax scale
  *  out        bf16 (fp32 when out_fp32) [n, s_q, h_q, d];  lse fp32
  *             [n, h_q, s_q]: finished partials that attn_merge_partial takes

@@ -614,6 +614,8 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
     seqlens[i] - s_q + t (nothing is visible from a negative one: O = 0, lse =
     -inf).  ``window_left`` / ``sink_tokens`` as in :func:`attn_fwd`; pages
     that no query sees are not read and may be given back (table entry -1).
+    A table no wider than the longest sequence needs is the fastest: its width
+    is what the host knows of the lengths.
     With ``out_fp32`` out is a partial for :func:`attn_merge_partial`.  Calls
     that overlap on the GPU need a ``workspace`` each (by default each call
     allocates its own)."""

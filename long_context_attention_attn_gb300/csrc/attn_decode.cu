@@ -22,8 +22,9 @@
 //   S^T[keys, rows] = K q^T,  O^T[d, rows] += V^T P^T   (m16n8k16, f16 in, fp32
 // sums), so a group of 8 rows is one N tile and the 8-bit codes are widened to
 // f16 (exactly) once for all rows.  q enters as f16 after a power-of-two scale
-// of its row (its 8 bits fit; what lies 2^-38 below the row's largest value is
-// dropped), P as f16 relative to a running maximum (11 bits).
+// of its row (all of its 8 bits down to 2^-31 of the row's largest value; below
+// that off by 2^-39 of it at most), P as f16 relative to a running maximum (11
+// bits).
 // The sums over d and over keys do not care for order, so a thread takes its
 // d's as 16 neighbouring bytes of a key (K) or of four keys (V) and byte
 // permutes pair the keys: no transposing loads.
@@ -49,7 +50,7 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kRescale = 8.f;
 // P * v_scale is held 2^7 times larger (<= 2^15, f16 ends at 2^16): it keeps its 11
 // bits down to 2^-21 of the largest, where one key has nearly all the weight and a
-// zero code others decide the sum.
+// zero code others decide the sum; below that it is off by 2^-32 of the largest.
 constexpr float kShift = 7.f;
 
 struct DecodeArgs {
@@ -1187,8 +1188,8 @@ struct Kernel {
 // and where the list cuts the work a CTA widens each code for more rows: up to 32 rows
 // 32 (at d = 256 the registers end at 16), above 64 or 128 on the tensor-memory path.
 // 48 sequences of 100 to 12000 tokens, Hkv 8, us at 32 / 64 / 128 rows by the
-// warp-level kernel and by the other: d 64 109 / 208 / 407 and 157 / 165 / 271; d 128
-// 161 / 294 / 567 and 190 / 221 / 303; d 256 326 / 635 / 1252 and 364 / 438 / 453.
+// warp-level kernel and by the other: d 64 109 / 208 / 407 and 157 / 170 / 283; d 128
+// 161 / 294 / 567 and 190 / 232 / 300; d 256 326 / 635 / 1252 and 364 / 422 / 452.
 template <int D, typename F>
 cudaError_t with_rows(const attn_decode_params& p, F&& f) {
   auto use = [&](auto k) {
