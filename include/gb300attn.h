@@ -348,6 +348,50 @@ GB300ATTN_API int attn_fwd_noalloc(const attn_fwd_params* p, attn_stream_t strea
  * no counterpart to this call either. */
 GB300ATTN_API int attn_fwd_noalloc_status(attn_stream_t stream);
 
+/* Position rotation of attention's inputs (the pages pass q and k already
+ * turned).  Pair i of a head's rotated part turns by the angle pos * freqs[i]:
+ *   y1 = amplitude (x1 cos - x2 sin),  y2 = amplitude (x2 cos + x1 sin)
+ *  freqs        fp64 [rot / 2], 8-byte aligned: radians per position.  Angles
+ *               are taken modulo a turn in 64-bit fixed point: exact for every
+ *               32-bit position up to the rounding of freqs / 2 pi.
+ *  rot          values of a head that turn: a multiple of 16, 16 .. 256
+ *  offset       the first of them, a multiple of 8; rot + offset <= d
+ *  interleaved  0: pair i is values (i, i + rot / 2) of the rotated part;
+ *               1: values (2 i, 2 i + 1)
+ *  amplitude    finite and positive; 0 = 1 */
+typedef struct attn_rotation {
+  const double* freqs;
+  int64_t rot, offset;
+  int32_t interleaved;
+  float amplitude;
+} attn_rotation;
+
+/* Turns the rows of q and k by their positions, or gradients back.
+ *  q, k       bf16 (fp32 when fp32 != 0) [tokens, h, d], token rows *_stride
+ *             elements apart (0 = h * d; else >= h * d and whole multiples of
+ *             16 bytes), 16-byte aligned; h_q or h_k may be 0 (q or k is then
+ *             not read).  d: a multiple of 16, at most 256.
+ *  q_out, k_out  the same, with strides of their own; q_out == q with the same
+ *             stride turns in place, other overlaps of rows are refused.  What
+ *             of a head does not turn is copied (in place: stays).
+ *  pos        int32 [tokens], any values
+ *  inverse    1: by -pos * freqs, the gradient of the rotation: (dq, dk) in
+ *             place of (q, k)
+ * Products and sums are fp32, rounded once to the type of the rows. */
+typedef struct attn_rope_params {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  const int32_t* pos;
+  int64_t tokens, h_q, h_k, d;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  int32_t fp32, inverse;
+  attn_rotation rotation;
+} attn_rope_params;
+
+GB300ATTN_API int attn_rope(const attn_rope_params* p, attn_stream_t stream);
+
 /* A paged key / value cache held in 8 bits, with one scale per page and head.
  * The pages have no counterpart to it; it is the serving side of the packed
  * attention above (the same mask, GQA mapping, O and lse).

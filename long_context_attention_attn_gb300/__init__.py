@@ -9,6 +9,7 @@ the shared library is missing or a tensor is not on a CUDA device.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Optional
 
@@ -28,7 +29,7 @@ EXPORTS = (
     "attn_read_device_status", "attn_status_string", "attn_fwd_noalloc",
     "attn_fwd_test_timeout", "attn_segments_from_seqlens", "attn_fwd_noalloc_status",
     "attn_tile_order", "attn_kv_append", "attn_kv_copy_pages", "attn_decode_workspace_bytes",
-    "attn_decode", "attn_decode_test_timeout",
+    "attn_decode", "attn_decode_test_timeout", "attn_rope",
 )
 
 
@@ -93,6 +94,23 @@ class DecodeParams(ctypes.Structure):
     ]
 
 
+class Rotation(ctypes.Structure):
+    _fields_ = [
+        ("freqs", ctypes.c_void_p), ("rot", ctypes.c_int64), ("offset", ctypes.c_int64),
+        ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+    ]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+        ("pos", ctypes.c_void_p), ("tokens", ctypes.c_int64), ("h_q", ctypes.c_int64), ("h_k", ctypes.c_int64),
+        ("d", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64), ("fp32", ctypes.c_int32),
+        ("inverse", ctypes.c_int32), ("rotation", Rotation),
+    ]
+
+
 _lib_handle = None
 
 
@@ -144,6 +162,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(h, name)
             f.argtypes = [ctypes.POINTER(DecodeParams), vp]
             f.restype = c_int
+        h.attn_rope.argtypes = [ctypes.POINTER(RopeParams), vp]
+        h.attn_rope.restype = c_int
         h.attn_status_string.argtypes = [c_int]
         h.attn_status_string.restype = ctypes.c_char_p
         _lib_handle = h
@@ -459,6 +479,101 @@ def _index(t, shape, index: int, what: str) -> int:
     return t.data_ptr()
 
 
+def rope_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, method: str = "linear",
+                     trained: int = 4096, fast: float = 32.0, slow: float = 1.0, device="cuda"):
+    """Frequencies for :func:`rope`: fp64 [rot / 2] radians per position, pair i's base^(-2 i / rot).
+
+    For contexts ``factor`` times longer than the ``trained`` tokens: "linear" divides all of them by
+    factor (positions squeezed); "base" raises the base by factor^(rot / (rot - 2)) (the fastest pair as
+    before, the slowest divided by factor); "parts" divides those of fewer than ``slow`` turns in the
+    trained length by factor, keeps those of more than ``fast``, and mixes the two in proportion to the
+    turns between."""
+    if rot < 2 or rot % 2 or not factor > 0 or not base > 0:
+        raise ValueError("rope_frequencies: rot must be even, base and factor positive")
+    if method not in ("linear", "base", "parts"):
+        raise ValueError("rope_frequencies: method is linear, base or parts")
+    if method == "base" and rot > 2:
+        base = base * factor ** (rot / (rot - 2))
+    f = torch.pow(torch.tensor(base, dtype=torch.float64), -torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    if method == "linear":
+        f = f / factor
+    elif method == "parts":
+        keep = ((f * trained / (2 * math.pi) - slow) / (fast - slow)).clamp(0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    return f.to(device)
+
+
+def _rotation(freqs, index: int, interleaved: bool, offset: int, amplitude: float) -> Rotation:
+    if freqs.dim() != 1 or freqs.dtype != torch.float64 or not freqs.is_contiguous():
+        raise ValueError("freqs must be a contiguous fp64 [rot / 2] tensor")
+    if freqs.get_device() != index:
+        raise ValueError("all tensors of a call must be on one CUDA device")
+    if not 0.0 < amplitude < math.inf:
+        raise ValueError("amplitude must be positive and finite")
+    return Rotation(freqs.data_ptr(), 2 * freqs.shape[0], offset, 1 if interleaved else 0, amplitude)
+
+
+def _rope_call(q, k, pos, freqs, interleaved, offset, amplitude, q_out, k_out, inverse):
+    one = k if q is None else q
+    if one is None:
+        raise ValueError("rope: q or k must be given")
+    index = one.get_device()
+    if index < 0:
+        raise ValueError("gb300attn runs on CUDA tensors only")
+    if one.dim() != 4 or one.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("q / k must be bf16 or fp32 [b, s, h, d] tensors")
+    b, s, _, d = one.shape
+    p = RopeParams()
+    p.pos, p.tokens, p.d = _index(pos, (b, s), index, "pos"), b * s, d
+    p.fp32, p.inverse = one.dtype == torch.float32, inverse
+    p.rotation = _rotation(freqs, index, interleaved, offset, amplitude)
+    out = []
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{name}_out without {name}")
+            out.append(None)
+            continue
+        h = x.shape[2] if x.dim() == 4 else 0
+        if y is None:
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        for t, what in ((x, name), (y, name + "_out")):
+            if t.shape != (b, s, h, d) or t.dtype != one.dtype:
+                raise ValueError(f"{what}: q and k (and their outputs) share b, s, d and the type")
+            if t.get_device() != index:
+                raise ValueError("all tensors of a call must be on one CUDA device")
+        if name == "q":
+            p.q, p.q_out, p.h_q = x.data_ptr(), y.data_ptr(), h
+            p.q_stride, p.q_out_stride = _row_stride(x, "q"), _row_stride(y, "q_out")
+        else:
+            p.k, p.k_out, p.h_k = x.data_ptr(), y.data_ptr(), h
+            p.k_stride, p.k_out_stride = _row_stride(x, "k"), _row_stride(y, "k_out")
+        out.append(y)
+    if b * s > 0 and p.h_q + p.h_k > 0:
+        _check(_on_device(index, lib().attn_rope, ctypes.byref(p)), "attn_rope")
+    return tuple(out)
+
+
+def rope(q, k, pos, freqs, *, interleaved: bool = False, offset: int = 0, amplitude: float = 1.0, q_out=None,
+         k_out=None):
+    """Turns q and k by their positions.  Returns (q_out, k_out): new tensors, or those given; ``q_out=q``
+    turns in place.
+
+    q [b, s, Hq, d], k [b, s, Hkv, d] bf16 (or both fp32; either may be None, token rows may lie apart, as
+    in a packed [b, s, Hq + 2 Hkv, d]); pos int32 [b, s]; freqs fp64 [rot / 2] radians per position
+    (:func:`rope_frequencies`).  The ``rot`` values of each head from ``offset`` on turn (multiples of 16
+    and 8): pair i is values (i, i + rot / 2) of them, or (2 i, 2 i + 1) with ``interleaved``, and becomes
+    ``amplitude`` * (x1 cos - x2 sin, x2 cos + x1 sin) of pos * freqs[i].  The rest is copied."""
+    return _rope_call(q, k, pos, freqs, interleaved, offset, amplitude, q_out, k_out, 0)
+
+
+def rope_bwd(dq, dk, pos, freqs, *, interleaved: bool = False, offset: int = 0, amplitude: float = 1.0, dq_out=None,
+             dk_out=None):
+    """Gradients of :func:`rope`'s inputs from those of its outputs (what attn_bwd returns; bf16 or fp32):
+    the same by the negative angles.  ``dq_out=dq`` works in place.  Returns (dq_out, dk_out)."""
+    return _rope_call(dq, dk, pos, freqs, interleaved, offset, amplitude, dq_out, dk_out, 1)
+
+
 def _kv_cache(k_cache, v_cache, k_scale, v_scale):
     """The KvCache of a cache: k / v e4m3 (or uint8) [num_pages, h_kv, page_size, d], pages dense
     inside (they may be the halves of one buffer), scales fp32 [num_pages, h_kv].  Returns it
@@ -487,14 +602,14 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale):
                    pages, h, size, d, st[0] if pages > 1 and st[0] != page else 0), index, h, d
 
 
-def _row_stride(x) -> int:
+def _row_stride(x, what: str = "k / v") -> int:
     """Elements between consecutive token rows of [b, s, h, d] (sizes of one have no stride)."""
     (b, s, h, d), st = x.shape, x.stride()
     step = st[1] if s > 1 else st[0] if b > 1 else h * d
     if (d > 1 and st[3] != 1) or (h > 1 and st[2] != d) or (s > 1 and b > 1 and st[0] != s * step):
-        raise ValueError("k / v: heads must be contiguous and token rows evenly spaced")
+        raise ValueError(f"{what}: heads must be contiguous and token rows evenly spaced")
     if step < h * d:  # (0, as of an expanded tensor, would mean contiguous)
-        raise ValueError("k / v: token rows must not overlap")
+        raise ValueError(f"{what}: token rows must not overlap")
     return step
 
 

@@ -445,11 +445,74 @@ int inverse_reorder_causal_lb(const void* in, void* out, int64_t outer, int64_t 
                         stream);
 }
 
-// ---- the paged cache
 static bool overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
+
+// ---- position rotation
+static int check_rotation(const attn_rotation& r, int64_t d) {
+  if (!r.freqs || !aligned(r.freqs, 8) || r.rot < 1 || r.offset < 0) return ATTN_ERR_INVALID_ARG;
+  if (r.amplitude != 0.f && (!(r.amplitude > 0.f) || !std::isfinite(r.amplitude))) return ATTN_ERR_INVALID_ARG;
+  if (r.rot > d || r.offset > d - r.rot) return ATTN_ERR_INVALID_ARG;
+  if (r.rot % 16 || r.rot > 256 || r.offset % 8) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// Token rows: `width` bytes each, `stride` bytes apart.
+struct Rows {
+  const void* base;
+  int64_t width, stride, tokens;
+  uint64_t extent() const { return (uint64_t)(tokens - 1) * stride + width; }
+};
+
+static int check_rows(const Rows& r) {
+  if (!r.base || !aligned(r.base, 16) || r.stride < r.width || r.stride % 16) return ATTN_ERR_INVALID_ARG;
+  // (the last row's offset then fits 64 bits with room to spare)
+  if (r.tokens > (1ll << 36) || r.stride > (1ll << 41) || r.tokens - 1 > (1ll << 47) / r.stride)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// Whether some row of `a` shares bytes with some row of `b` (columns of one buffer do not).
+static bool rows_meet(const Rows& a, const Rows& b) {
+  if (!overlap(a.base, a.extent(), b.base, b.extent())) return false;
+  if (a.stride != b.stride) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.base), y = reinterpret_cast<uintptr_t>(b.base);
+  const int64_t ahead = x <= y ? (int64_t)((y - x) % a.stride) : (int64_t)(a.stride - 1 - (x - y - 1) % a.stride);
+  return ahead < a.width || a.stride - ahead < b.width;
+}
+
+// `out` takes what was in `in`: the same rows, or others.
+static bool turns_over(const Rows& in, const Rows& out) {
+  return (in.base != out.base || in.stride != out.stride) && rows_meet(in, out);
+}
+
+int attn_rope(const attn_rope_params* p, attn_stream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  if (p->tokens < 1 || p->h_q < 0 || p->h_k < 0 || p->h_q + p->h_k < 1 || p->d < 1) return ATTN_ERR_INVALID_ARG;
+  if (p->h_q > 65535 || p->h_k > 65535 || p->d > 256 || p->d % 16) return ATTN_ERR_UNSUPPORTED;
+  int rc = check_rotation(p->rotation, p->d);
+  if (rc != ATTN_OK) return rc;
+  if (!p->pos || !aligned(p->pos, 4)) return ATTN_ERR_INVALID_ARG;
+  if (p->q_stride < 0 || p->k_stride < 0 || p->q_out_stride < 0 || p->k_out_stride < 0 || p->q_stride > (1ll << 40) ||
+      p->k_stride > (1ll << 40) || p->q_out_stride > (1ll << 40) || p->k_out_stride > (1ll << 40))
+    return ATTN_ERR_INVALID_ARG;
+  const int64_t es = p->fp32 ? 4 : 2;
+  auto rows = [&](const void* base, int64_t h, int64_t stride) {
+    return Rows{base, h * p->d * es, (stride > 0 ? stride : h * p->d) * es, p->tokens};
+  };
+  const Rows q = rows(p->q, p->h_q, p->q_stride), k = rows(p->k, p->h_k, p->k_stride);
+  const Rows qo = rows(p->q_out, p->h_q, p->q_out_stride), ko = rows(p->k_out, p->h_k, p->k_out_stride);
+  for (const Rows* r : {&q, &qo, &k, &ko})
+    if (r->width > 0 && (rc = check_rows(*r)) != ATTN_OK) return rc;
+  if ((q.width > 0 && turns_over(q, qo)) || (k.width > 0 && turns_over(k, ko))) return ATTN_ERR_INVALID_ARG;
+  if (q.width > 0 && k.width > 0 && (rows_meet(q, ko) || rows_meet(k, qo) || rows_meet(qo, ko)))
+    return ATTN_ERR_INVALID_ARG;
+  return cuda_status(launch_rope(*p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---- the paged cache
 
 // Bytes from the first to the last value of k (or v).
 static uint64_t cache_extent(const attn_kv_cache& c) {

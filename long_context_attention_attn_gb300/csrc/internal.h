@@ -264,6 +264,9 @@ cudaError_t launch_kv_append(const attn_kv_append_params& p, cudaStream_t st);
 cudaError_t launch_kv_copy(const attn_kv_cache& c, const int* src, const int* dst, int64_t n,
                            cudaStream_t st);
 
+// ---- rope.cu
+cudaError_t launch_rope(const attn_rope_params& p, cudaStream_t st);
+
 // ---- attn_decode.cu
 cudaError_t decode_workspace(const attn_decode_params& p, size_t* bytes);
 cudaError_t launch_attn_decode(const attn_decode_params& p, cudaStream_t st);
