@@ -459,6 +459,27 @@ typedef struct attn_kv_append_params {
 
 GB300ATTN_API int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream);
 
+/* attn_kv_append with the rotation applied on the way: the new token at position
+ * start[i] + j of sequence i has its K turned by that position before it is
+ * scaled and rounded (once: fp32 in between), and its row of q beside them.
+ *  append     as for attn_kv_append
+ *  q          bf16 [append.tokens, h_q, d], token rows q_stride elements apart
+ *             (as token_stride), or NULL with h_q = 0
+ *  q_out      the same with q_out_stride; q_out == q with the same stride turns
+ *             in place.  Rows of every sequence's new tokens are written, those
+ *             past the page table among them; all other rows stay as they are.
+ * A row of q that belongs to two sequences is not turned in place (the result
+ * would be unspecified). */
+typedef struct attn_kv_append_rope_params {
+  attn_kv_append_params append;
+  attn_rotation rotation;
+  const void* q;
+  void* q_out;
+  int64_t h_q, q_stride, q_out_stride;
+} attn_kv_append_rope_params;
+
+GB300ATTN_API int attn_kv_append_rope(const attn_kv_append_rope_params* p, attn_stream_t stream);
+
 /* Copies whole pages of K and V with their scales inside a cache: page src[i]
  * to page dst[i] for i < n_pairs (int32 device arrays).  Forking a sequence
  * shares its full pages and copies the last one; compaction moves pages to

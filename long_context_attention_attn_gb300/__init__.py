@@ -29,7 +29,7 @@ EXPORTS = (
     "attn_read_device_status", "attn_status_string", "attn_fwd_noalloc",
     "attn_fwd_test_timeout", "attn_segments_from_seqlens", "attn_fwd_noalloc_status",
     "attn_tile_order", "attn_kv_append", "attn_kv_copy_pages", "attn_decode_workspace_bytes",
-    "attn_decode", "attn_decode_test_timeout", "attn_rope",
+    "attn_decode", "attn_decode_test_timeout", "attn_rope", "attn_kv_append_rope",
 )
 
 
@@ -111,6 +111,13 @@ class RopeParams(ctypes.Structure):
     ]
 
 
+class KvAppendRopeParams(ctypes.Structure):
+    _fields_ = [
+        ("append", KvAppendParams), ("rotation", Rotation), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("h_q", ctypes.c_int64), ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+    ]
+
+
 _lib_handle = None
 
 
@@ -154,6 +161,8 @@ def lib() -> ctypes.CDLL:
         h.attn_segments_from_seqlens.restype = c_int
         h.attn_kv_append.argtypes = [ctypes.POINTER(KvAppendParams), vp]
         h.attn_kv_append.restype = c_int
+        h.attn_kv_append_rope.argtypes = [ctypes.POINTER(KvAppendRopeParams), vp]
+        h.attn_kv_append_rope.restype = c_int
         h.attn_kv_copy_pages.argtypes = [ctypes.POINTER(KvCache), vp, vp, i64, vp]
         h.attn_kv_copy_pages.restype = c_int
         h.attn_decode_workspace_bytes.argtypes = [ctypes.POINTER(DecodeParams)]
@@ -613,23 +622,8 @@ def _row_stride(x, what: str = "k / v") -> int:
     return step
 
 
-def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens=None,
-                    tok_start=None, max_new: Optional[int] = None):
-    """Appends new tokens to a paged 8-bit cache, in place.
-
-    k, v bf16 [b, s, h_kv, d] (or the halves of a packed [b, s, 2, h_kv, d]);
-    k_cache / v_cache float8_e4m3fn [num_pages, h_kv, page_size, d] with fp32
-    scales [num_pages, h_kv]; page_table int32 [n, max_pages]; start int32 [n]
-    the position of each sequence's first new token (negative: none).
-    Sequence i's new tokens are row i's first ``lens[i]`` (n = b; all s without
-    ``lens``), or with ``tok_start`` int32 [n] the ``lens[i]`` tokens from flat
-    token ``tok_start[i]`` of the b * s on (packed prompts).  ``max_new`` bounds
-    lens (without them it is every sequence's length) and sizes the launch: give
-    the longest of packed prompts (default: s, with ``tok_start`` b * s).  Several
-    sequences with ``tok_start`` need ``lens`` or ``max_new``.  Each page's scale is the smallest power of two that fits its values; where a
-    page already holds tokens the larger of that and its scale is kept and
-    grown scales requantise them.  Pages shared between sequences are copied
-    first (:func:`kv_cache_copy_pages`)."""
+def _append_params(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens, tok_start, max_new):
+    """(KvAppendParams, device index, whether there is anything to append)."""
     cache, index, h, d = _kv_cache(k_cache, v_cache, k_scale, v_scale)
     if (k.dim() != 4 or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16 or v.shape != k.shape
             or k.shape[2] != h or k.shape[3] != d):
@@ -649,16 +643,68 @@ def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start,
         # (each would take all tokens behind its first, those of the sequences after it too)
         raise ValueError("tok_start for several sequences needs lens (or max_new)")
     most = s if tok_start is None else b * s
-    p = KvAppendParams(
+    return KvAppendParams(
         cache, k.data_ptr(), v.data_ptr(), b * s, step,
         _index(page_table, page_table.shape, index, "page_table"), n, max_pages,
         _index(start, (n,), index, "start"),
         None if lens is None else _index(lens, (n,), index, "lens"),
         None if tok_start is None else _index(tok_start, (n,), index, "tok_start"),
-        s, most if max_new is None else min(int(max_new), most))
-    if b * s == 0 or n == 0:
-        return
-    _check(_on_device(index, lib().attn_kv_append, ctypes.byref(p)), "attn_kv_append")
+        s, most if max_new is None else min(int(max_new), most)), index, b * s > 0 and n > 0
+
+
+def kv_cache_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens=None,
+                    tok_start=None, max_new: Optional[int] = None):
+    """Appends new tokens to a paged 8-bit cache, in place.
+
+    k, v bf16 [b, s, h_kv, d] (or the halves of a packed [b, s, 2, h_kv, d]);
+    k_cache / v_cache float8_e4m3fn [num_pages, h_kv, page_size, d] with fp32
+    scales [num_pages, h_kv]; page_table int32 [n, max_pages]; start int32 [n]
+    the position of each sequence's first new token (negative: none).
+    Sequence i's new tokens are row i's first ``lens[i]`` (n = b; all s without
+    ``lens``), or with ``tok_start`` int32 [n] the ``lens[i]`` tokens from flat
+    token ``tok_start[i]`` of the b * s on (packed prompts).  ``max_new`` bounds
+    lens (without them it is every sequence's length) and sizes the launch: give
+    the longest of packed prompts (default: s, with ``tok_start`` b * s).  Several
+    sequences with ``tok_start`` need ``lens`` or ``max_new``.  Each page's scale is the smallest power of two that fits its values; where a
+    page already holds tokens the larger of that and its scale is kept and
+    grown scales requantise them.  Pages shared between sequences are copied
+    first (:func:`kv_cache_copy_pages`)."""
+    p, index, some = _append_params(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens, tok_start,
+                                    max_new)
+    if some:
+        _check(_on_device(index, lib().attn_kv_append, ctypes.byref(p)), "attn_kv_append")
+
+
+def kv_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, freqs, lens=None,
+                         tok_start=None, max_new: Optional[int] = None, *, interleaved: bool = False,
+                         offset: int = 0, amplitude: float = 1.0, q_out=None):
+    """:func:`kv_cache_append` with the rotation on the way: the new token at position start[i] + j has its K
+    turned as :func:`rope` would (rounded only once, to the cache's 8 bits), and its row of q beside them,
+    in one launch.  Returns q turned: ``q_out``, by default q itself (in place), None without q.
+
+    q bf16 [b, s, Hq, d] (or None) has the rows of k and v; freqs fp64 [rot / 2] and ``interleaved``,
+    ``offset``, ``amplitude`` as in :func:`rope`, the rest as in :func:`kv_cache_append`.  Rows of q that
+    belong to no sequence's new tokens stay as they are, those of q_out too; a row must not belong to two."""
+    a, index, some = _append_params(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens, tok_start,
+                                    max_new)
+    p = KvAppendRopeParams(a, _rotation(freqs, index, interleaved, offset, amplitude))
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+    else:
+        if q_out is None:
+            q_out = q
+        for t, what in ((q, "q"), (q_out, "q_out")):
+            if (t.dim() != 4 or t.dtype != torch.bfloat16 or t.shape[:2] != k.shape[:2] or t.shape[3] != k.shape[3]
+                    or t.shape[2] != q.shape[2]):
+                raise ValueError(f"{what} must be a bf16 [b, s, h_q, d] tensor with the rows and head dim of k")
+            if t.get_device() != index:
+                raise ValueError("all tensors of a call must be on one CUDA device")
+        p.q, p.q_out, p.h_q = q.data_ptr(), q_out.data_ptr(), q.shape[2]
+        p.q_stride, p.q_out_stride = _row_stride(q, "q"), _row_stride(q_out, "q_out")
+    if some:
+        _check(_on_device(index, lib().attn_kv_append_rope, ctypes.byref(p)), "attn_kv_append_rope")
+    return q_out
 
 
 def kv_cache_copy_pages(k_cache, v_cache, k_scale, v_scale, src, dst):

@@ -544,8 +544,7 @@ static int check_table(const attn_kv_cache& c, const int32_t* table, int64_t n, 
   return ATTN_OK;
 }
 
-int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
-  if (!p) return ATTN_ERR_INVALID_ARG;
+static int check_append(const attn_kv_append_params* p) {
   const attn_kv_cache& c = p->cache;
   int rc = check_cache(c);
   if (rc == ATTN_OK) rc = check_table(c, p->page_table, p->n, p->max_pages);
@@ -567,7 +566,44 @@ int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
     if (overlap(in, in_bytes, c.k, cache_extent(c)) || overlap(in, in_bytes, c.v, cache_extent(c)) ||
         overlap(in, in_bytes, c.k_scale, sc_bytes) || overlap(in, in_bytes, c.v_scale, sc_bytes))
       return ATTN_ERR_INVALID_ARG;
+  return ATTN_OK;
+}
+
+int attn_kv_append(const attn_kv_append_params* p, attn_stream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  const int rc = check_append(p);
+  if (rc != ATTN_OK) return rc;
   const cudaError_t e = launch_kv_append(*p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : cuda_status(e);
+}
+
+int attn_kv_append_rope(const attn_kv_append_rope_params* p, attn_stream_t stream) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  const attn_kv_append_params& ap = p->append;
+  const attn_kv_cache& c = ap.cache;
+  int rc = check_append(&ap);
+  if (rc == ATTN_OK) rc = check_rotation(p->rotation, c.d);
+  if (rc != ATTN_OK) return rc;
+  if (p->h_q < 0 || p->q_stride < 0 || p->q_out_stride < 0 || p->q_stride > (1ll << 40) ||
+      p->q_out_stride > (1ll << 40))
+    return ATTN_ERR_INVALID_ARG;
+  if (p->h_q > 65535) return ATTN_ERR_UNSUPPORTED;
+  if (p->h_q > 0) {
+    auto rows = [&](const void* base, int64_t h, int64_t stride) {
+      return Rows{base, h * c.d * 2, (stride > 0 ? stride : h * c.d) * 2, ap.tokens};
+    };
+    const Rows q = rows(p->q, p->h_q, p->q_stride), qo = rows(p->q_out, p->h_q, p->q_out_stride);
+    if ((rc = check_rows(q)) != ATTN_OK || (rc = check_rows(qo)) != ATTN_OK) return rc;
+    if (turns_over(q, qo) || rows_meet(qo, rows(ap.k, c.h_kv, ap.token_stride)) ||
+        rows_meet(qo, rows(ap.v, c.h_kv, ap.token_stride)))
+      return ATTN_ERR_INVALID_ARG;
+    const uint64_t sc_bytes = (uint64_t)c.num_pages * c.h_kv * 4;
+    for (const Rows* r : {&q, &qo})
+      if (overlap(r->base, r->extent(), c.k, cache_extent(c)) || overlap(r->base, r->extent(), c.v, cache_extent(c)) ||
+          overlap(r->base, r->extent(), c.k_scale, sc_bytes) || overlap(r->base, r->extent(), c.v_scale, sc_bytes))
+        return ATTN_ERR_INVALID_ARG;
+  }
+  const cudaError_t e = launch_kv_append_rope(*p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : cuda_status(e);
 }
 

@@ -261,6 +261,7 @@ cudaError_t launch_attn_bwd_split(const SplitLaunch& L, cudaStream_t st);
 
 // ---- kv_cache.cu
 cudaError_t launch_kv_append(const attn_kv_append_params& p, cudaStream_t st);
+cudaError_t launch_kv_append_rope(const attn_kv_append_rope_params& p, cudaStream_t st);
 cudaError_t launch_kv_copy(const attn_kv_cache& c, const int* src, const int* dst, int64_t n,
                            cudaStream_t st);
 
