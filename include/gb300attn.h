@@ -545,6 +545,42 @@ GB300ATTN_API int attn_decode(const attn_decode_params* p, attn_stream_t stream)
  * launched.  Not for production use. */
 GB300ATTN_API int attn_decode_test_timeout(const attn_decode_params* p, attn_stream_t stream);
 
+/* attn_decode for a batch whose sequences share their first pages (one
+ * instruction or document before many continuations): what a group shares is read
+ * once for all of its sequences.  The results are attn_decode's.
+ *  base          as for attn_decode: tables name every page, the shared ones too.
+ *                The workspace is attn_decode_shared_workspace_bytes()'.
+ *  shared_pages  int32 [n]: the first shared_pages[i] entries of row i of the page
+ *                table are the same in every row of i's group, and so is the
+ *                number; all of these pages' slots hold tokens of the shared
+ *                prefix.  A sequence may be shorter than that (an empty slot: 0
+ *                tokens) and sees the keys up to its last token.  Clamped to
+ *                [0, max_pages].
+ *  group_start   int32 [n_groups + 1]: group j is the sequences group_start[j] ..
+ *                group_start[j + 1] - 1; non-decreasing, 0 first and n last
+ *                (sequences of no group must have shared_pages 0); NULL with
+ *                n_groups = 1: all sequences are one group
+ *  max_group     the most sequences of a group (sizes the launch), 1 .. n; larger
+ *                groups are right, but slower.  With 1 nothing is shared and this is
+ *                attn_decode.
+ * Results are bit-identical from run to run, and differ from attn_decode's by the
+ * order of sums.  Where groups disagree with what is said here results are
+ * unspecified; no other memory is read or written. */
+typedef struct attn_decode_shared_params {
+  attn_decode_params base;
+  const int32_t* shared_pages;
+  const int32_t* group_start;
+  int64_t n_groups, max_group;
+} attn_decode_shared_params;
+
+/* Scratch size (bytes) on the current device; 0 on invalid sizes. */
+GB300ATTN_API size_t attn_decode_shared_workspace_bytes(const attn_decode_shared_params* p);
+GB300ATTN_API int attn_decode_shared(const attn_decode_shared_params* p, attn_stream_t stream);
+
+/* attn_decode_test_timeout for attn_decode_shared: the copies of the shared keys are
+ * withheld. */
+GB300ATTN_API int attn_decode_shared_test_timeout(const attn_decode_shared_params* p, attn_stream_t stream);
+
 /* Static description of a status code. */
 GB300ATTN_API const char* attn_status_string(int status);
 

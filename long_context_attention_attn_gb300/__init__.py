@@ -30,6 +30,7 @@ EXPORTS = (
     "attn_fwd_test_timeout", "attn_segments_from_seqlens", "attn_fwd_noalloc_status",
     "attn_tile_order", "attn_kv_append", "attn_kv_copy_pages", "attn_decode_workspace_bytes",
     "attn_decode", "attn_decode_test_timeout", "attn_rope", "attn_kv_append_rope",
+    "attn_decode_shared_workspace_bytes", "attn_decode_shared", "attn_decode_shared_test_timeout",
 )
 
 
@@ -91,6 +92,13 @@ class DecodeParams(ctypes.Structure):
         ("out_fp32", ctypes.c_int32), ("sink_tokens", ctypes.c_int64), ("scale", ctypes.c_float),
         ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
+class DecodeSharedParams(ctypes.Structure):
+    _fields_ = [
+        ("base", DecodeParams), ("shared_pages", ctypes.c_void_p), ("group_start", ctypes.c_void_p),
+        ("n_groups", ctypes.c_int64), ("max_group", ctypes.c_int64),
     ]
 
 
@@ -170,6 +178,12 @@ def lib() -> ctypes.CDLL:
         for name in ("attn_decode", "attn_decode_test_timeout"):
             f = getattr(h, name)
             f.argtypes = [ctypes.POINTER(DecodeParams), vp]
+            f.restype = c_int
+        h.attn_decode_shared_workspace_bytes.argtypes = [ctypes.POINTER(DecodeSharedParams)]
+        h.attn_decode_shared_workspace_bytes.restype = ctypes.c_size_t
+        for name in ("attn_decode_shared", "attn_decode_shared_test_timeout"):
+            f = getattr(h, name)
+            f.argtypes = [ctypes.POINTER(DecodeSharedParams), vp]
             f.restype = c_int
         h.attn_rope.argtypes = [ctypes.POINTER(RopeParams), vp]
         h.attn_rope.restype = c_int
@@ -799,6 +813,62 @@ def attn_decode(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, *,
         p.workspace = workspace.data_ptr()
         p.workspace_bytes = workspace.nbytes
     _check(_on_device(index, lib().attn_decode, ref), "attn_decode")
+    return out, lse
+
+
+def _shared_params(base, index: int, n: int, shared_pages, group_start, max_group) -> DecodeSharedParams:
+    if group_start is not None and (group_start.dim() != 1 or group_start.shape[0] < 2):
+        raise ValueError("group_start must be a contiguous int32 [n_groups + 1] tensor")
+    return DecodeSharedParams(
+        base, _index(shared_pages, (n,), index, "shared_pages"),
+        None if group_start is None else _index(group_start, group_start.shape, index, "group_start"),
+        1 if group_start is None else group_start.shape[0] - 1, n if max_group is None else int(max_group))
+
+
+def workspace_bytes_decode_shared(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, shared_pages,
+                                  group_start=None, *, max_group: Optional[int] = None, window_left: int = -1,
+                                  sink_tokens: int = 0) -> int:
+    """Workspace bytes attn_decode_shared needs for these arguments on q's device (0 if it rejects them; 256
+    where it uses none)."""
+    base, index, _, _ = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
+                                       sink_tokens, None, None, None, False)
+    p = _shared_params(base, index, q.shape[0], shared_pages, group_start, max_group)
+    with torch.cuda.device(index):
+        return lib().attn_decode_shared_workspace_bytes(ctypes.byref(p))
+
+
+def attn_decode_shared(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, shared_pages, group_start=None, *,
+                       max_group: Optional[int] = None, window_left: int = -1, sink_tokens: int = 0,
+                       scale: Optional[float] = None, out=None, lse=None, out_fp32: bool = False,
+                       workspace: Optional[torch.Tensor] = None):
+    """:func:`attn_decode` for sequences that share their first pages (one instruction or document before
+    many continuations): what a group shares is read once for all of its sequences.  Returns (out, lse).
+
+    The first ``shared_pages[i]`` (int32 [n]) entries of row i of the page table, full pages all, are those of
+    every sequence of i's group; group j is the sequences group_start[j] .. group_start[j + 1] - 1 (int32
+    [n_groups + 1], from 0 to n; None: all sequences are one group).  ``max_group`` is the most sequences
+    of a group (default: n); it decides how many rows a CTA takes.  The rest is as in
+    :func:`attn_decode`, whose results these are but for the order of sums."""
+    base, index, out, lse = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
+                                           sink_tokens, scale, out, lse, out_fp32)
+    p = _shared_params(base, index, q.shape[0], shared_pages, group_start, max_group)
+    if q.shape[0] == 0:
+        return out, lse
+    ref = ctypes.byref(p)
+    if workspace is None:
+        if torch._C._cuda_getDevice() == index:
+            need = lib().attn_decode_shared_workspace_bytes(ref)
+        else:
+            with torch.cuda.device(index):
+                need = lib().attn_decode_shared_workspace_bytes(ref)
+        if need > 256:  # (256: the call uses none)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's device")
+    if workspace is not None:
+        p.base.workspace = workspace.data_ptr()
+        p.base.workspace_bytes = workspace.nbytes
+    _check(_on_device(index, lib().attn_decode_shared, ref), "attn_decode_shared")
     return out, lse
 
 

@@ -664,6 +664,42 @@ int attn_decode_test_timeout(const attn_decode_params* p, attn_stream_t stream) 
   return decode_impl(p, stream, true);
 }
 
+static int check_decode_shared(const attn_decode_shared_params* p) {
+  if (!p) return ATTN_ERR_INVALID_ARG;
+  const int rc = check_decode(&p->base);
+  if (rc != ATTN_OK) return rc;
+  if (!p->shared_pages || !aligned(p->shared_pages, 4) || !aligned(p->group_start, 4) || p->n_groups < 1 ||
+      (!p->group_start && p->n_groups != 1) || p->max_group < 1 || p->max_group > p->base.n)
+    return ATTN_ERR_INVALID_ARG;
+  if (p->n_groups > 65535) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+size_t attn_decode_shared_workspace_bytes(const attn_decode_shared_params* p) {
+  size_t n = 0;
+  if (check_decode_shared(p) != ATTN_OK || decode_shared_workspace(*p, &n) != cudaSuccess) return 0;
+  return n > 0 ? n : 256;
+}
+
+static int decode_shared_impl(const attn_decode_shared_params* p, attn_stream_t stream, bool withhold) {
+  const int rc = check_decode_shared(p);
+  if (rc != ATTN_OK) return rc;
+  size_t need = 0;
+  if (!aligned(p->base.workspace, 256)) return ATTN_ERR_INVALID_ARG;
+  if (decode_shared_workspace(*p, &need) != cudaSuccess) return ATTN_ERR_CUDA;
+  if (need > 0 && (!p->base.workspace || p->base.workspace_bytes < need)) return ATTN_ERR_INVALID_ARG;
+  const cudaError_t l = launch_attn_decode_shared(*p, withhold, reinterpret_cast<cudaStream_t>(stream));
+  return l == cudaErrorNotSupported ? ATTN_ERR_UNSUPPORTED : cuda_status(l);
+}
+
+int attn_decode_shared(const attn_decode_shared_params* p, attn_stream_t stream) {
+  return decode_shared_impl(p, stream, false);
+}
+
+int attn_decode_shared_test_timeout(const attn_decode_shared_params* p, attn_stream_t stream) {
+  return decode_shared_impl(p, stream, true);
+}
+
 int attn_read_device_status(const void* workspace, attn_stream_t stream) {
   if (!workspace || !aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

@@ -1,6 +1,6 @@
 // The kernel for more rows than the warp-level one is good for (drafted tokens
 // times a large group): 64 or 128 rows per CTA on the tensor-memory path, included
-// by attn_decode.cu.
+// by attn_decode_kernels.cuh.
 //
 //   S[rows, keys] = q K^T,  O[rows, d] += P V   (f16 in, fp32 sums)
 //
@@ -33,21 +33,20 @@
 #pragma once
 
 // One piece of work: blocks [t0, t1) of an item; whole: all of it.
-struct TensorPiece {
-  int seq, kvh, rt, t0, t1, len;
+template <int M>
+struct TensorPiece : Piece<M> {
   bool whole;
-  Span span;
 };
 
 // A way through the CTA's run of the list, one per role, in shared memory: the
 // role's leader goes on, sync is the role's barrier.
-template <typename T>
+template <typename T, int M, int R>
 struct TensorWalk {
   int64_t at, end;
   int64_t seq_at;  // where the sequence starts in the list
   int seq;
   bool more;
-  TensorPiece piece;
+  TensorPiece<M> piece;
 
   // (one thread, after place)
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Placement& pl) {
@@ -65,14 +64,15 @@ struct TensorWalk {
     seq = t * pl.per;
     seq_at = pl.before[t] * a.h_kv;
     for (; seq < a.n - 1; ++seq) {
-      const int64_t c = (int64_t)span_of<T>(a, a.lens[seq]).weight * a.h_kv;
+      const Entry e = entry_of<T, M, R>(a, seq);
+      const int64_t c = (int64_t)e.span.weight * e.tiles * a.h_kv;
       if (at < seq_at + c) break;
       seq_at += c;
     }
   }
   // The next piece with a block, if there is one (false: the run is done).
   template <typename Sync>
-  __device__ __forceinline__ bool next(const DecodeArgs& a, TensorPiece& p, bool leader, Sync&& sync) {
+  __device__ __forceinline__ bool next(const DecodeArgs& a, TensorPiece<M>& p, bool leader, Sync&& sync) {
     sync();  // everybody has the last one
     if (leader) more = advance(a);
     sync();
@@ -83,10 +83,10 @@ struct TensorWalk {
  private:
   __device__ __forceinline__ bool advance(const DecodeArgs& a) {
     while (at < end && seq < a.n) {
-      TensorPiece p;
+      TensorPiece<M> p;
       p.seq = seq;
-      p.len = a.lens[seq];
-      p.span = span_of<T>(a, p.len);
+      const Entry entry = entry_of<T, M, R>(a, seq);
+      p.take(entry);
       if (p.span.count == 0) {
         ++seq;
         continue;
@@ -94,17 +94,22 @@ struct TensorWalk {
       // the piece [w0, w1) of the item's weight: its first kItemCost hold no block
       const int64_t in_seq = at - seq_at;
       const int weight = p.span.weight;
-      p.kvh = (int)(in_seq / weight);
+      const int item = (int)(in_seq / weight);
+      p.kvh = item;
       p.rt = blockIdx.x % a.row_tiles;
-      const int w0 = (int)(in_seq - (int64_t)p.kvh * weight);
+      const int w0 = (int)(in_seq - (int64_t)item * weight);
       const int w1 = (int)min((int64_t)weight, w0 + (end - at));
       p.t0 = max(w0 - T::kItemCost, 0);
       p.t1 = max(w1 - T::kItemCost, 0);
       p.whole = p.t0 == 0 && w1 == weight;
       at += w1 - w0;
-      if (w1 == weight && p.kvh == a.h_kv - 1) {
-        seq_at += (int64_t)weight * a.h_kv;
+      if (w1 == weight && item == a.h_kv * entry.tiles - 1) {
+        seq_at += (int64_t)weight * a.h_kv * entry.tiles;
         ++seq;
+      }
+      if constexpr (M == kShared) {
+        p.kvh = item / entry.tiles;
+        p.rt = item % entry.tiles;
       }
       if (p.t1 > p.t0) {
         piece = p;
@@ -197,7 +202,7 @@ __device__ __forceinline__ uint32_t p_col(uint32_t i) {
     return C::col_s + (i & 1) * C::kKeys;
 }
 
-template <int D, int NT>
+template <int D, int NT, int M>
 __global__ void __launch_bounds__(TensorCfg<D, NT>::kThreads, 1)
 attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v) {
@@ -220,7 +225,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     uint64_t drain[2];
   };
   __shared__ Bars bars;
-  __shared__ TensorWalk<T> walks[6];
+  __shared__ TensorWalk<T, M, R> walks[6];
   __shared__ int64_t before[kThreads + 1];
   // of a tile's groups of 16 keys: scales and whether they have a page; of its
   // blocks: the first key and whether every query sees all of them
@@ -261,7 +266,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     tmem_alloc(&s_tmem, C::kCols);
     tmem_relinquish();
   }
-  const Placement pl = place<T>(a, before);
+  const Placement pl = place<T, M, R>(a, before);
   // roles: 0 K, 1 V, 2 softmax, 3 S, 4 loader, 5 O
   const int role = warp < 12 ? warp >> 2 : warp - 9;
   if (lane == 0 && (warp >= 12 || (warp & 3) == 0)) walks[role].begin(a, pl);
@@ -270,13 +275,13 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const WaitCtx ctx{&s_abort, nullptr};
-  TensorWalk<T>& walk = walks[role];
+  TensorWalk<T, M, R>& walk = walks[role];
   auto warp_sync = [] { __syncwarp(); };
   auto group_sync = [&] { asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + role) : "memory"); };
   // of piece number n
   auto s_nan = [&](int n) { return reinterpret_cast<uint32_t*>(smem + C::nan_off) + (n & 1) * (D * 4); };
 
-  TensorPiece p;
+  TensorPiece<M> p;
   if (role == 4) {
     // ======================================================== loader
     // 16 blocks of keys at a time, a lane per group of 16 keys: their pages are looked
@@ -286,9 +291,22 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     uint32_t i = 0;  // tiles so far
     bool ok = true;
     while (!a.withhold && walk.next(a, p, lane == 0, warp_sync)) {
-      const int* table = a.table + (int64_t)p.seq * a.max_pages;
+      const int* table = p.table(a);
       const int page_mask = (1 << a.page_shift) - 1;
-      const int p_first = p.len - a.s_q, p_last = p.len - 1;  // query positions
+      int p_first = p.len - a.s_q, p_last = p.len - 1;  // query positions
+      if constexpr (M == kShared) {  // of the sequences that have rows here
+        const int rows = a.s_q * a.g, end = p.first + (min(p.rows(a), p.rt * R + R) - 1) / rows;
+        p_first = 0x7fffffff;
+        p_last = -1;
+        for (int m = p.first + p.rt * R / rows + lane; m <= end; m += 32) {
+          // (rows at negative positions see nothing: the fold leaves them out)
+          const int len = a.lens[m];
+          if (len > 0) p_first = min(p_first, max(len - a.s_q, 0));
+          p_last = max(p_last, len - 1);
+        }
+        p_first = __reduce_min_sync(0xffffffffu, p_first);
+        p_last = __reduce_max_sync(0xffffffffu, p_last);
+      }
       auto key_of = [&](int t) { return p.span.block(t + (lane >> 1)) * 32 + (lane & 1) * 16; };
       auto look_up = [&](int t) {
         return t + (lane >> 1) < p.t1 && key_of(t) < p.span.hi ? table[key_of(t) >> a.page_shift] : -1;
@@ -304,7 +322,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         const bool take = valid(pid0);
         const bool both = ((__ballot_sync(0xffffffffu, take) >> (lane & 30)) & 3u) == 3u;
         const bool all = both && key + 32 <= p.span.hi && (key >= p.span.lo || key + 32 <= p.span.sink_hi) &&
-                         key + 31 <= p_first && (a.window < 0 || p_last - key <= a.window || key + 31 < a.sink);
+                         key + 31 <= p_first && (a.window < 0 || p_last - key <= a.window || key + 31 < p.sink(a));
         for (int u = 0; u < kTurn && t + u < p.t1; u += NB, ++i) {
           const int slot = i % kStages;
           if (i >= kStages) ok = wait_on(&bars.free[slot], (i / kStages - 1) & 1, ctx);
@@ -411,7 +429,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     while (walk.next(a, p, (threadIdx.x & 127) == 0, group_sync)) {
       if (is_v) {
         if (ok && n > 1) ok = wait_on(&bars.done[n & 1], ((n >> 1) - 1) & 1, ctx);
-        if (ok && a.s_q > 1)
+        if (ok && (a.s_q > 1 || M == kShared))
           for (int u = threadIdx.x & 127; u < D * 4; u += 128) s_nan(n)[u] = 0u;
         if (ok && (threadIdx.x & 127) == 0) s_any_nan[n & 1] = 0;
         group_sync();
@@ -423,9 +441,8 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
       if (is_v && ok) {
         tc_fence_after();
         const int th = threadIdx.x & 127, row = p.rt * R + th % R;
-        const bool mine = row < a.rows;
-        const int tok = mine ? row / a.g : 0, head = p.kvh * a.g + (mine ? row - tok * a.g : 0);
-        const int64_t orow = ((int64_t)p.seq * a.s_q + tok) * a.h_q + head;
+        const bool mine = row < p.rows(a);
+        const int64_t orow = RowPlace<M>(a, p, mine ? row : 0).orow;
         const uint32_t my_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + orow * D);
         float amax = 0.f;
@@ -484,7 +501,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           const int key = block.x + lane;
           const bool some = s_ok[m][2 * wb + (lane >> 4)] && key < p.span.hi &&
                             (key >= p.span.lo || key < p.span.sink_hi);  // any query sees it
-          if (a.s_q > 1 && some) {
+          if ((a.s_q > 1 || M == kShared) && some) {
             // a NaN that not every query sees (0 * NaN is NaN) is left out of the
             // product and noted for those that do
             uint32_t any = 0u;
@@ -495,14 +512,14 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
             }
             if (any) {
               s_any_nan[n & 1] = 1;
-              const int rows = min(a.rows - p.rt * R, R);
+              const int rows = min(p.rows(a) - p.rt * R, R);
 #pragma unroll 1
               for (int r32 = 0; r32 < rows; r32 += 32) {
                 uint32_t mask = 0u;
 #pragma unroll 1
                 for (int r = r32; r < min(rows, r32 + 32); ++r) {
-                  const int q = p.len - a.s_q + (p.rt * R + r) / a.g;
-                  if (key <= q && (a.window < 0 || q - key <= a.window || key < a.sink)) mask |= 1u << (r & 31);
+                  const int q = RowPlace<M>(a, p, p.rt * R + r).pos;
+                  if (key <= q && (a.window < 0 || q - key <= a.window || key < p.sink(a))) mask |= 1u << (r & 31);
                 }
 #pragma unroll 1
                 for (int d = 0; d < D; ++d)
@@ -560,11 +577,11 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     bool ok = true;
     while (walk.next(a, p, th == 0, group_sync)) {
       const int row = p.rt * R + r;
-      const bool mine = row < a.rows;
-      const bool busy = p.rt * R + (wq * 32) % R < a.rows;  // this warp has rows
-      const int tok = mine ? row / a.g : 0, head = p.kvh * a.g + (mine ? row - tok * a.g : 0);
-      const int64_t orow = ((int64_t)p.seq * a.s_q + tok) * a.h_q + head;
-      const int pos = mine ? p.len - a.s_q + tok : -1;
+      const bool mine = row < p.rows(a);
+      const bool busy = p.rt * R + (wq * 32) % R < p.rows(a);  // this warp has rows
+      const RowPlace<M> to(a, p, mine ? row : 0);
+      const int64_t orow = to.orow;
+      const int pos = mine ? to.pos : -1;
       if (ok) ok = wait_on(&bars.q_full[n & 1], (n >> 1) & 1, ctx);
       const float fac = s_fac[n & 1][th];
       // the references of P and of P * v_scale (negated; at first below every score),
@@ -588,7 +605,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           auto sees = [&](int j) {  // key j of the tile
             const int key = s_block[m][j >> 5].x + (j & 31);
             return s_ok[m][j >> 4] && key < p.span.hi && key <= pos &&
-                   (a.window < 0 || pos - key <= a.window || key < a.sink);
+                   (a.window < 0 || pos - key <= a.window || key < p.sink(a));
           };
           float sum;
 #pragma unroll 1
@@ -738,7 +755,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
       const float lse2 = z == 0.f ? -INFINITY : ref + log2f(z);
       if (mine && copy == 0) {
         if (p.whole)
-          a.lse[((int64_t)p.seq * a.h_q + head) * a.s_q + tok] = lse2 * kLn2;
+          a.lse[to.lse] = lse_out<M>(lse2);
         else
           a.part_lse[part * R + r] = lse2;
       }
@@ -760,7 +777,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
               if ((s_nan(n)[(c + j) * 4 + wq] >> lane) & 1u) o[j] = bad;
           }
           if (!mine) continue;
-          if (p.whole && !a.out_fp32) {
+          if (M == kWhole && p.whole && !a.out_fp32) {
             uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + c);
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
@@ -777,7 +794,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         // the copies' sum through shared memory, a d per lane
         float* buf = reinterpret_cast<float*>(smem + C::sum_off);
         const int64_t* s_orow = reinterpret_cast<const int64_t*>(smem + C::row_off);
-        const int rows = min(a.rows - p.rt * R, R);
+        const int rows = min(p.rows(a) - p.rt * R, R);
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           float o[32];
@@ -796,7 +813,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
             if (nans && ((s_nan(n)[(c + lane) * 4 + (q >> 5)] >> (q & 31)) & 1u)) x = bad;
             if (!p.whole)
               a.part_o[(part * R + q) * D + c + lane] = x;
-            else if (a.out_fp32)
+            else if (M != kWhole || a.out_fp32)
               static_cast<float*>(a.out)[s_orow[q] * D + c + lane] = x;
             else
               static_cast<__nv_bfloat16*>(a.out)[s_orow[q] * D + c + lane] = __float2bfloat16_rn(x);
@@ -815,4 +832,6 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
+  // (this grid may begin before the one of the shared keys ends, but does not end before)
+  if constexpr (M == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
