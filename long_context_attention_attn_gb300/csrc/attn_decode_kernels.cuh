@@ -82,6 +82,7 @@ struct DecodeArgs {
   const int* shared_pages;
   const int* group_start;
   int n_seq;
+  int64_t copy_floats;  // between out (and lse) of a row's partials (attn_decode_group.cuh)
 };
 
 // How a kernel is cut.  A block of K and V is 8 KB (4 KB at d = 64): 32 keys, 16
@@ -93,6 +94,8 @@ struct DecodeArgs {
 // three CTAs and two slots 173 us (1.09 GB).
 template <int D, int NT>
 struct Tune {
+  // Shortest run: a shorter one would only add partials to fold.
+  static constexpr int kMinRun = 16;
   static constexpr bool kTensor = false;
   static constexpr int kBlock = D == 256 ? 16 : 32;
   static constexpr int kStages = (D == 128 && NT <= 2) || (D == 256 && NT == 1) ? 2 : 3;
@@ -115,6 +118,7 @@ struct Tune {
 // The kernel of 64 or 128 rows per CTA (attn_decode_tensor.cuh), one CTA per SM.
 template <int D>
 struct TensorTune {
+  static constexpr int kMinRun = 16;
   static constexpr bool kTensor = true;
   static constexpr int kBlock = 32;
   static constexpr int kStages = D == 64 ? 8 : 3;  // tiles of codes: of 128 keys (64 at d = 256)
@@ -132,8 +136,6 @@ struct Tune<D, 16> : TensorTune<D> {};
 // 512 tokens (Hq 32 Hkv 8 d 128) 17.3 us by the list, 15.6 us so; of up to 2048
 // 31.8 and 32.9.
 constexpr int kAloneBlocks = 4;
-// Shortest run: a shorter one would only add partials to fold.
-constexpr int kMinRun = 16;
 constexpr int kMaxCluster = 8;  // CTAs per item, at most (a size every GPU takes)
 
 // The blocks of keys that some query of a sequence of length `len` may see:
@@ -265,9 +267,9 @@ __device__ __forceinline__ Placement place(const DecodeArgs& a, int64_t* before)
   return place<M>(a, before, T::kBlock, T::kItemCost, R);
 }
 
-// Weight per CTA: an equal share of the list, and no less than kMinRun.
-__device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total) {
-  return max((total + a.runs - 1) / a.runs, (int64_t)kMinRun);
+// Weight per CTA: an equal share of the list, and no less than the shortest.
+__device__ __forceinline__ int64_t run_length(const DecodeArgs& a, int64_t total, int shortest) {
+  return max((total + a.runs - 1) / a.runs, (int64_t)shortest);
 }
 
 // ---------------------------------------------------------------- primitives
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     __shared__ int64_t before[kThreads + 1];
     const Placement pl = place<T, M, C::R>(a, before);
     const int64_t total = before[kThreads] * a.h_kv;
-    const int64_t run = run_length(a, total);
+    const int64_t run = run_length(a, total, T::kMinRun);
     at = blockIdx.x / a.row_tiles * run;
     end = min(at + run, total);
     if (at >= end) {
@@ -1161,7 +1163,7 @@ __global__ void __launch_bounds__(kFoldThreads) attn_decode_combine_kernel(const
   const int rt = blockIdx.x % a.row_tiles, kvh = blockIdx.x / a.row_tiles % a.h_kv;
   const int seq = blockIdx.x / (a.row_tiles * a.h_kv);
   const int64_t total = before[kThreads] * a.h_kv;
-  const int64_t run = run_length(a, total);
+  const int64_t run = run_length(a, total, T::kMinRun);
   const int t = seq / pl.per;
   int64_t seq_at = before[t];
   for (int i = t * pl.per; i < seq; ++i) seq_at += entry_of<T, kWhole, R>(a, i).span.weight;
@@ -1243,9 +1245,10 @@ struct Shape {
 
 template <int D, int NT, int M>
 struct Kernel {
-  static constexpr int kD = D;
+  static constexpr int kD = D, kCopies = 1;  // partials of a row
   using T = Tune<D, NT>;
   using C = std::conditional_t<T::kTensor, TensorCfg<D, NT>, Cfg<D, NT>>;
+  static constexpr int kPartRows = C::R;  // of a slot of partials
   // CTAs that fill the device once
   static cudaError_t resident(int* n) {
     static std::atomic<int> cache[kMaxDevices];
@@ -1301,7 +1304,7 @@ struct Kernel {
     }
     // no more than shortest runs
     const int64_t entries = M == kShared ? groups + p.n * rows / C::R : p.n;
-    const int64_t most = ((blocks + T::kItemCost) * entries * p.cache.h_kv + kMinRun - 1) / kMinRun;
+    const int64_t most = ((blocks + T::kItemCost) * entries * p.cache.h_kv + T::kMinRun - 1) / T::kMinRun;
     const int64_t runs = n / row_tiles > 1 ? n / row_tiles : 1;
     s->runs = most < runs ? (int)most : (int)runs;
     return cudaSuccess;

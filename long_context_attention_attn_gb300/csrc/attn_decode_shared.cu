@@ -19,103 +19,96 @@ namespace gb300 {
 
 namespace {
 
+#include "attn_decode_group.cuh"
+
 // What one list's kernel leaves.
 struct Part {
-  const float* part_o;    // pieces of items that several CTAs took
+  const float* part_o;    // pieces of items that several CTAs took: slots of part_rows rows
   const float* part_lse;
-  const float* whole_o;   // [n, s_q, h_q, D]: rows of items that one CTA took
-  const float* whole_lse; // [n, h_q, s_q]
-  int block, item_cost, tile, runs, row_tiles;
+  const float* whole_o;   // [copies][n, s_q, h_q, D]: rows of items that one CTA took
+  const float* whole_lse; // [copies][n, h_q, s_q]
+  int64_t copy_floats;    // between copies
+  int block, item_cost, shortest, tile, part_rows, copies, runs, row_tiles;
 };
 
-constexpr int kFoldMost = 32;  // pieces at a time
-
-// Where a row's pieces lie.
+// Where a row's partials lie.
 struct RowPieces {
   int64_t c0, s0, run;  // first CTA's run, first block of the item
-  int n, rt, in_tile;   // pieces, row tile, row in the tile
-};
-
-// A list with its runs, as its kernel cuts it.
-struct List {
-  DecodeArgs a;
-  Part part;
-  int64_t run;
+  int n, rt, in_tile;   // partials (copies of pieces), row tile, row in the tile
 };
 
 template <int M>
-__device__ __forceinline__ RowPieces pieces_of(const List& l, const Entry& e, int64_t entry_at, int kvh, int row) {
+__device__ __forceinline__ RowPieces pieces_of(const Part& l, int64_t run, const Entry& e, int64_t entry_at, int kvh,
+                                               int row) {
   RowPieces p;
-  p.rt = row / l.part.tile;
-  p.in_tile = row - p.rt * l.part.tile;
+  p.rt = row / l.tile;
+  p.in_tile = row - p.rt * l.tile;
   const int64_t item = M == kShared ? (int64_t)kvh * e.tiles + p.rt : kvh;
-  p.s0 = entry_at + item * e.span.weight + l.part.item_cost;
-  p.run = l.run;
-  p.c0 = p.s0 / l.run;
-  p.n = e.span.count ? (int)((p.s0 + e.span.count - 1) / l.run - p.c0) + 1 : 0;
+  p.s0 = entry_at + item * e.span.weight + l.item_cost;
+  p.run = run;
+  p.c0 = p.s0 / run;
+  p.n = e.span.count ? ((int)((p.s0 + e.span.count - 1) / run - p.c0) + 1) * l.copies : 0;
   if (M == kShared) p.rt = 0;  // (a CTA's run has all of its tiles)
   return p;
 }
 
-// Row of part_o / part_lse of piece i.
-__device__ __forceinline__ int64_t piece_row(const Part& l, const RowPieces& p, int i) {
-  // a piece that starts inside its item is the first of its CTA, one that ends inside it the last
-  const int64_t slot = 2 * ((p.c0 + i) * l.row_tiles + p.rt) + ((p.c0 + i) * p.run <= p.s0 ? 1 : 0);
-  return slot * l.tile + p.in_tile;
-}
+constexpr int kFoldMost = 64;  // partials at a time
 
-// One thread per four values of a row, the rows of an item over blockIdx.y.
+// The rows of a sequence and kv head over blockIdx.y, a thread per four values; where a CTA
+// has fewer rows than its threads hold, several threads share a row's partials.
 template <int D>
 __global__ void __launch_bounds__(kFoldThreads)
     decode_shared_fold_kernel(const DecodeArgs a, const Part shared, const Part own, int n_groups) {
   constexpr int kVec = D / 4, RP = kFoldThreads / kVec;
   __shared__ int64_t before_s[kThreads + 1], before_o[kThreads + 1];
   __shared__ RowPieces rows_s[RP], rows_o[RP];
+  __shared__ const float* s_src[kFoldMost][RP];
   __shared__ float s_w[kFoldMost][RP];
   __shared__ float s_ref[RP], s_old[RP];
+  __shared__ float4 s_acc[kFoldThreads];
+  __shared__ float s_z[kFoldThreads / kVec];
   __shared__ int s_most;
-  List ls{a, shared, 0}, lo{a, own, 0};
-  ls.a.n = n_groups;
-  ls.a.runs = shared.runs;
-  lo.a.runs = own.runs;
-  const Placement ps = place<kShared>(ls.a, before_s, shared.block, shared.item_cost, shared.tile);
-  const Placement po = place<kOwn>(lo.a, before_o, own.block, own.item_cost, own.tile);
-  ls.run = run_length(ls.a, before_s[kThreads] * a.h_kv);
-  lo.run = run_length(lo.a, before_o[kThreads] * a.h_kv);
+  DecodeArgs as = a, ao = a;
+  as.n = n_groups;
+  as.runs = shared.runs;
+  ao.runs = own.runs;
+  const Placement ps = place<kShared>(as, before_s, shared.block, shared.item_cost, shared.tile);
+  const Placement po = place<kOwn>(ao, before_o, own.block, own.item_cost, own.tile);
   const int kvh = blockIdx.x % a.h_kv, seq = blockIdx.x / a.h_kv, r0 = blockIdx.y * RP;
+  const int rows = min(RP, a.rows - r0);
   if (threadIdx.x == 0) s_most = 0;
   __syncthreads();
-  if (threadIdx.x < RP) {
+  if (threadIdx.x < rows) {
     // the sequence's group: the last one that starts at or before it
-    int lo_g = 0, hi_g = n_groups;
-    while (hi_g - lo_g > 1) {
-      const int mid = (lo_g + hi_g) / 2;
+    int g = 0, end = n_groups;
+    while (end - g > 1) {
+      const int mid = (g + end) / 2;
       if (group_bound(a, mid) <= seq)
-        lo_g = mid;
+        g = mid;
       else
-        hi_g = mid;
+        end = mid;
     }
     const int row = r0 + threadIdx.x;
     RowPieces s, o;
-    s.n = o.n = 0;
-    if (row < a.rows) {
-      const Entry eg = entry_of<kShared>(ls.a, lo_g, shared.block, shared.item_cost, shared.tile);
-      const int in_group = seq - eg.first;
-      if (in_group >= 0 && (in_group + 1) * a.rows <= eg.rows && a.lens[seq] - a.s_q + row / a.g >= 0) {
-        const int t = lo_g / ps.per;
-        int64_t at = before_s[t];
-        for (int i = t * ps.per; i < lo_g; ++i) {
-          const Entry e = entry_of<kShared>(ls.a, i, shared.block, shared.item_cost, shared.tile);
-          at += (int64_t)e.span.weight * e.tiles;
-        }
-        s = pieces_of<kShared>(ls, eg, at * a.h_kv, kvh, in_group * a.rows + row);
+    s.n = 0;
+    const Entry eg = entry_of<kShared>(as, g, shared.block, shared.item_cost, shared.tile);
+    const int in_group = seq - eg.first;
+    if (in_group >= 0 && (in_group + 1) * a.rows <= eg.rows && a.lens[seq] - a.s_q + row / a.g >= 0) {
+      const int t = g / ps.per;
+      int64_t at = before_s[t];
+      for (int i = t * ps.per; i < g; ++i) {
+        const Entry e = entry_of<kShared>(as, i, shared.block, shared.item_cost, shared.tile);
+        at += (int64_t)e.span.weight * e.tiles;
       }
-      const int t = seq / po.per;
-      int64_t at = before_o[t];
-      for (int i = t * po.per; i < seq; ++i)
-        at += entry_of<kOwn>(lo.a, i, own.block, own.item_cost, own.tile).span.weight;
-      o = pieces_of<kOwn>(lo, entry_of<kOwn>(lo.a, seq, own.block, own.item_cost, own.tile), at * a.h_kv, kvh, row);
+      s = pieces_of<kShared>(shared, run_length(as, before_s[kThreads] * a.h_kv, shared.shortest), eg, at * a.h_kv, kvh,
+                             in_group * a.rows + row);
     }
+    const int t = seq / po.per;
+    int64_t at = before_o[t];
+    for (int i = t * po.per; i < seq; ++i)
+      at += entry_of<kOwn>(ao, i, own.block, own.item_cost, own.tile).span.weight;
+    o = pieces_of<kOwn>(own, run_length(ao, before_o[kThreads] * a.h_kv, own.shortest),
+                        entry_of<kOwn>(ao, seq, own.block, own.item_cost, own.tile), at * a.h_kv, kvh, row);
     rows_s[threadIdx.x] = s;
     rows_o[threadIdx.x] = o;
     atomicMax(&s_most, s.n + o.n);
@@ -126,62 +119,90 @@ __global__ void __launch_bounds__(kFoldThreads)
   // everything the two grids before this one wrote
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  struct Source {
-    const float* o;
-    const float* lse;
-  };
-  // piece i of the CTA's row r: its values and its lse
-  auto source = [&](int r, int i) {
-    const RowPieces& s = rows_s[r];
-    const bool sh = i < s.n;
-    const RowPieces& p = sh ? s : rows_o[r];
+  // Partial i of the CTA's row r: its values; its lse.
+  auto source = [&](int r, int i, const float*& lse) -> const float* {
+    const bool sh = i < rows_s[r].n;
+    const RowPieces& p = sh ? rows_s[r] : rows_o[r];
     const Part& l = sh ? shared : own;
-    if (p.n == 1) {
+    const int j = sh ? i : i - rows_s[r].n;
+    const int piece = j / l.copies, copy = j - piece * l.copies;
+    if (p.n == l.copies) {
       const int row = r0 + r, tok = row / a.g, head = kvh * a.g + row % a.g;
-      return Source{l.whole_o + (((int64_t)seq * a.s_q + tok) * a.h_q + head) * D,
-                    l.whole_lse + ((int64_t)seq * a.h_q + head) * a.s_q + tok};
+      lse = l.whole_lse + copy * l.copy_floats + ((int64_t)seq * a.h_q + head) * a.s_q + tok;
+      return l.whole_o + copy * l.copy_floats + (((int64_t)seq * a.s_q + tok) * a.h_q + head) * D;
     }
-    const int64_t at = piece_row(l, p, sh ? i : i - s.n);
-    return Source{l.part_o + at * D, l.part_lse + at};
+    // a piece that starts inside its item is the first of its CTA, one that ends inside it the last
+    const int64_t slot = 2 * ((p.c0 + piece) * l.row_tiles + p.rt) + ((p.c0 + piece) * p.run <= p.s0 ? 1 : 0);
+    const int64_t at = slot * l.part_rows + copy * l.tile + p.in_tile;
+    lse = l.part_lse + at;
+    return l.part_o + at * D;
   };
-  const int r = threadIdx.x / kVec, d4 = threadIdx.x % kVec;
+  const int q = threadIdx.x / kVec, d4 = threadIdx.x % kVec;
+  int held = 1;  // rows, as a power of two
+  while (held < rows) held *= 2;
+  const int ways = RP / held, r = q & (held - 1), way = q / held;
+  const bool mine = r < rows;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float z = 0.f;
   for (int b0 = 0; b0 < most; b0 += kFoldMost) {
     const int np = min(kFoldMost, most - b0);
-    for (int u = threadIdx.x; u < np * RP; u += kFoldThreads) {
-      const int i = u / RP, row = u % RP;
-      s_w[i][row] = b0 + i < rows_s[row].n + rows_o[row].n ? *source(row, b0 + i).lse : -INFINITY;
+    for (int u = threadIdx.x; u < np * held; u += kFoldThreads) {
+      const int i = u / held, row = u & (held - 1);
+      float w = -INFINITY;
+      const float* src = nullptr;
+      if (row < rows && b0 + i < rows_s[row].n + rows_o[row].n) {
+        const float* lse;
+        src = source(row, b0 + i, lse);
+        w = *lse;
+      }
+      s_w[i][row] = w;
+      s_src[i][row] = src;
     }
     __syncthreads();
-    if (threadIdx.x < RP) {
+    if (threadIdx.x < rows) {
       float top = s_ref[threadIdx.x];
       for (int i = 0; i < np; ++i) top = fmaxf(top, s_w[i][threadIdx.x]);
       s_old[threadIdx.x] = top == -INFINITY ? 0.f : ex2(s_ref[threadIdx.x] - top);
       s_ref[threadIdx.x] = top;
     }
     __syncthreads();
-    const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
-    z *= old;
-    acc.x *= old;
-    acc.y *= old;
-    acc.z *= old;
-    acc.w *= old;
-    const int mine = min(np, rows_s[r].n + rows_o[r].n - b0);
+    if (mine) {
+      const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
+      z *= old;
+      acc.x *= old;
+      acc.y *= old;
+      acc.z *= old;
+      acc.w *= old;
+      const int here = min(np, rows_s[r].n + rows_o[r].n - b0);
 #pragma unroll 4
-    for (int i = 0; i < mine; ++i) {
-      const float f = ex2(s_w[i][r] - ref);
-      const float4 v = reinterpret_cast<const float4*>(source(r, b0 + i).o)[d4];
-      z += f;
-      acc.x += v.x * f;
-      acc.y += v.y * f;
-      acc.z += v.z * f;
-      acc.w += v.w * f;
+      for (int i = way; i < here; i += ways) {
+        const float f = ex2(s_w[i][r] - ref);
+        const float4 v = reinterpret_cast<const float4*>(s_src[i][r])[d4];
+        z += f;
+        acc.x += v.x * f;
+        acc.y += v.y * f;
+        acc.z += v.z * f;
+        acc.w += v.w * f;
+      }
     }
     __syncthreads();
   }
+  if (ways > 1) {
+    s_acc[threadIdx.x] = acc;
+    if (d4 == 0) s_z[q] = z;
+    __syncthreads();
+    if (way > 0) return;
+    for (int w = 1; w < ways; ++w) {
+      const float4 v = s_acc[(w * held + r) * kVec + d4];
+      z += s_z[w * held + r];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+    }
+  }
+  if (!mine) return;
   const int row = r0 + r;
-  if (row >= a.rows) return;
   const float inv = z == 0.f ? 0.f : 1.f / z;
   const int tok = row / a.g, head = kvh * a.g + row % a.g;
   const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
@@ -199,10 +220,21 @@ __global__ void __launch_bounds__(kFoldThreads)
 template <int D, typename F>
 cudaError_t with_both(const attn_decode_shared_params& p, F&& f) {
   const attn_decode_params& q = p.base;
-  const int64_t rows = q.s_q * (q.h_q / q.cache.h_kv);
-  return with_rows<D, kShared>(q, p.n_groups, p.max_group * rows, [&](auto ks, const Shape& ss) {
+  const int64_t rows = q.s_q * (q.h_q / q.cache.h_kv), most = p.max_group * rows;
+  auto with_own = [&](auto ks, const Shape& ss) {
     return with_rows<D, kOwn>(q, 0, rows, [&](auto ko, const Shape& so) { return f(ks, ss, ko, so); });
-  });
+  };
+  if constexpr (D < 256) {
+    if (most > 32) {
+      auto use = [&](auto k) {
+        Shape sh;
+        const cudaError_t e = k.shape(q, p.n_groups, &sh);
+        return e == cudaSuccess ? with_own(k, sh) : e;
+      };
+      return most > 128 ? use(GroupKernel<D, false>()) : use(GroupKernel<D, true>());
+    }
+  }
+  return with_rows<D, kShared>(q, p.n_groups, most, with_own);
 }
 
 template <typename F>
@@ -215,14 +247,17 @@ cudaError_t dispatch(const attn_decode_shared_params& p, F&& f) {
 // Floats of a list's partials, and of a problem's rows.
 template <typename K>
 size_t part_floats(const Shape& sh, int64_t d) {
-  return align_up(2 * (size_t)sh.runs * sh.row_tiles * K::C::R * (d + 1), 64);
+  return align_up(2 * (size_t)sh.runs * sh.row_tiles * K::kPartRows * (d + 1), 64);
 }
 size_t row_floats(const attn_decode_params& p) { return align_up((size_t)p.n * p.s_q * p.h_q * (p.cache.d + 1), 64); }
 
 template <typename K>
 Part part_of(const DecodeArgs& a, const Shape& sh) {
-  return Part{a.part_o, a.part_lse, static_cast<const float*>(a.out), a.lse, K::T::kBlock, K::T::kItemCost, K::C::R,
-              sh.runs, sh.row_tiles};
+  return Part{a.part_o,        a.part_lse,       static_cast<const float*>(a.out),
+              a.lse,           a.copy_floats,    K::T::kBlock,
+              K::T::kItemCost, K::T::kMinRun,    K::C::R,
+              K::kPartRows,    K::kCopies,       sh.runs,
+              sh.row_tiles};
 }
 
 }  // namespace
@@ -230,8 +265,9 @@ Part part_of(const DecodeArgs& a, const Shape& sh) {
 cudaError_t decode_shared_workspace(const attn_decode_shared_params& p, size_t* bytes) {
   if (p.max_group <= 1) return decode_workspace(p.base, bytes);
   return dispatch(p, [&](auto ks, const Shape& ss, auto ko, const Shape& so) {
+    using KS = decltype(ks);
     *bytes = 4 * (part_floats<decltype(ks)>(ss, p.base.cache.d) + part_floats<decltype(ko)>(so, p.base.cache.d) +
-                  2 * row_floats(p.base));
+                  (KS::kCopies + 1) * row_floats(p.base));
     return cudaSuccess;
   });
 }
@@ -260,8 +296,10 @@ cudaError_t launch_attn_decode_shared(const attn_decode_shared_params& p, bool w
     float* rows = o.part_o + part_floats<KO>(so, D);
     s.out = rows;
     s.lse = rows + row_values;
-    o.out = rows + row_floats(q);
-    o.lse = rows + row_floats(q) + row_values;
+    s.copy_floats = (int64_t)row_floats(q);
+    rows += KS::kCopies * row_floats(q);
+    o.out = rows;
+    o.lse = rows + row_values;
     s.out_fp32 = o.out_fp32 = 1;
     cudaError_t e = ks.launch(s, ss, false, st);
     if (e == cudaSuccess) e = ko.launch(o, so, true, st);

@@ -51,7 +51,7 @@ struct TensorWalk {
   // (one thread, after place)
   __device__ __forceinline__ void begin(const DecodeArgs& a, const Placement& pl) {
     const int64_t total = pl.before[kThreads] * a.h_kv;
-    const int64_t run = run_length(a, total);
+    const int64_t run = run_length(a, total, T::kMinRun);
     at = blockIdx.x / a.row_tiles * run;
     end = min(at + run, total);
     if (at >= end) return;
@@ -70,7 +70,8 @@ struct TensorWalk {
       seq_at += c;
     }
   }
-  // The next piece with a block, if there is one (false: the run is done).
+  // The next piece with a block, if there is one (false: the run is done): next for the whole
+  // role, advance for the leader.
   template <typename Sync>
   __device__ __forceinline__ bool next(const DecodeArgs& a, TensorPiece<M>& p, bool leader, Sync&& sync) {
     sync();  // everybody has the last one
@@ -79,8 +80,6 @@ struct TensorWalk {
     p = piece;
     return more;
   }
-
- private:
   __device__ __forceinline__ bool advance(const DecodeArgs& a) {
     while (at < end && seq < a.n) {
       TensorPiece<M> p;
