@@ -17,8 +17,9 @@
 // Warps by role: 0-7 softmax, 8-11 widen V (a thread per key), 12 loads, 13 and 14 issue the
 // products of a group each.
 //
-// Tensor memory holds, per group, S [128][128] (P of 64 keys at a time over the half of S
-// that it came from) and O [128][D].
+// Tensor memory holds, per group, S [128][128] and O [128][D].  A tile goes in halves of 64
+// keys: P of a half lies over its S, and the S of the next tile's half is computed as soon
+// as O has it, while the softmax works on the other half.
 //
 // Every wait ends as in attn_decode_tensor.cuh.
 #pragma once
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
     uint64_t q_full, widened;  // of a piece: q in shared memory; all of V widened
     // of a group
     uint64_t meta_full[2];     // a tile's scales are there
-    uint64_t s_full[2];        // S is
+    uint64_t s_full[2][2];     // half of S is
     uint64_t p_full[2][2];     // half of P is
     uint64_t o_done[2][2];     // O has it
     uint64_t drain[2];
@@ -143,8 +144,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
       mbar_init(&bars.v_full[i], 128);
       mbar_init(&bars.v_used[i], kUsers);
       mbar_init(&bars.meta_full[i], 1);
-      mbar_init(&bars.s_full[i], 1);
       for (int h = 0; h < 2; ++h) {
+        mbar_init(&bars.s_full[i][h], 1);
         mbar_init(&bars.p_full[i][h], 128);
         mbar_init(&bars.o_done[i][h], 1);
       }
@@ -257,61 +258,73 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
     } else if (warp >= 13) {
       // ====================================================== products of a group
       const int g = warp - 13;
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kKeys), idesc_o = idesc_f16_f32(128, D, false, true);
+      constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kKeys / 2), idesc_o = idesc_f16_f32(128, D, false, true);
       const bool mine = kTurns || p.rt * R + g * 128 < p.rows(a);  // the group has rows
       const uint32_t t_s = tmem + g * C::kGroupCols, t_o = t_s + kKeys;
       const uint32_t q_lo = sdesc_lo(smem_u32(smem + (kTurns ? 0 : g) * 128 * D), 16);
       uint32_t c = c0;
+      constexpr int kEvery = kTurns ? 2 : 1;
       if (ok) ok = wait_on(&bars.q_full, n & 1, ctx);
-      for (int t = kTurns ? g : 0; t < tiles; t += kTurns ? 2 : 1) {
+      // S of half h of tile t (the group's c-th), over P of the same half of its tile before
+      auto issue_s = [&](int t, uint32_t c, int h) {
         const uint32_t i = i0 + t;
-        const int slot = i % kStages, buf = i & 1;
-        if (ok) ok = wait_on(&bars.full[slot], (i / kStages) & 1, ctx);
-        if (!mine) {  // (in step: a stage is not filled again before both have passed it)
-          if (ok) ok = wait_on(&bars.v_full[buf], (i >> 1) & 1, ctx);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok && lane == 0) {
-            mbar_arrive(&bars.k_free[slot]);
-            mbar_arrive(&bars.v_used[buf]);
-          }
-          __syncwarp();
-          continue;
-        }
-        // S lies where P of the group's tile before was
-        if (ok && c > 0) ok = wait_on(&bars.o_done[g][1], (c - 1) & 1, ctx);
+        const int slot = i % kStages;
+        if (ok && h == 0) ok = wait_on(&bars.full[slot], (i / kStages) & 1, ctx);
+        if (ok && c > 0) ok = wait_on(&bars.o_done[g][h], (c - 1) & 1, ctx);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && lane == 0) {
           tc_fence_after();
-          mbar_arrive(&bars.meta_full[g]);
-          const uint32_t b = sdesc_lo(smem_u32(smem + C::k_off + slot * 2 * C::kCodes), 16);
+          if (h == 0) mbar_arrive(&bars.meta_full[g]);
+          const uint32_t b = sdesc_lo(smem_u32(smem + C::k_off + slot * 2 * C::kCodes + h * 64 * D), 16);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {  // hi, then lo
             const int part = kk / (D / 32), at = kk % (D / 32) * 32;
-            mma_codes<D>(t_s, q_lo + ((part * C::kQ + at) >> 4), b + (at >> 4), idesc_s, kk > 0 ? 1u : 0u);
+            mma_codes<D>(t_s + h * 64, q_lo + ((part * C::kQ + at) >> 4), b + (at >> 4), idesc_s, kk > 0 ? 1u : 0u);
           }
-          mma_commit(&bars.s_full[g]);
-          mma_commit(&bars.k_free[slot]);
+          mma_commit(&bars.s_full[g][h]);
+          if (h == 1) mma_commit(&bars.k_free[slot]);
         }
         __syncwarp();
-        if (ok) ok = wait_on(&bars.v_full[buf], (i >> 1) & 1, ctx);
-        const uint32_t v = sdesc_lo(smem_u32(smem + C::v_off + buf * C::kV16), C::kBlock64);
-        const bool first = t < (kTurns ? 2 : 1);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (ok) ok = wait_on(&bars.p_full[g][h], c & 1, ctx);
+      };
+      if (!mine) {
+        // (in step: a stage is not filled again before both groups have passed it)
+        for (int t = 0; t < tiles; ++t) {
+          const uint32_t i = i0 + t;
+          if (ok) ok = wait_on(&bars.full[i % kStages], (i / kStages) & 1, ctx);
+          if (ok) ok = wait_on(&bars.v_full[i & 1], (i >> 1) & 1, ctx);
           ok = __all_sync(0xffffffffu, ok);
           if (ok && lane == 0) {
-            tc_fence_after();
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_ts_lo(t_o, t_s + h * 64 + kk * 8, v + (((h * 4 + kk) * 2048) >> 4), idesc_o,
-                        kk > 0 || h > 0 || !first ? 1u : 0u);
-            mma_commit(&bars.o_done[g][h]);
-            if (h == 1) mma_commit(&bars.v_used[buf]);
+            mbar_arrive(&bars.k_free[i % kStages]);
+            mbar_arrive(&bars.v_used[i & 1]);
           }
           __syncwarp();
         }
-        ++c;
+      } else if ((kTurns ? g : 0) < tiles) {
+        const int t0 = kTurns ? g : 0;
+        issue_s(t0, c, 0);
+        issue_s(t0, c, 1);
+        for (int t = t0; t < tiles; t += kEvery, ++c) {
+          const uint32_t i = i0 + t;
+          const int buf = i & 1;
+          if (ok) ok = wait_on(&bars.v_full[buf], (i >> 1) & 1, ctx);
+          const uint32_t v = sdesc_lo(smem_u32(smem + C::v_off + buf * C::kV16), C::kBlock64);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (ok) ok = wait_on(&bars.p_full[g][h], c & 1, ctx);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && lane == 0) {
+              tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_ts_lo(t_o, t_s + h * 64 + kk * 8, v + (((h * 4 + kk) * 2048) >> 4), idesc_o,
+                          kk > 0 || h > 0 || t > t0 ? 1u : 0u);
+              mma_commit(&bars.o_done[g][h]);
+              if (h == 1) mma_commit(&bars.v_used[buf]);
+            }
+            __syncwarp();
+            if (t + kEvery < tiles) issue_s(t + kEvery, c + 1, h);
+          }
+        }
       }
     } else if (warp >= 8) {
       // ====================================================== V to f16
@@ -451,13 +464,14 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         const uint32_t i = i0 + (kTurns ? 2 * t + g : t);
         const int m = i % C::kMeta;
         if (ok) ok = wait_on(&bars.meta_full[g], c & 1, ctx);
-        if (ok) ok = wait_on(&bars.s_full[g], c & 1, ctx);
         __syncwarp();
-        tc_fence_after();
         const bool all_seen = s_tile[m].y;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int col0 = h * 64;
+          if (ok) ok = wait_on(&bars.s_full[g][h], c & 1, ctx);
+          __syncwarp();
+          tc_fence_after();
           if (busy) {
             uint32_t pk[32];
             auto sees = [&](int j) {  // key j of the tile
