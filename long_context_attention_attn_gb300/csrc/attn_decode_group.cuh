@@ -122,9 +122,10 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
   __shared__ Bars bars;
   __shared__ TensorWalk<T, kShared, R> walk;
   __shared__ int64_t before[kThreads + 1];
-  // of a tile's groups of 16 keys: scales and whether they have a page; its first key
+  // of a tile's groups of 16 keys: scales, V's as a logarithm too, and whether they have a
+  // page; its first key
   // and whether every row sees all of it
-  __shared__ float s_ks[C::kMeta][8], s_vs[C::kMeta][8];
+  __shared__ __align__(16) float s_ks[C::kMeta][8], s_vs[C::kMeta][8], s_lv[C::kMeta][8];
   __shared__ uint8_t s_ok[C::kMeta][8];
   __shared__ int2 s_tile[C::kMeta];
   __shared__ float s_fac[R];  // what the scores of q's rows are multiplied by
@@ -138,21 +139,21 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.full[i], 8);
       mbar_init(&bars.k_free[i], kUsers);
-      mbar_init(&bars.v_free[i], 128);
+      mbar_init(&bars.v_free[i], 4);  // (a warp each)
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars.v_full[i], 128);
+      mbar_init(&bars.v_full[i], 4);
       mbar_init(&bars.v_used[i], kUsers);
       mbar_init(&bars.meta_full[i], 1);
       for (int h = 0; h < 2; ++h) {
         mbar_init(&bars.s_full[i][h], 1);
-        mbar_init(&bars.p_full[i][h], 128);
+        mbar_init(&bars.p_full[i][h], 4);
         mbar_init(&bars.o_done[i][h], 1);
       }
       mbar_init(&bars.drain[i], 1);
     }
-    mbar_init(&bars.q_full, R);
-    mbar_init(&bars.widened, 128);
+    mbar_init(&bars.q_full, R / 32);
+    mbar_init(&bars.widened, 4);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
     }
     __syncthreads();
     if (!walk.more) break;
-    const TensorPiece<kShared> p = walk.piece;
+    const TensorPiece<kShared>& p = walk.piece;
     const int tiles = p.t1 - p.t0;
     // the group's tiles of this piece
     auto tiles_of = [&](int g) { return kTurns ? (tiles + 1 - g) / 2 : tiles; };
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
             const int m = i % C::kMeta, g = lane & 7;
             s_ks[m][g] = take ? ks : 0.f;
             s_vs[m][g] = take ? vs : 0.f;
+            s_lv[m][g] = take ? lg2(vs) : 0.f;
             s_ok[m][g] = take;
             if (g == 0) s_tile[m] = make_int2(key0, all);
             if (take) {
@@ -256,63 +258,44 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
       }
       if (i > i0) loaded = i;
     } else if (warp >= 13) {
-      // ====================================================== products of a group
+      // ====================================================== products of a group: one thread
       const int g = warp - 13;
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kKeys / 2), idesc_o = idesc_f16_f32(128, D, false, true);
-      const bool mine = kTurns || p.rt * R + g * 128 < p.rows(a);  // the group has rows
-      const uint32_t t_s = tmem + g * C::kGroupCols, t_o = t_s + kKeys;
-      const uint32_t q_lo = sdesc_lo(smem_u32(smem + (kTurns ? 0 : g) * 128 * D), 16);
-      uint32_t c = c0;
       constexpr int kEvery = kTurns ? 2 : 1;
-      if (ok) ok = wait_on(&bars.q_full, n & 1, ctx);
-      // S of half h of tile t (the group's c-th), over P of the same half of its tile before
-      auto issue_s = [&](int t, uint32_t c, int h) {
-        const uint32_t i = i0 + t;
-        const int slot = i % kStages;
-        if (ok && h == 0) ok = wait_on(&bars.full[slot], (i / kStages) & 1, ctx);
-        if (ok && c > 0) ok = wait_on(&bars.o_done[g][h], (c - 1) & 1, ctx);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok && lane == 0) {
-          tc_fence_after();
-          if (h == 0) mbar_arrive(&bars.meta_full[g]);
-          const uint32_t b = sdesc_lo(smem_u32(smem + C::k_off + slot * 2 * C::kCodes + h * 64 * D), 16);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {  // hi, then lo
-            const int part = kk / (D / 32), at = kk % (D / 32) * 32;
-            mma_codes<D>(t_s + h * 64, q_lo + ((part * C::kQ + at) >> 4), b + (at >> 4), idesc_s, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(&bars.s_full[g][h]);
-          if (h == 1) mma_commit(&bars.k_free[slot]);
-        }
-        __syncwarp();
-      };
-      if (!mine) {
-        // (in step: a stage is not filled again before both groups have passed it)
-        for (int t = 0; t < tiles; ++t) {
+      constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kKeys / 2), idesc_o = idesc_f16_f32(128, D, false, true);
+      const int t0 = kTurns ? g : 0;
+      if (lane > 0) {
+        // (nothing to do)
+      } else if (!kTurns && p.rt * R + g * 128 >= p.rows(a)) {
+        // a group without rows: in step, since a stage is not filled again before both groups
+        // have passed it
+        for (int t = 0; t < tiles && ok; ++t) {
           const uint32_t i = i0 + t;
-          if (ok) ok = wait_on(&bars.full[i % kStages], (i / kStages) & 1, ctx);
-          if (ok) ok = wait_on(&bars.v_full[i & 1], (i >> 1) & 1, ctx);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok && lane == 0) {
-            mbar_arrive(&bars.k_free[i % kStages]);
-            mbar_arrive(&bars.v_used[i & 1]);
-          }
-          __syncwarp();
+          ok = mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, ctx);
+          if (ok) ok = mbar_wait(&bars.v_full[i & 1], (i >> 1) & 1, ctx);
+          if (!ok) break;
+          mbar_arrive(&bars.k_free[i % kStages]);
+          mbar_arrive(&bars.v_used[i & 1]);
         }
-      } else if ((kTurns ? g : 0) < tiles) {
-        const int t0 = kTurns ? g : 0;
-        issue_s(t0, c, 0);
-        issue_s(t0, c, 1);
-        for (int t = t0; t < tiles; t += kEvery, ++c) {
-          const uint32_t i = i0 + t;
-          const int buf = i & 1;
-          if (ok) ok = wait_on(&bars.v_full[buf], (i >> 1) & 1, ctx);
-          const uint32_t v = sdesc_lo(smem_u32(smem + C::v_off + buf * C::kV16), C::kBlock64);
+      } else if (ok && t0 < tiles) {
+        const uint32_t t_s = tmem + g * C::kGroupCols, t_o = t_s + kKeys;
+        const uint32_t q_lo = sdesc_lo(smem_u32(smem + (kTurns ? 0 : g) * 128 * D), 16);
+        const uint32_t k_lo = sdesc_lo(smem_u32(smem + C::k_off), 16);
+        const uint32_t v_lo = sdesc_lo(smem_u32(smem + C::v_off), C::kBlock64);
+        ok = mbar_wait(&bars.q_full, n & 1, ctx);
+        uint32_t c = c0;
+        // t = t0 - kEvery: both halves of S of the first tile; then, half by half, O of tile t
+        // and S of the tile after it, over P that O has just taken
+        for (int t = t0 - kEvery; t < tiles && ok; t += kEvery) {
+          const uint32_t i = i0 + t, i1 = i + kEvery;
+          const int buf = i & 1, slot = i1 % kStages;
+          const bool begun = t >= t0, more = t + kEvery < tiles;
+          if (begun) ok = mbar_wait(&bars.v_full[buf], (i >> 1) & 1, ctx);
+          const uint32_t v = v_lo + ((buf * C::kV16) >> 4), k = k_lo + ((slot * 2 * C::kCodes) >> 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            if (ok) ok = wait_on(&bars.p_full[g][h], c & 1, ctx);
-            ok = __all_sync(0xffffffffu, ok);
-            if (ok && lane == 0) {
+            if (begun) {
+              if (ok) ok = mbar_wait(&bars.p_full[g][h], (c - 1) & 1, ctx);
+              if (!ok) break;
               tc_fence_after();
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
@@ -321,11 +304,26 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
               mma_commit(&bars.o_done[g][h]);
               if (h == 1) mma_commit(&bars.v_used[buf]);
             }
-            __syncwarp();
-            if (t + kEvery < tiles) issue_s(t + kEvery, c + 1, h);
+            if (more) {
+              if (h == 0) ok = mbar_wait(&bars.full[slot], (i1 / kStages) & 1, ctx);
+              if (ok && c > 0) ok = mbar_wait(&bars.o_done[g][h], (c - 1) & 1, ctx);
+              if (!ok) break;
+              tc_fence_after();
+              if (h == 0) mbar_arrive(&bars.meta_full[g]);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {  // hi, then lo
+                const int part = kk / (D / 32), at = kk % (D / 32) * 32;
+                mma_codes<D>(t_s + h * 64, q_lo + ((part * C::kQ + at) >> 4), k + ((h * 64 * D + at) >> 4), idesc_s,
+                             kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&bars.s_full[g][h]);
+              if (h == 1) mma_commit(&bars.k_free[slot]);
+            }
           }
+          ++c;
         }
       }
+      __syncwarp();
     } else if (warp >= 8) {
       // ====================================================== V to f16
       const int k = threadIdx.x & 127;  // this thread's key of a tile
@@ -381,10 +379,12 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
             for (int j = 0; j < D / 4; ++j) w[j] = 0u;
           }
         }
-        mbar_arrive(&bars.v_free[slot]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_free[slot]);
         // the f16 tile that was there has been multiplied
         if (i >= 2) ok = wait_on(&bars.v_used[buf], ((i >> 1) - 1) & 1, ctx);
-        if (!ok) continue;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         uint8_t* dst = smem + C::v_off + buf * C::kV16;
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) {  // 8 d's
@@ -396,9 +396,11 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
           *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kBlock64 + k * 128 + (((c ^ k) & 7) << 4)) = f;
         }
         fence_proxy_async_smem();
-        mbar_arrive(&bars.v_full[buf]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.v_full[buf]);
       }
-      if (ok) mbar_arrive(&bars.widened);
+      __syncwarp();
+      if (ok && lane == 0) mbar_arrive(&bars.widened);
     } else {
       // ====================================================== softmax
       const int g = warp >> 2, wq = warp & 3, th = threadIdx.x & 127;
@@ -449,7 +451,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                                                                    lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
         }
         fence_proxy_async_smem();
-        if (ok) mbar_arrive(&bars.q_full);
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(&bars.q_full);
       }
       if (ok) ok = wait_on(&bars.q_full, n & 1, ctx);
       const float fac = s_fac[r];
@@ -473,62 +476,62 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
           __syncwarp();
           tc_fence_after();
           if (busy) {
-            uint32_t pk[32];
-            auto sees = [&](int j) {  // key j of the tile
-              const int key = s_tile[m].x + j;
-              return s_ok[m][j >> 4] && key < p.span.hi && key <= pos &&
-                     (a.window < 0 || pos - key <= a.window || key < a.sink);
-            };
-            float sum;
-#pragma unroll 1
-            for (bool again = false;; again = true) {
-              float top = 0.f, top_o = 0.f, part[8] = {};
+            const float4 ks4 = *reinterpret_cast<const float4*>(&s_ks[m][4 * h]);
+            const float4 vs4 = *reinterpret_cast<const float4*>(&s_vs[m][4 * h]);
+            // Where every row sees all keys and b * v_scale is far from fp32's ends (it is but for pages
+            // of zeros and the like), P * v_scale comes straight from the exponential, and the sum of
+            // P from the sums over 16 keys, which tell of values past f16's range too.
+            const float v_most = b * fmaxf(fmaxf(vs4.x, vs4.y), fmaxf(vs4.z, vs4.w)),
+                        v_least = b * fminf(fminf(vs4.x, vs4.y), fminf(vs4.z, vs4.w));
+            bool done = __all_sync(0xffffffffu, all_seen && v_most < 0x1p60f && v_least > 0x1p-60f);
+            if (done) {
+              const float4 lv4 = *reinterpret_cast<const float4*>(&s_lv[m][4 * h]);
+              const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w},
+                          lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
+              const float shift = nmo + kShift;
+              uint32_t pk[32];
+              float sum = 0.f, most = 0.f;
 #pragma unroll
               for (int cc = 0; cc < 64; cc += 32) {
-                float e[32];
+                float2 e[16];
                 tmem_ld32(t_s + col0 + cc, reinterpret_cast<uint32_t*>(e));
-                // (b * v_scale may pass fp32's range: attn_decode_tensor.cuh)
-                float f[2], v[2], v_all[2];
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  f[x] = fac * s_ks[m][(col0 + cc) / 16 + x];
-                  v_all[x] = b * s_vs[m][(col0 + cc) / 16 + x];
-                  v[x] = fminf(v_all[x], FLT_MAX);
-                }
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; j += 2)
-                  fma_f32x2(e[j], e[j + 1], e[j], e[j + 1], f[j >> 4], f[j >> 4], nm, nm);
-                if (!all_seen) {
+                for (int x = 0; x < 2; ++x) {  // 16 keys
+                  const int u = cc / 16 + x;
+                  const float f = fac * ks[u], o = lv[u] + shift;
 #pragma unroll
-                  for (int j = 0; j < 32; ++j)
-                    if (!sees(col0 + cc + j)) e[j] = -INFINITY;
+                  for (int j = 8 * x; j < 8 * x + 8; ++j) e[j] = __ffma2_rn(e[j], make_float2(f, f), make_float2(o, o));
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) e[j] = ex2(e[j]);
+                for (int j = 0; j < 16; ++j) e[j] = make_float2(ex2(e[j].x), ex2(e[j].y));
+#pragma unroll
+                for (int j = 0; j < 16; ++j) pk[cc / 2 + j] = pack_f16(e[j].x, e[j].y);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) e[j] = __fadd2_rn(e[j], e[j + 1]);
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) e[j] = __fadd2_rn(e[j], e[j + 2]);
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                  float y[4];
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    const float* z = e + 16 * x + 4 * j;
-                    y[j] = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-                  }
-                  const float most = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
-                  top = fmaxf(top, most);
-                  top_o = fmaxf(top_o, most * v_all[x]);  // (0 * infinity counts as nothing)
-                }
-#pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                  add_f32x2(part[j & 6], part[(j & 6) + 1], part[j & 6], part[(j & 6) + 1], e[j], e[j + 1]);
-                  mul_f32x2(e[j], e[j + 1], e[j], e[j + 1], v[j >> 4], v[j >> 4]);
-                  pk[(cc + j) / 2] = pack_f16(e[j], e[j + 1]);
+                  const float2 y = __fadd2_rn(e[8 * x], e[8 * x + 4]);
+                  most = fmaxf(most, y.x + y.y);
+                  sum += (y.x + y.y) * __fdividef(1.f, b * vs[cc / 16 + x]);
                 }
               }
-              sum = ((part[0] + part[1]) + (part[2] + part[3])) + ((part[4] + part[5]) + (part[6] + part[7]));
-              if (again || !__any_sync(0xffffffffu, top > 256.f || top_o > 32768.f)) break;
-
-              // raise the references where a score passed them, to the largest of these keys
+              done = !__any_sync(0xffffffffu, most > 32768.f || sum > 16384.f);
+              if (done) {
+                l += sum;
+                tmem_st32(t_s + col0, pk);
+              }
+            }
+            if (!done) {
+              auto sees = [&](int j) {  // key j of the tile
+                const int key = s_tile[m].x + j;
+                return s_ok[m][j >> 4] && key < p.span.hi && key <= pos &&
+                       (a.window < 0 || pos - key <= a.window || key < a.sink);
+              };
+              // raise the references where a score passes them by more than kRescale, to the largest of
+              // these keys
               float x = -INFINITY, xo = -INFINITY;
 #pragma unroll 1
               for (int j0 = col0; j0 < col0 + 64; j0 += 16) {
@@ -542,36 +545,62 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                 x = fmaxf(x, y);
                 xo = fmaxf(xo, y + lv);
               }
-              const float nm1 = x + nm > 0.f ? -x : nm;
-              // (b stays a normal number: attn_decode_tensor.cuh)
-              const float nmo1 = fminf(fmaxf(xo + nmo > 0.f ? -xo : nmo, nm1 - 130.f), nm1 + 119.f);
-              const float fo = ex2(nmo1 - nmo);
-              l *= ex2(nm1 - nm);
-              nm = nm1;
-              nmo = nmo1;
-              b = ex2(nmo1 - nm1 + kShift);
-              if (t > 0 || h > 0) {
-                if (ok)
-                  ok = h ? wait_on(&bars.o_done[g][0], c & 1, ctx) : wait_on(&bars.o_done[g][1], (c - 1) & 1, ctx);
-                __syncwarp();
-                tc_fence_after();
+              if (__any_sync(0xffffffffu, x + nm > kRescale || xo + nmo > (v_most > FLT_MAX ? 0.f : kRescale))) {
+                const float nm1 = x + nm > 0.f ? -x : nm;
+                // (b stays a normal number: attn_decode_tensor.cuh)
+                const float nmo1 = fminf(fmaxf(xo + nmo > 0.f ? -xo : nmo, nm1 - 130.f), nm1 + 119.f);
+                const float fo = ex2(nmo1 - nmo);
+                l *= ex2(nm1 - nm);
+                nm = nm1;
+                nmo = nmo1;
+                b = ex2(nmo1 - nm1 + kShift);
+                if (t > 0 || h > 0) {
+                  if (ok)
+                    ok = h ? wait_on(&bars.o_done[g][0], c & 1, ctx) : wait_on(&bars.o_done[g][1], (c - 1) & 1, ctx);
+                  __syncwarp();
+                  tc_fence_after();
 #pragma unroll 1
-                for (int cc = 0; cc < D; cc += 32) {
-                  float o[32];
-                  tmem_ld32(t_o + cc, reinterpret_cast<uint32_t*>(o));
-                  tmem_wait_ld();
+                  for (int cc = 0; cc < D; cc += 32) {
+                    float o[32];
+                    tmem_ld32(t_o + cc, reinterpret_cast<uint32_t*>(o));
+                    tmem_wait_ld();
 #pragma unroll
-                  for (int j = 0; j < 32; ++j) o[j] *= fo;
-                  tmem_st32(t_o + cc, reinterpret_cast<const uint32_t*>(o));
+                    for (int j = 0; j < 32; ++j) o[j] *= fo;
+                    tmem_st32(t_o + cc, reinterpret_cast<const uint32_t*>(o));
+                  }
                 }
               }
+              // P 16 keys at a time, over scores that have been read
+#pragma unroll 1
+              for (int cc = 0; cc < 64; cc += 16) {
+                float2 e[8];
+                uint32_t pk[8];
+                tmem_ld16(t_s + col0 + cc, reinterpret_cast<uint32_t*>(e));
+                // (b * v_scale may pass fp32's range where keys are out of sight or of next to no weight: 0
+                // * infinity is NaN, so P takes the largest finite value)
+                const float f = fac * s_ks[m][(col0 + cc) / 16], v = fminf(b * s_vs[m][(col0 + cc) / 16], FLT_MAX);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  e[j] = __ffma2_rn(e[j], make_float2(f, f), make_float2(nm, nm));
+                  if (!all_seen) {
+                    if (!sees(col0 + cc + 2 * j)) e[j].x = -INFINITY;
+                    if (!sees(col0 + cc + 2 * j + 1)) e[j].y = -INFINITY;
+                  }
+                  e[j] = make_float2(ex2(e[j].x), ex2(e[j].y));
+                  l += e[j].x + e[j].y;
+                  e[j] = __fmul2_rn(e[j], make_float2(v, v));
+                  pk[j] = pack_f16(e[j].x, e[j].y);
+                }
+                tmem_st8(t_s + col0 + cc / 2, pk);
+              }
             }
-            l += sum;
-            tmem_st32(t_s + col0, pk);
             tmem_wait_st();
           }
           tc_fence_before();
-          if (ok) mbar_arrive(&bars.p_full[g][h]);
+          // (a warp arrives with all of its lanes' results or not at all)
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok && lane == 0) mbar_arrive(&bars.p_full[g][h]);
         }
       }
       if (count > 0) {
