@@ -122,11 +122,12 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
   __shared__ Bars bars;
   __shared__ TensorWalk<T, kShared, R> walk;
   __shared__ int64_t before[kThreads + 1];
-  // of a tile's groups of 16 keys: scales, V's as a logarithm too, and whether they have a
-  // page; its first key
+  // of a tile's groups of 16 keys: scales, V's logarithms and inverses, and whether they
+  // have a page; the least and the largest scale of V, its first key
   // and whether every row sees all of it
-  __shared__ __align__(16) float s_ks[C::kMeta][8], s_vs[C::kMeta][8], s_lv[C::kMeta][8];
+  __shared__ __align__(16) float s_ks[C::kMeta][8], s_vs[C::kMeta][8], s_lv[C::kMeta][8], s_iv[C::kMeta][8];
   __shared__ uint8_t s_ok[C::kMeta][8];
+  __shared__ float2 s_range[C::kMeta];
   __shared__ int2 s_tile[C::kMeta];
   __shared__ float s_fac[R];  // what the scores of q's rows are multiplied by
   __shared__ int s_any_nan;
@@ -225,6 +226,12 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         const bool all = whole && key0 + kKeys <= p.span.hi && (key0 >= p.span.lo || key0 + kKeys <= p.span.sink_hi) &&
                          key0 + kKeys - 1 <= p_first &&
                          (a.window < 0 || p_last - key0 <= a.window || key0 + kKeys - 1 < a.sink);
+        float2 range = make_float2(vs, vs);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+          range.x = fminf(range.x, __shfl_xor_sync(0xffffffffu, range.x, o));
+          range.y = fmaxf(range.y, __shfl_xor_sync(0xffffffffu, range.y, o));
+        }
         for (int u = 0; u < kTurn && t + u < p.t1; ++u, ++i) {
           const int slot = i % kStages;
           if (i >= kStages) {
@@ -238,8 +245,12 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
             s_ks[m][g] = take ? ks : 0.f;
             s_vs[m][g] = take ? vs : 0.f;
             s_lv[m][g] = take ? lg2(vs) : 0.f;
+            s_iv[m][g] = take ? 1.f / vs : 0.f;
             s_ok[m][g] = take;
-            if (g == 0) s_tile[m] = make_int2(key0, all);
+            if (g == 0) {
+              s_tile[m] = make_int2(key0, all);
+              s_range[m] = range;
+            }
             if (take) {
               mbar_arrive_expect_tx(&bars.full[slot], 2 * 16 * D);
               const int y = key & page_mask;
@@ -410,35 +421,35 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
       const RowPlace<kShared> to(a, p, mine ? row : 0);
       const int pos = mine ? to.pos : -1;
       if (!kTurns || g == 0) {
-        // ---- q's row as two e4m3 values each, the largest value in (224, 448]
+        // ---- q's row (all of its loads at once) as two e4m3 values each, the largest value in
+        // (224, 448]
         const uint4* src = reinterpret_cast<const uint4*>(a.q + to.orow * D);
-        float amax = 0.f;
-        bool finite = true;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = mine ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint4 x[D / 8];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x0 = fabsf(__uint_as_float(w[j] << 16)), x1 = fabsf(__uint_as_float(w[j] & 0xffff0000u));
-            finite = finite && x0 < INFINITY && x1 < INFINITY;
-            amax = fmaxf(amax, fmaxf(x0, x1));
-          }
+        for (int c = 0; c < D / 8; ++c) x[c] = mine ? src[c] : make_uint4(0u, 0u, 0u, 0u);
+        // (magnitudes of bf16 order like their bits, two in a word)
+        uint32_t top = 0u;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          top = __vmaxu2(top, x[c].x & 0x7fff7fffu);
+          top = __vmaxu2(top, x[c].y & 0x7fff7fffu);
+          top = __vmaxu2(top, x[c].z & 0x7fff7fffu);
+          top = __vmaxu2(top, x[c].w & 0x7fff7fffu);
         }
-        const uint32_t bits = __float_as_uint(finite ? amax : 0.f);
-        const int ex = bits ? max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100) : 0;
+        const uint32_t bits = max(top << 16, top & 0xffff0000u);
+        const bool finite = bits < 0x7f800000u;
+        const int ex = finite && bits ? max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100) : 0;
         const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
         // (a row with an infinity or NaN has no softmax: all of it is NaN)
         const float more = finite ? 0.f : bad;
         s_fac[r] = mine ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) + more : 0.f;
         uint8_t* dst = smem + (kTurns ? 0 : g) * 128 * D;
-#pragma unroll 2
+#pragma unroll
         for (int c = 0; c < D / 16; ++c) {  // 16 values
           uint32_t hi[8], lo[8];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint4 x = mine ? src[2 * c + u] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            const uint32_t w[4] = {x[2 * c + u].x, x[2 * c + u].y, x[2 * c + u].z, x[2 * c + u].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               split_codes(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv, hi[4 * u + j],
@@ -460,65 +471,57 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
       // the references of P and of P * v_scale (negated; at first below every score),
       // 2^(m - mo + kShift), the sum of P
       float nm = FLT_MAX, nmo = FLT_MAX, b = 1.f, l = 0.f;
+      float shift = FLT_MAX, b_inv = 1.f;  // nmo + kShift, 1 / b
       const int count = busy || kTurns || p.rt * R + g * 128 < p.rows(a) ? tiles_of(g) : 0;
       uint32_t c = c0;
 #pragma unroll 1
       for (int t = 0; t < count; ++t, ++c) {
         const uint32_t i = i0 + (kTurns ? 2 * t + g : t);
         const int m = i % C::kMeta;
-        if (ok) ok = wait_on(&bars.meta_full[g], c & 1, ctx);
+        if (ok) ok = mbar_wait(&bars.meta_full[g], c & 1, ctx);
         __syncwarp();
         const bool all_seen = s_tile[m].y;
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int col0 = h * 64;
-          if (ok) ok = wait_on(&bars.s_full[g][h], c & 1, ctx);
+          if (ok) ok = mbar_wait(&bars.s_full[g][h], c & 1, ctx);
           __syncwarp();
           tc_fence_after();
           if (busy) {
-            const float4 ks4 = *reinterpret_cast<const float4*>(&s_ks[m][4 * h]);
-            const float4 vs4 = *reinterpret_cast<const float4*>(&s_vs[m][4 * h]);
             // Where every row sees all keys and b * v_scale is far from fp32's ends (it is but for pages
             // of zeros and the like), P * v_scale comes straight from the exponential, and the sum of
             // P from the sums over 16 keys, which tell of values past f16's range too.
-            const float v_most = b * fmaxf(fmaxf(vs4.x, vs4.y), fmaxf(vs4.z, vs4.w)),
-                        v_least = b * fminf(fminf(vs4.x, vs4.y), fminf(vs4.z, vs4.w));
-            bool done = __all_sync(0xffffffffu, all_seen && v_most < 0x1p60f && v_least > 0x1p-60f);
+            bool done = all_seen;
             if (done) {
-              const float4 lv4 = *reinterpret_cast<const float4*>(&s_lv[m][4 * h]);
-              const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w},
-                          lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
-              const float shift = nmo + kShift;
               uint32_t pk[32];
               float sum = 0.f, most = 0.f;
+              float2 e[32];
+              tmem_ld32(t_s + col0, reinterpret_cast<uint32_t*>(e));
+              tmem_ld32(t_s + col0 + 32, reinterpret_cast<uint32_t*>(e) + 32);
+              tmem_wait_ld();
 #pragma unroll
-              for (int cc = 0; cc < 64; cc += 32) {
-                float2 e[16];
-                tmem_ld32(t_s + col0 + cc, reinterpret_cast<uint32_t*>(e));
-                tmem_wait_ld();
+              for (int x = 0; x < 4; ++x) {  // 16 keys
+                const float f = fac * s_ks[m][4 * h + x], o = s_lv[m][4 * h + x] + shift;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {  // 16 keys
-                  const int u = cc / 16 + x;
-                  const float f = fac * ks[u], o = lv[u] + shift;
-#pragma unroll
-                  for (int j = 8 * x; j < 8 * x + 8; ++j) e[j] = __ffma2_rn(e[j], make_float2(f, f), make_float2(o, o));
-                }
-#pragma unroll
-                for (int j = 0; j < 16; ++j) e[j] = make_float2(ex2(e[j].x), ex2(e[j].y));
-#pragma unroll
-                for (int j = 0; j < 16; ++j) pk[cc / 2 + j] = pack_f16(e[j].x, e[j].y);
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) e[j] = __fadd2_rn(e[j], e[j + 1]);
-#pragma unroll
-                for (int j = 0; j < 16; j += 4) e[j] = __fadd2_rn(e[j], e[j + 2]);
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                  const float2 y = __fadd2_rn(e[8 * x], e[8 * x + 4]);
-                  most = fmaxf(most, y.x + y.y);
-                  sum += (y.x + y.y) * __fdividef(1.f, b * vs[cc / 16 + x]);
-                }
+                for (int j = 8 * x; j < 8 * x + 8; ++j) e[j] = __ffma2_rn(e[j], make_float2(f, f), make_float2(o, o));
               }
-              done = !__any_sync(0xffffffffu, most > 32768.f || sum > 16384.f);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) e[j] = make_float2(ex2(e[j].x), ex2(e[j].y));
+#pragma unroll
+              for (int j = 0; j < 32; ++j) pk[j] = pack_f16(e[j].x, e[j].y);
+#pragma unroll
+              for (int w = 1; w < 8; w *= 2)
+#pragma unroll
+                for (int j = 0; j < 32; j += 2 * w) e[j] = __fadd2_rn(e[j], e[j + w]);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                const float y = e[8 * x].x + e[8 * x].y;
+                most = fmaxf(most, y);
+                sum += y * (s_iv[m][4 * h + x] * b_inv);
+              }
+              const float2 range = s_range[m];
+              done = __all_sync(0xffffffffu, !(most > 32768.f) && !(sum > 16384.f) && b * range.y < 0x1p60f &&
+                                                 b * range.x > 0x1p-60f);
               if (done) {
                 l += sum;
                 tmem_st32(t_s + col0, pk);
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                 x = fmaxf(x, y);
                 xo = fmaxf(xo, y + lv);
               }
-              if (__any_sync(0xffffffffu, x + nm > kRescale || xo + nmo > (v_most > FLT_MAX ? 0.f : kRescale))) {
+              if (__any_sync(0xffffffffu, x + nm > kRescale || xo + nmo > (b * s_range[m].y > FLT_MAX ? 0.f : kRescale))) {
                 const float nm1 = x + nm > 0.f ? -x : nm;
                 // (b stays a normal number: attn_decode_tensor.cuh)
                 const float nmo1 = fminf(fmaxf(xo + nmo > 0.f ? -xo : nmo, nm1 - 130.f), nm1 + 119.f);
@@ -554,6 +557,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                 nm = nm1;
                 nmo = nmo1;
                 b = ex2(nmo1 - nm1 + kShift);
+                b_inv = ex2(nm1 - nmo1 - kShift);
+                shift = nmo1 + kShift;
                 if (t > 0 || h > 0) {
                   if (ok)
                     ok = h ? wait_on(&bars.o_done[g][0], c & 1, ctx) : wait_on(&bars.o_done[g][1], (c - 1) & 1, ctx);
@@ -598,8 +603,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
             tmem_wait_st();
           }
           tc_fence_before();
-          // (a warp arrives with all of its lanes' results or not at all)
-          ok = __all_sync(0xffffffffu, ok);
+          // (a lane that gave up has only its own row to spoil, and that one ends as NaN)
+          __syncwarp();
           if (ok && lane == 0) mbar_arrive(&bars.p_full[g][h]);
         }
       }

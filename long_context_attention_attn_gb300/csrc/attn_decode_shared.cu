@@ -58,7 +58,7 @@ constexpr int kFoldMost = 64;  // partials at a time
 // has fewer rows than its threads hold, several threads share a row's partials.
 template <int D>
 __global__ void __launch_bounds__(kFoldThreads)
-    decode_shared_fold_kernel(const DecodeArgs a, const Part shared, const Part own, int n_groups) {
+    decode_shared_fold_kernel(const DecodeArgs a, const Part shared, const Part own, int n_groups, int heads) {
   constexpr int kVec = D / 4, RP = kFoldThreads / kVec;
   __shared__ int64_t before_s[kThreads + 1], before_o[kThreads + 1];
   __shared__ RowPieces rows_s[RP], rows_o[RP];
@@ -74,12 +74,14 @@ __global__ void __launch_bounds__(kFoldThreads)
   ao.runs = own.runs;
   const Placement ps = place<kShared>(as, before_s, shared.block, shared.item_cost, shared.tile);
   const Placement po = place<kOwn>(ao, before_o, own.block, own.item_cost, own.tile);
-  const int kvh = blockIdx.x % a.h_kv, seq = blockIdx.x / a.h_kv, r0 = blockIdx.y * RP;
+  const int parts = (a.h_kv + heads - 1) / heads;
+  const int seq = blockIdx.x / parts, r0 = blockIdx.y * RP;
+  const int kvh0 = blockIdx.x % parts * heads, kvh1 = min(kvh0 + heads, a.h_kv);
   const int rows = min(RP, a.rows - r0);
-  if (threadIdx.x == 0) s_most = 0;
-  __syncthreads();
-  if (threadIdx.x < rows) {
-    // the sequence's group: the last one that starts at or before it
+  // the sequence's group (the last one that starts at or before it), and where the lists have them
+  __shared__ Entry s_eg, s_eo;
+  __shared__ int64_t s_at[2];
+  if (threadIdx.x == 0) {
     int g = 0, end = n_groups;
     while (end - g > 1) {
       const int mid = (g + end) / 2;
@@ -88,132 +90,143 @@ __global__ void __launch_bounds__(kFoldThreads)
       else
         end = mid;
     }
-    const int row = r0 + threadIdx.x;
-    RowPieces s, o;
-    s.n = 0;
-    const Entry eg = entry_of<kShared>(as, g, shared.block, shared.item_cost, shared.tile);
-    const int in_group = seq - eg.first;
-    if (in_group >= 0 && (in_group + 1) * a.rows <= eg.rows && a.lens[seq] - a.s_q + row / a.g >= 0) {
-      const int t = g / ps.per;
-      int64_t at = before_s[t];
-      for (int i = t * ps.per; i < g; ++i) {
-        const Entry e = entry_of<kShared>(as, i, shared.block, shared.item_cost, shared.tile);
-        at += (int64_t)e.span.weight * e.tiles;
-      }
-      s = pieces_of<kShared>(shared, run_length(as, before_s[kThreads] * a.h_kv, shared.shortest), eg, at * a.h_kv, kvh,
-                             in_group * a.rows + row);
+    int64_t at = before_s[g / ps.per];
+    for (int i = g / ps.per * ps.per; i < g; ++i) {
+      const Entry e = entry_of<kShared>(as, i, shared.block, shared.item_cost, shared.tile);
+      at += (int64_t)e.span.weight * e.tiles;
     }
-    const int t = seq / po.per;
-    int64_t at = before_o[t];
-    for (int i = t * po.per; i < seq; ++i)
-      at += entry_of<kOwn>(ao, i, own.block, own.item_cost, own.tile).span.weight;
-    o = pieces_of<kOwn>(own, run_length(ao, before_o[kThreads] * a.h_kv, own.shortest),
-                        entry_of<kOwn>(ao, seq, own.block, own.item_cost, own.tile), at * a.h_kv, kvh, row);
-    rows_s[threadIdx.x] = s;
-    rows_o[threadIdx.x] = o;
-    atomicMax(&s_most, s.n + o.n);
-    s_ref[threadIdx.x] = -INFINITY;
+    s_at[0] = at * a.h_kv;
+    s_eg = entry_of<kShared>(as, g, shared.block, shared.item_cost, shared.tile);
   }
-  __syncthreads();
-  const int most = s_most;
-  // everything the two grids before this one wrote
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-
-  // Partial i of the CTA's row r: its values; its lse.
-  auto source = [&](int r, int i, const float*& lse) -> const float* {
-    const bool sh = i < rows_s[r].n;
-    const RowPieces& p = sh ? rows_s[r] : rows_o[r];
-    const Part& l = sh ? shared : own;
-    const int j = sh ? i : i - rows_s[r].n;
-    const int piece = j / l.copies, copy = j - piece * l.copies;
-    if (p.n == l.copies) {
-      const int row = r0 + r, tok = row / a.g, head = kvh * a.g + row % a.g;
-      lse = l.whole_lse + copy * l.copy_floats + ((int64_t)seq * a.h_q + head) * a.s_q + tok;
-      return l.whole_o + copy * l.copy_floats + (((int64_t)seq * a.s_q + tok) * a.h_q + head) * D;
-    }
-    // a piece that starts inside its item is the first of its CTA, one that ends inside it the last
-    const int64_t slot = 2 * ((p.c0 + piece) * l.row_tiles + p.rt) + ((p.c0 + piece) * p.run <= p.s0 ? 1 : 0);
-    const int64_t at = slot * l.part_rows + copy * l.tile + p.in_tile;
-    lse = l.part_lse + at;
-    return l.part_o + at * D;
-  };
-  const int q = threadIdx.x / kVec, d4 = threadIdx.x % kVec;
-  int held = 1;  // rows, as a power of two
-  while (held < rows) held *= 2;
-  const int ways = RP / held, r = q & (held - 1), way = q / held;
-  const bool mine = r < rows;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float z = 0.f;
-  for (int b0 = 0; b0 < most; b0 += kFoldMost) {
-    const int np = min(kFoldMost, most - b0);
-    for (int u = threadIdx.x; u < np * held; u += kFoldThreads) {
-      const int i = u / held, row = u & (held - 1);
-      float w = -INFINITY;
-      const float* src = nullptr;
-      if (row < rows && b0 + i < rows_s[row].n + rows_o[row].n) {
-        const float* lse;
-        src = source(row, b0 + i, lse);
-        w = *lse;
-      }
-      s_w[i][row] = w;
-      s_src[i][row] = src;
-    }
+  if (threadIdx.x == 32) {
+    int64_t at = before_o[seq / po.per];
+    for (int i = seq / po.per * po.per; i < seq; ++i)
+      at += entry_of<kOwn>(ao, i, own.block, own.item_cost, own.tile).span.weight;
+    s_at[1] = at * a.h_kv;
+    s_eo = entry_of<kOwn>(ao, seq, own.block, own.item_cost, own.tile);
+  }
+  const int64_t run_s = run_length(as, before_s[kThreads] * a.h_kv, shared.shortest);
+  const int64_t run_o = run_length(ao, before_o[kThreads] * a.h_kv, own.shortest);
+  const int len = a.lens[seq];
+  bool waited = false;
+  for (int kvh = kvh0; kvh < kvh1; ++kvh) {
+    __syncthreads();  // (the last head's partials have been read)
+    if (threadIdx.x == 0) s_most = 0;
     __syncthreads();
     if (threadIdx.x < rows) {
-      float top = s_ref[threadIdx.x];
-      for (int i = 0; i < np; ++i) top = fmaxf(top, s_w[i][threadIdx.x]);
-      s_old[threadIdx.x] = top == -INFINITY ? 0.f : ex2(s_ref[threadIdx.x] - top);
-      s_ref[threadIdx.x] = top;
+      const int row = r0 + threadIdx.x, in_group = seq - s_eg.first;
+      RowPieces s;
+      s.n = 0;
+      if (in_group >= 0 && (in_group + 1) * a.rows <= s_eg.rows && len - a.s_q + row / a.g >= 0)
+        s = pieces_of<kShared>(shared, run_s, s_eg, s_at[0], kvh, in_group * a.rows + row);
+      const RowPieces o = pieces_of<kOwn>(own, run_o, s_eo, s_at[1], kvh, row);
+      rows_s[threadIdx.x] = s;
+      rows_o[threadIdx.x] = o;
+      atomicMax(&s_most, s.n + o.n);
+      s_ref[threadIdx.x] = -INFINITY;
     }
     __syncthreads();
-    if (mine) {
-      const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
-      z *= old;
-      acc.x *= old;
-      acc.y *= old;
-      acc.z *= old;
-      acc.w *= old;
-      const int here = min(np, rows_s[r].n + rows_o[r].n - b0);
+    const int most = s_most;
+    // everything the two grids before this one wrote
+    if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+    waited = true;
+
+    // Partial i of the CTA's row r: its values; its lse.
+    auto source = [&](int r, int i, const float*& lse) -> const float* {
+      const bool sh = i < rows_s[r].n;
+      const RowPieces& p = sh ? rows_s[r] : rows_o[r];
+      const Part& l = sh ? shared : own;
+      const int j = sh ? i : i - rows_s[r].n;
+      const int piece = j / l.copies, copy = j - piece * l.copies;
+      if (p.n == l.copies) {
+        const int row = r0 + r, tok = row / a.g, head = kvh * a.g + row % a.g;
+        lse = l.whole_lse + copy * l.copy_floats + ((int64_t)seq * a.h_q + head) * a.s_q + tok;
+        return l.whole_o + copy * l.copy_floats + (((int64_t)seq * a.s_q + tok) * a.h_q + head) * D;
+      }
+      // a piece that starts inside its item is the first of its CTA, one that ends inside it the last
+      const int64_t slot = 2 * ((p.c0 + piece) * l.row_tiles + p.rt) + ((p.c0 + piece) * p.run <= p.s0 ? 1 : 0);
+      const int64_t at = slot * l.part_rows + copy * l.tile + p.in_tile;
+      lse = l.part_lse + at;
+      return l.part_o + at * D;
+    };
+    const int q = threadIdx.x / kVec, d4 = threadIdx.x % kVec;
+    int held = 1;  // rows, as a power of two
+    while (held < rows) held *= 2;
+    const int ways = RP / held, r = q & (held - 1), way = q / held;
+    const bool mine = r < rows;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float z = 0.f;
+    for (int b0 = 0; b0 < most; b0 += kFoldMost) {
+      const int np = min(kFoldMost, most - b0);
+      for (int u = threadIdx.x; u < np * held; u += kFoldThreads) {
+        const int i = u / held, row = u & (held - 1);
+        float w = -INFINITY;
+        const float* src = nullptr;
+        if (row < rows && b0 + i < rows_s[row].n + rows_o[row].n) {
+          const float* lse;
+          src = source(row, b0 + i, lse);
+          w = *lse;
+        }
+        s_w[i][row] = w;
+        s_src[i][row] = src;
+      }
+      __syncthreads();
+      if (threadIdx.x < rows) {
+        float top = s_ref[threadIdx.x];
+        for (int i = 0; i < np; ++i) top = fmaxf(top, s_w[i][threadIdx.x]);
+        s_old[threadIdx.x] = top == -INFINITY ? 0.f : ex2(s_ref[threadIdx.x] - top);
+        s_ref[threadIdx.x] = top;
+      }
+      __syncthreads();
+      if (mine) {
+        const float top = s_ref[r], ref = top == -INFINITY ? 0.f : top, old = s_old[r];
+        z *= old;
+        acc.x *= old;
+        acc.y *= old;
+        acc.z *= old;
+        acc.w *= old;
+        const int here = min(np, rows_s[r].n + rows_o[r].n - b0);
 #pragma unroll 4
-      for (int i = way; i < here; i += ways) {
-        const float f = ex2(s_w[i][r] - ref);
-        const float4 v = reinterpret_cast<const float4*>(s_src[i][r])[d4];
-        z += f;
-        acc.x += v.x * f;
-        acc.y += v.y * f;
-        acc.z += v.z * f;
-        acc.w += v.w * f;
+        for (int i = way; i < here; i += ways) {
+          const float f = ex2(s_w[i][r] - ref);
+          const float4 v = reinterpret_cast<const float4*>(s_src[i][r])[d4];
+          z += f;
+          acc.x += v.x * f;
+          acc.y += v.y * f;
+          acc.z += v.z * f;
+          acc.w += v.w * f;
+        }
+      }
+      __syncthreads();
+    }
+    if (ways > 1) {
+      s_acc[threadIdx.x] = acc;
+      if (d4 == 0) s_z[q] = z;
+      __syncthreads();
+      if (way > 0) continue;
+      for (int w = 1; w < ways; ++w) {
+        const float4 v = s_acc[(w * held + r) * kVec + d4];
+        z += s_z[w * held + r];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
       }
     }
-    __syncthreads();
+    if (!mine) continue;
+    const int row = r0 + r;
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    const int tok = row / a.g, head = kvh * a.g + row % a.g;
+    const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
+    const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    if (a.out_fp32)
+      reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = o;
+    else
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
+          make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
+    if (d4 == 0)
+      a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (s_ref[r] + log2f(z)) * kLn2;
   }
-  if (ways > 1) {
-    s_acc[threadIdx.x] = acc;
-    if (d4 == 0) s_z[q] = z;
-    __syncthreads();
-    if (way > 0) return;
-    for (int w = 1; w < ways; ++w) {
-      const float4 v = s_acc[(w * held + r) * kVec + d4];
-      z += s_z[w * held + r];
-      acc.x += v.x;
-      acc.y += v.y;
-      acc.z += v.z;
-      acc.w += v.w;
-    }
-  }
-  if (!mine) return;
-  const int row = r0 + r;
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  const int tok = row / a.g, head = kvh * a.g + row % a.g;
-  const int64_t orow = ((int64_t)seq * a.s_q + tok) * a.h_q + head;
-  const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (a.out_fp32)
-    reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D)[d4] = o;
-  else
-    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D)[d4] =
-        make_uint2(pack_bf16(o.x, o.y), pack_bf16(o.z, o.w));
-  if (d4 == 0)
-    a.lse[((int64_t)seq * a.h_q + head) * a.s_q + tok] = z == 0.f ? -INFINITY : (s_ref[r] + log2f(z)) * kLn2;
 }
 
 // f(kernel of the shared keys, its shape, kernel of the own keys, its shape)
@@ -310,12 +323,17 @@ cudaError_t launch_attn_decode_shared(const attn_decode_shared_params& p, bool w
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cfg.gridDim = dim3((unsigned)(q.n * q.cache.h_kv), (unsigned)((a.rows + RP - 1) / RP));
+    // kv heads of a CTA: as many as leave work for every SM several times over (where lists lie is
+    // looked up once for them)
+    const int64_t blocks = (a.rows + RP - 1) / RP;
+    int64_t heads = q.n * q.cache.h_kv * blocks / ((int64_t)sm_count() * 8);
+    heads = heads < 1 ? 1 : heads > q.cache.h_kv ? q.cache.h_kv : heads;
+    cfg.gridDim = dim3((unsigned)(q.n * ((q.cache.h_kv + heads - 1) / heads)), (unsigned)blocks);
     cfg.blockDim = dim3(kFoldThreads);
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     return cudaLaunchKernelEx(&cfg, decode_shared_fold_kernel<D>, a, part_of<KS>(s, ss), part_of<KO>(o, so),
-                              (int)p.n_groups);
+                              (int)p.n_groups, (int)heads);
   });
 }
 
