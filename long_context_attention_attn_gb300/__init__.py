@@ -527,54 +527,59 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, me
 
 
 def _rotation(freqs, index: int, interleaved: bool, offset: int, amplitude: float) -> Rotation:
-    if freqs.dim() != 1 or freqs.dtype != torch.float64 or not freqs.is_contiguous():
+    shape = freqs.shape
+    if len(shape) != 1 or freqs.dtype != torch.float64 or not freqs.is_contiguous():
         raise ValueError("freqs must be a contiguous fp64 [rot / 2] tensor")
     if freqs.get_device() != index:
         raise ValueError("all tensors of a call must be on one CUDA device")
     if not 0.0 < amplitude < math.inf:
         raise ValueError("amplitude must be positive and finite")
-    return Rotation(freqs.data_ptr(), 2 * freqs.shape[0], offset, 1 if interleaved else 0, amplitude)
+    return Rotation(freqs.data_ptr(), 2 * shape[0], offset, 1 if interleaved else 0, amplitude)
+
+
+def _rope_rows(x, out, b: int, s: int, d: int, kind, index: int, what: str):
+    """(out, its address, heads, row strides of x and out) of one tensor to turn: out is allocated where None."""
+    shape = x.shape
+    if (len(shape) != 4 or shape[0] != b or shape[1] != s or shape[3] != d or x.dtype != kind
+            or x.get_device() != index):
+        raise ValueError(f"{what}: q and k must be [b, s, h, d] tensors of one b, s, d, type and CUDA device")
+    step = _row_stride(x, what)
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+        return out, out.data_ptr(), shape[2], step, shape[2] * d
+    if out.shape != shape or out.dtype != kind or out.get_device() != index:
+        raise ValueError(f"{what}_out must have the shape, type and device of {what}")
+    return out, out.data_ptr(), shape[2], step, _row_stride(out, what + "_out")
 
 
 def _rope_call(q, k, pos, freqs, interleaved, offset, amplitude, q_out, k_out, inverse):
     one = k if q is None else q
     if one is None:
         raise ValueError("rope: q or k must be given")
-    index = one.get_device()
+    index, kind, shape = one.get_device(), one.dtype, one.shape
     if index < 0:
         raise ValueError("gb300attn runs on CUDA tensors only")
-    if one.dim() != 4 or one.dtype not in (torch.bfloat16, torch.float32):
+    if len(shape) != 4 or (kind != torch.bfloat16 and kind != torch.float32):
         raise ValueError("q / k must be bf16 or fp32 [b, s, h, d] tensors")
-    b, s, _, d = one.shape
-    p = RopeParams()
-    p.pos, p.tokens, p.d = _index(pos, (b, s), index, "pos"), b * s, d
-    p.fp32, p.inverse = one.dtype == torch.float32, inverse
-    p.rotation = _rotation(freqs, index, interleaved, offset, amplitude)
-    out = []
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError(f"{name}_out without {name}")
-            out.append(None)
-            continue
-        h = x.shape[2] if x.dim() == 4 else 0
-        if y is None:
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        for t, what in ((x, name), (y, name + "_out")):
-            if t.shape != (b, s, h, d) or t.dtype != one.dtype:
-                raise ValueError(f"{what}: q and k (and their outputs) share b, s, d and the type")
-            if t.get_device() != index:
-                raise ValueError("all tensors of a call must be on one CUDA device")
-        if name == "q":
-            p.q, p.q_out, p.h_q = x.data_ptr(), y.data_ptr(), h
-            p.q_stride, p.q_out_stride = _row_stride(x, "q"), _row_stride(y, "q_out")
-        else:
-            p.k, p.k_out, p.h_k = x.data_ptr(), y.data_ptr(), h
-            p.k_stride, p.k_out_stride = _row_stride(x, "k"), _row_stride(y, "k_out")
-        out.append(y)
-    if b * s > 0 and p.h_q + p.h_k > 0:
+    b, s, _, d = shape
+    q_ptr = q_dst = k_ptr = k_dst = None
+    h_q = h_k = q_step = k_step = q_out_step = k_out_step = 0
+    if q is not None:
+        q_out, q_dst, h_q, q_step, q_out_step = _rope_rows(q, q_out, b, s, d, kind, index, "q")
+        q_ptr = q.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        k_out, k_dst, h_k, k_step, k_out_step = _rope_rows(k, k_out, b, s, d, kind, index, "k")
+        k_ptr = k.data_ptr()
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    p = RopeParams(q_ptr, k_ptr, q_dst, k_dst, _index(pos, (b, s), index, "pos"), b * s, h_q, h_k, d, q_step, k_step,
+                   q_out_step, k_out_step, 1 if kind == torch.float32 else 0, inverse,
+                   _rotation(freqs, index, interleaved, offset, amplitude))
+    if b * s > 0 and h_q + h_k > 0:
         _check(_on_device(index, lib().attn_rope, ctypes.byref(p)), "attn_rope")
-    return tuple(out)
+    return q_out, k_out
 
 
 def rope(q, k, pos, freqs, *, interleaved: bool = False, offset: int = 0, amplitude: float = 1.0, q_out=None,
@@ -627,7 +632,10 @@ def _kv_cache(k_cache, v_cache, k_scale, v_scale):
 
 def _row_stride(x, what: str = "k / v") -> int:
     """Elements between consecutive token rows of [b, s, h, d] (sizes of one have no stride)."""
-    (b, s, h, d), st = x.shape, x.stride()
+    b, s, h, d = x.shape
+    if x.is_contiguous():
+        return h * d
+    st = x.stride()
     step = st[1] if s > 1 else st[0] if b > 1 else h * d
     if (d > 1 and st[3] != 1) or (h > 1 and st[2] != d) or (s > 1 and b > 1 and st[0] != s * step):
         raise ValueError(f"{what}: heads must be contiguous and token rows evenly spaced")
@@ -701,21 +709,26 @@ def kv_cache_append_rope(q, k, v, k_cache, v_cache, k_scale, v_scale, page_table
     belong to no sequence's new tokens stay as they are, those of q_out too; a row must not belong to two."""
     a, index, some = _append_params(k, v, k_cache, v_cache, k_scale, v_scale, page_table, start, lens, tok_start,
                                     max_new)
-    p = KvAppendRopeParams(a, _rotation(freqs, index, interleaved, offset, amplitude))
+    turning = _rotation(freqs, index, interleaved, offset, amplitude)
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
+        p = KvAppendRopeParams(a, turning, None, None, 0, 0, 0)
     else:
-        if q_out is None:
+        b, s, _, d = k.shape
+        shape = q.shape
+        if (len(shape) != 4 or shape[0] != b or shape[1] != s or shape[3] != d or q.dtype != torch.bfloat16
+                or q.get_device() != index):
+            raise ValueError("q must be a bf16 [b, s, h_q, d] tensor with the rows, head dim and device of k")
+        step = _row_stride(q, "q")
+        if q_out is None or q_out is q:
             q_out = q
-        for t, what in ((q, "q"), (q_out, "q_out")):
-            if (t.dim() != 4 or t.dtype != torch.bfloat16 or t.shape[:2] != k.shape[:2] or t.shape[3] != k.shape[3]
-                    or t.shape[2] != q.shape[2]):
-                raise ValueError(f"{what} must be a bf16 [b, s, h_q, d] tensor with the rows and head dim of k")
-            if t.get_device() != index:
-                raise ValueError("all tensors of a call must be on one CUDA device")
-        p.q, p.q_out, p.h_q = q.data_ptr(), q_out.data_ptr(), q.shape[2]
-        p.q_stride, p.q_out_stride = _row_stride(q, "q"), _row_stride(q_out, "q_out")
+            p = KvAppendRopeParams(a, turning, q.data_ptr(), q.data_ptr(), shape[2], step, step)
+        else:
+            if q_out.shape != shape or q_out.dtype != torch.bfloat16 or q_out.get_device() != index:
+                raise ValueError("q_out must have the shape, type and device of q")
+            p = KvAppendRopeParams(a, turning, q.data_ptr(), q_out.data_ptr(), shape[2], step,
+                                   _row_stride(q_out, "q_out"))
     if some:
         _check(_on_device(index, lib().attn_kv_append_rope, ctypes.byref(p)), "attn_kv_append_rope")
     return q_out
