@@ -46,7 +46,7 @@ __device__ __forceinline__ void turn_q(const AppendArgs& a, const TurnArgs& t, u
     const int64_t row = row0 + j;
     if (row < 0 || row >= a.tokens) continue;
     // (positions past 31 bits wrap: no page table goes there)
-    turn_token<__nv_bfloat16, kPairs>(t.q + row * t.q_stride, t.q_out + row * t.q_out_stride, nullptr, nullptr, D,
+    turn_token<__nv_bfloat16, kPairs, 2, false>(t.q + row * t.q_stride, t.q_out + row * t.q_out_stride, nullptr, nullptr, D,
                                       t.h_q, h0, h1, t.copy, t.turning, (int)((uint32_t)start + (uint32_t)j), turns,
                                       tab + threadIdx.x / 32 * kMaxRot);
   }
@@ -111,8 +111,8 @@ __device__ __forceinline__ void append_unit(const AppendArgs& a, const Turning& 
   for (int c = 0; c < kC; ++c) {
     r[c][0] = r[c][1] = make_uint4(0u, 0u, 0u, 0u);
     if (c * T + tid < chunks) {
-      r[c][0] = load_stream(row + (int64_t)c * kStep * a.token_stride + va);
-      r[c][1] = load_stream(row + (int64_t)c * kStep * a.token_stride + vb);
+      r[c][0] = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)c * kStep * a.token_stride + va));
+      r[c][1] = __ldg(reinterpret_cast<const uint4*>(row + (int64_t)c * kStep * a.token_stride + vb));
     }
   }
   float x[kC][16];
@@ -193,8 +193,9 @@ __device__ __forceinline__ void append_unit(const AppendArgs& a, const Turning& 
   if (tid == 0) *scale = now;
 }
 
+// (two prompts of 32768 tokens: 276 us at 80 registers, 254 at 64)
 template <int T, int kC>
-constexpr int kMinCtas = T <= 128 ? 6 : T == 256 ? 3 : 1;
+constexpr int kMinCtas = T <= 128 ? 8 : T == 256 ? 4 : 1;
 
 template <int T, int kC, int D, bool kPairs>
 __global__ void __launch_bounds__(T < 128 ? 128 : T, kMinCtas<T, kC>)
@@ -229,8 +230,8 @@ cudaError_t launch_t(const AppendArgs& a, TurnArgs& t, bool interleaved, cudaStr
   return cudaGetLastError();
 }
 
-// Two chunks a thread (their 16 values in fp32 and their angles take 80 registers), four
-// for units of more than 1024.
+// Two chunks a thread (four, with their 16 values in fp32, took 161 registers: 323 us for two
+// prompts of 32768 tokens where two took 277), four for units of more than 1024.
 template <int D>
 cudaError_t launch_d(const AppendArgs& a, TurnArgs& t, bool interleaved, cudaStream_t st) {
   const int chunks = (a.max_new < a.page_size ? a.max_new : a.page_size) * (D / 16);

@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
   for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < a.items; item += step) {
     const int64_t token = item / a.chunks;
     const int h0 = (int)(item - token * a.chunks) * a.heads_per_chunk;
-    turn_token<E, kInterleaved>(static_cast<const E*>(a.q) + token * a.q_stride,
+    turn_token<E, kInterleaved, 4, true>(static_cast<const E*>(a.q) + token * a.q_stride,
                                 static_cast<E*>(a.q_out) + token * a.q_out_stride,
                                 static_cast<const E*>(a.k) + token * a.k_stride,
                                 static_cast<E*>(a.k_out) + token * a.k_out_stride, a.d, a.h_q, h0,
@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
 template <typename E>
 cudaError_t launch(const RopeArgs& a, bool interleaved, cudaStream_t st) {
   const int64_t need = (a.items + kWarps - 1) / kWarps;
-  const int64_t most = (int64_t)sm_count() * 64;
+  // (65536 tokens of 40 heads of 192: 325 us with 12 CTAs per SM, 299 with 24, 299 with 64)
+  const int64_t most = (int64_t)sm_count() * 24;
   const unsigned grid = (unsigned)(need < most ? need : most);
   if (interleaved)
     rope_kernel<E, true><<<grid, kWarps * 32, 0, st>>>(a);
