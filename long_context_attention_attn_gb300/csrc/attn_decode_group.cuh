@@ -24,6 +24,9 @@
 // Every wait ends as in attn_decode_tensor.cuh.
 #pragma once
 
+// A tile: every row sees all of it; all of its keys exist.
+enum { kAllRows = 1, kAllKeys = 2 };
+
 struct GroupTune {
   static constexpr int kBlock = 128;  // a tile
   // q's conversion, the first copies' latency and the last O, in tiles
@@ -124,7 +127,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
   __shared__ int64_t before[kThreads + 1];
   // of a tile's groups of 16 keys: scales, V's logarithms and inverses, and whether they
   // have a page; the least and the largest scale of V, its first key
-  // and whether every row sees all of it
+  // and kAllRows, kAllKeys
   __shared__ __align__(16) float s_ks[C::kMeta][8], s_vs[C::kMeta][8], s_lv[C::kMeta][8], s_iv[C::kMeta][8];
   __shared__ uint8_t s_ok[C::kMeta][8];
   __shared__ float2 s_range[C::kMeta];
@@ -223,8 +226,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         const int key = key_of(t), key0 = key - (lane & 7) * 16;
         const bool take = valid(pid0);
         const bool whole = ((__ballot_sync(0xffffffffu, take) >> (lane & 24)) & 0xffu) == 0xffu;
-        const bool all = whole && key0 + kKeys <= p.span.hi && (key0 >= p.span.lo || key0 + kKeys <= p.span.sink_hi) &&
-                         key0 + kKeys - 1 <= p_first &&
+        const bool keys = whole && key0 + kKeys <= p.span.hi;
+        const bool all = keys && key0 + kKeys - 1 <= p_first &&
                          (a.window < 0 || p_last - key0 <= a.window || key0 + kKeys - 1 < a.sink);
         float2 range = make_float2(vs, vs);
 #pragma unroll
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
             s_iv[m][g] = take ? 1.f / vs : 0.f;
             s_ok[m][g] = take;
             if (g == 0) {
-              s_tile[m] = make_int2(key0, all);
+              s_tile[m] = make_int2(key0, (all ? kAllRows : 0) | (keys ? kAllKeys : 0));
               s_range[m] = range;
             }
             if (take) {
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
           w[4 * c + 3] = x.w;
         }
         const int2 tile = s_tile[m];
-        if (!tile.y) {
+        if (!(tile.y & kAllRows)) {
           const int key = tile.x + k;
           const bool some = s_ok[m][k >> 4] && key < p.span.hi && (key >= p.span.lo || key < p.span.sink_hi);
           if (some) {
@@ -480,7 +483,13 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         const int m = i % C::kMeta;
         if (ok) ok = mbar_wait(&bars.meta_full[g], c & 1, ctx);
         __syncwarp();
-        const bool all_seen = s_tile[m].y;
+        const int2 tile = s_tile[m];
+        const bool all_seen = tile.y & kAllRows;
+        // this row sees all of the tile, or nothing
+        const bool full = tile.x + kKeys - 1 <= pos &&
+                          (a.window < 0 || pos - tile.x <= a.window || tile.x + kKeys - 1 < a.sink);
+        const bool none = tile.x > pos || (a.window >= 0 && pos - (tile.x + kKeys - 1) > a.window && tile.x >= a.sink);
+        const bool quick = all_seen || ((tile.y & kAllKeys) && __all_sync(0xffffffffu, full || none));
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
           const int col0 = h * 64;
@@ -488,10 +497,11 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
           __syncwarp();
           tc_fence_after();
           if (busy) {
-            // Where every row sees all keys and b * v_scale is far from fp32's ends (it is but for pages
-            // of zeros and the like), P * v_scale comes straight from the exponential, and the sum of
-            // P from the sums over 16 keys, which tell of values past f16's range too.
-            bool done = all_seen;
+            // Where each row sees all keys or none and b * v_scale is far from fp32's ends (it is but for
+            // pages of zeros and the like), P * v_scale comes straight from the exponential, and the
+            // sum of P from the sums over 16 keys, which tell of values past f16's range too (and
+            // of NaN, which may be out of sight).
+            bool done = quick;
             if (done) {
               uint32_t pk[32];
               float sum = 0.f, most = 0.f;
@@ -501,7 +511,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
               tmem_wait_ld();
 #pragma unroll
               for (int x = 0; x < 4; ++x) {  // 16 keys
-                const float f = fac * s_ks[m][4 * h + x], o = s_lv[m][4 * h + x] + shift;
+                const float f = fac * s_ks[m][4 * h + x], o = s_lv[m][4 * h + x] + (none ? -INFINITY : shift);
 #pragma unroll
                 for (int j = 8 * x; j < 8 * x + 8; ++j) e[j] = __ffma2_rn(e[j], make_float2(f, f), make_float2(o, o));
               }
@@ -520,7 +530,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                 sum += y * (s_iv[m][4 * h + x] * b_inv);
               }
               const float2 range = s_range[m];
-              done = __all_sync(0xffffffffu, !(most > 32768.f) && !(sum > 16384.f) && b * range.y < 0x1p60f &&
+              done = __all_sync(0xffffffffu, most <= 32768.f && sum <= 16384.f && b * range.y < 0x1p60f &&
                                                  b * range.x > 0x1p-60f);
               if (done) {
                 l += sum;
@@ -529,7 +539,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
             }
             if (!done) {
               auto sees = [&](int j) {  // key j of the tile
-                const int key = s_tile[m].x + j;
+                const int key = tile.x + j;
                 return s_ok[m][j >> 4] && key < p.span.hi && key <= pos &&
                        (a.window < 0 || pos - key <= a.window || key < a.sink);
               };

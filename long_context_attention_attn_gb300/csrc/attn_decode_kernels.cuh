@@ -203,6 +203,7 @@ __device__ __forceinline__ Entry entry_of(const DecodeArgs& a, int i, int block,
     int p0 = 0;
     if (a.window >= 0 && e.len > 0) {  // the first position of any that sees a key
       p0 = 0x7fffffff;
+#pragma unroll 8
       for (int m = 0; m < members; ++m) {
         const int len = a.lens[e.first + m];
         if (len > 0) p0 = min(p0, max(len - a.s_q, 0));
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     at = blockIdx.x / a.row_tiles * run;
     end = min(at + run, total);
     if (at >= end) {
-      if constexpr (M == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (M == kOwn && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
       return;
     }
     // the sequence of the run's first block
@@ -1143,8 +1144,9 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
       __syncthreads();  // the ring, q and the row values are free again
     }
   }
-  // (this grid may begin before the one of the shared keys ends, but does not end before)
-  if constexpr (M == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (this grid may begin before the one of the shared keys ends, but does not end before: its
+  // first CTA stays, the others make room)
+  if (M == kOwn && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // Folds the partials of an item that several CTAs shared, and writes the empty

@@ -275,8 +275,22 @@ Part part_of(const DecodeArgs& a, const Shape& sh) {
 
 }  // namespace
 
+// Whether attn_decode does it better: no group has two members, or the problem is so
+// small (by the page table's width) that it takes a cluster of CTAs per item, one launch in
+// place of three that wait for one another (and uses no scratch).  us of attn_decode and of
+// the three, Hq 32, Hkv 8, d 128, own tokens 60 to 200, by clusters: 4 sequences behind 2048
+// tokens 9.1 / 15.4, behind 8192 15.1 / 20.1; 16 behind 2048 14.7 / 27.3; by the list: 8 behind
+// 8192 23.3 / 25.5, behind 16384 35.1 / 28.8; 32 behind 4096 37.4 / 33.3.
+static cudaError_t plain_is_better(const attn_decode_shared_params& p, bool* plain, size_t* bytes) {
+  const cudaError_t e = decode_workspace(p.base, bytes);
+  *plain = p.max_group <= 1 || *bytes == 0;
+  return e;
+}
+
 cudaError_t decode_shared_workspace(const attn_decode_shared_params& p, size_t* bytes) {
-  if (p.max_group <= 1) return decode_workspace(p.base, bytes);
+  bool plain = false;
+  const cudaError_t e = plain_is_better(p, &plain, bytes);
+  if (e != cudaSuccess || plain) return e;
   return dispatch(p, [&](auto ks, const Shape& ss, auto ko, const Shape& so) {
     using KS = decltype(ks);
     *bytes = 4 * (part_floats<decltype(ks)>(ss, p.base.cache.d) + part_floats<decltype(ko)>(so, p.base.cache.d) +
@@ -287,8 +301,11 @@ cudaError_t decode_shared_workspace(const attn_decode_shared_params& p, size_t* 
 
 cudaError_t launch_attn_decode_shared(const attn_decode_shared_params& p, bool withhold, cudaStream_t st) {
   const attn_decode_params& q = p.base;
-  // (no group has two members: nothing is read twice)
-  if (p.max_group <= 1) return launch_attn_decode(q, withhold, st);
+  bool plain = false;
+  size_t bytes = 0;
+  const cudaError_t e = plain_is_better(p, &plain, &bytes);
+  if (e != cudaSuccess) return e;
+  if (plain) return launch_attn_decode(q, withhold, st);
   return dispatch(p, [&](auto ks, const Shape& ss, auto ko, const Shape& so) {
     using KS = decltype(ks);
     using KO = decltype(ko);

@@ -831,6 +831,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     tc_fence_after();
     tmem_dealloc(tmem, C::kCols);
   }
-  // (this grid may begin before the one of the shared keys ends, but does not end before)
-  if constexpr (M == kOwn) asm volatile("griddepcontrol.wait;" ::: "memory");
+  // (this grid may begin before the one of the shared keys ends, but does not end before: its
+  // first CTA stays, the others make room)
+  if (M == kOwn && blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
