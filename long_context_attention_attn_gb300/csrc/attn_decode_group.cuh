@@ -538,11 +538,11 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
               }
             }
             if (!done) {
-              auto sees = [&](int j) {  // key j of the tile
-                const int key = tile.x + j;
-                return s_ok[m][j >> 4] && key < p.span.hi && key <= pos &&
-                       (a.window < 0 || pos - key <= a.window || key < a.sink);
-              };
+              // keys of the tile that this row sees: up to j_last, from j_first on or below j_sink, on pages
+              // that there are
+              const int j_last = min(pos, p.span.hi - 1) - tile.x, j_first = a.window < 0 ? 0 : max(pos - tile.x, 0) - a.window,
+                        j_sink = a.window < 0 ? 0 : a.sink - tile.x;
+              auto sees = [&](int j) { return j <= j_last && (j >= j_first || j < j_sink); };
               // raise the references where a score passes them by more than kRescale, to the largest of
               // these keys
               float x = -INFINITY, xo = -INFINITY;
@@ -554,7 +554,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                 const float f = fac * s_ks[m][j0 / 16], lv = lg2(s_vs[m][j0 / 16]);
                 float y = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) y = fmaxf(y, all_seen || sees(j0 + j) ? e[j] * f : -INFINITY);
+                for (int j = 0; j < 16; ++j) y = fmaxf(y, sees(j0 + j) ? e[j] * f : -INFINITY);
+                if (!s_ok[m][j0 / 16]) y = -INFINITY;
                 x = fmaxf(x, y);
                 xo = fmaxf(xo, y + lv);
               }
@@ -594,14 +595,13 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                 // (b * v_scale may pass fp32's range where keys are out of sight or of next to no weight: 0
                 // * infinity is NaN, so P takes the largest finite value)
                 const float f = fac * s_ks[m][(col0 + cc) / 16], v = fminf(b * s_vs[m][(col0 + cc) / 16], FLT_MAX);
+                const bool here = s_ok[m][(col0 + cc) / 16];
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                   e[j] = __ffma2_rn(e[j], make_float2(f, f), make_float2(nm, nm));
-                  if (!all_seen) {
-                    if (!sees(col0 + cc + 2 * j)) e[j].x = -INFINITY;
-                    if (!sees(col0 + cc + 2 * j + 1)) e[j].y = -INFINITY;
-                  }
+                  if (!here || !sees(col0 + cc + 2 * j)) e[j].x = -INFINITY;
+                  if (!here || !sees(col0 + cc + 2 * j + 1)) e[j].y = -INFINITY;
                   e[j] = make_float2(ex2(e[j].x), ex2(e[j].y));
                   l += e[j].x + e[j].y;
                   e[j] = __fmul2_rn(e[j], make_float2(v, v));

@@ -537,7 +537,7 @@ struct RowPlace {
     if constexpr (M == kShared) {
       seq = p.first + tok / a.s_q;
       t = tok % a.s_q;
-      pos = a.lens[seq] - a.s_q + t;
+      pos = max(a.lens[seq], 0) - a.s_q + t;
     } else {
       pos = p.len - a.s_q + t;
     }

@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kFoldThreads)
   }
   const int64_t run_s = run_length(as, before_s[kThreads] * a.h_kv, shared.shortest);
   const int64_t run_o = run_length(ao, before_o[kThreads] * a.h_kv, own.shortest);
-  const int len = a.lens[seq];
+  const int len = max(a.lens[seq], 0);
   bool waited = false;
   for (int kvh = kvh0; kvh < kvh1; ++kvh) {
     __syncthreads();  // (the last head's partials have been read)
