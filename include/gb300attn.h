@@ -561,9 +561,11 @@ GB300ATTN_API int attn_decode_test_timeout(const attn_decode_params* p, attn_str
  *                (sequences of no group must have shared_pages 0); NULL with
  *                n_groups = 1: all sequences are one group
  *  max_group     the most sequences of a group (sizes the launch), 1 .. n; larger
- *                groups are right, but slower.  With 1 nothing is shared and this is
- *                attn_decode.
- * Results are bit-identical from run to run, and differ from attn_decode's by the
+ *                groups are right, but slower
+ * With max_group 1, and where the problem is so small by its table's width that
+ * attn_decode needs one launch and no scratch (some 16 sequences of 2k tokens, 4 of
+ * 8k), this is attn_decode, which is then the faster.  A query row with an infinity or
+ * NaN gives NaN where it sees a key.  Results are bit-identical from run to run, and differ from attn_decode's by the
  * order of sums.  Where groups disagree with what is said here results are
  * unspecified; no other memory is read or written. */
 typedef struct attn_decode_shared_params {

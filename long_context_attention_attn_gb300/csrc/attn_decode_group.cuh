@@ -675,8 +675,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
     __syncthreads();
     tc_fence_after();
   }
-  // copies and products have ended (so they have, unless a wait ran out)
-  if (warp == 12 && lane == 0 && !ok)
+  // copies and products have ended (so they have, unless a wait ran out somewhere)
+  if (warp == 12 && lane == 0)
     for (uint32_t j = loaded < kStages ? 0 : loaded - kStages; j < loaded; ++j)
       mbar_wait_drain(&bars.full[j % kStages], (j / kStages) & 1, nullptr);
   if (warp >= 13 && lane == 0) {
