@@ -21,6 +21,11 @@
 // keys: P of a half lies over its S, and the S of the next tile's half is computed as soon
 // as O has it, while the softmax works on the other half.
 //
+// Bound by latency: 2048 rows over 32768 keys, Hkv 8, d 128, in 259 us (1070 TFLOP/s, 56 % of
+// the measured rate), tensor pipe 42 % and issue 49 % of the time.  A half of 64 keys takes a softmax
+// warp some 2000 cycles for 280 instructions, two such warps to a scheduler; from P to O
+// to the next S of the same half are 1700 more, beside the other half's softmax.
+//
 // Every wait ends as in attn_decode_tensor.cuh.
 #pragma once
 
@@ -29,8 +34,13 @@ enum { kAllRows = 1, kAllKeys = 2 };
 
 struct GroupTune {
   static constexpr int kBlock = 128;  // a tile
-  // q's conversion, the first copies' latency and the last O, in tiles
-  static constexpr int kItemCost = 3;
+  // q's conversion, the first copies' latency and the last O, in tiles (us with 1 / 3 / 6: three
+  // groups under a window 37.8 / 34.1 / 34.5; 16 sequences behind 60000 tokens, d 64, 46 / 45 / 38;
+  // 64 behind 8192 71.9 / 71.6 / 70.5)
+  static constexpr int kItemCost = 6;
+  // Longer runs take fewer CTAs, beside which the own keys begin: that pays only where those
+  // are many (us with 4 / 5 / 8: 64 sequences behind 2048 tokens, own 60 to 200, 35.5 / 42.8 / 48.2;
+  // 64 behind 8192, own 100 to 2000, 71.7 / 67.8 / 63.9)
   static constexpr int kMinRun = 4;
 };
 

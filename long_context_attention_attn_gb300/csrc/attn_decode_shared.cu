@@ -12,7 +12,8 @@
 //
 // The shared keys have members * s_q * g rows, 4 d flops each for 2 d bytes: from about
 // 140 rows on they are bound by the products, below by reading the keys; the own
-// keys by reading them (a group's rows would be 2 d bytes each without sharing).
+// keys by reading them.  us (attn_decode's in brackets), Hkv 8, d 128: 64 sequences behind
+// 8192 tokens, Hq 32, 45 (111); 64 behind 16384 57 (207); 128 behind 32768, Hq 128, 303.
 #include "attn_decode_kernels.cuh"
 
 namespace gb300 {
@@ -238,6 +239,9 @@ cudaError_t with_both(const attn_decode_shared_params& p, F&& f) {
     return with_rows<D, kOwn>(q, 0, rows, [&](auto ko, const Shape& so) { return f(ks, ss, ko, so); });
   };
   if constexpr (D < 256) {
+    // (us by the warp-level kernel and by this one, d 128: 24 rows over 32768 keys 34.6 / 45.9, 32 rows
+    // 36.5 / 53.6; by attn_decode_tensor.cuh and by this one: 48 rows 45.7 / 46.1, 64 rows 46.3 / 47.7, d 64
+    // 40.3 / 37.5; 2048 rows with 128 and with 256 rows a CTA 395 / 308)
     if (most > 32) {
       auto use = [&](auto k) {
         Shape sh;
@@ -343,7 +347,7 @@ cudaError_t launch_attn_decode_shared(const attn_decode_shared_params& p, bool w
     // kv heads of a CTA: as many as leave work for every SM several times over (where lists lie is
     // looked up once for them)
     const int64_t blocks = (a.rows + RP - 1) / RP;
-    int64_t heads = q.n * q.cache.h_kv * blocks / ((int64_t)sm_count() * 8);
+    int64_t heads = q.n * q.cache.h_kv * blocks / ((int64_t)sm_count() * 3);
     heads = heads < 1 ? 1 : heads > q.cache.h_kv ? q.cache.h_kv : heads;
     cfg.gridDim = dim3((unsigned)(q.n * ((q.cache.h_kv + heads - 1) / heads)), (unsigned)blocks);
     cfg.blockDim = dim3(kFoldThreads);

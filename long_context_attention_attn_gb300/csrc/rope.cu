@@ -4,7 +4,9 @@
 //   y1 = amp (x1 cos t - x2 sin t),  y2 = amp (x2 cos t + x1 sin t),  t = pos * f_i
 //
 // Bound by HBM: every value is read and written once, with 3 flops.  A warp takes a
-// token: its angles once, for all heads, then 32 heads' worth of rows stream through.
+// token: its angles once, for all heads, then 32 lanes' worth of rows at a time stream
+// through.  65536 tokens of 40 heads of 192 (64 turn): 297 us, 6.79 TB/s; 16384 tokens of 20
+// heads of 128 29 us, 5.7 TB/s.
 #include "internal.h"
 #include "rotation.cuh"
 
