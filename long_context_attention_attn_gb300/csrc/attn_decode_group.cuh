@@ -1,13 +1,17 @@
 // The shared keys of groups with more than 32 rows, on the tensor-memory path, included by
 // attn_decode_shared.cu.
 //
-//   S[rows, keys] = q K^T (e4m3 in, q as two of them),  O[rows, d] += P V (f16 in), fp32 sums
+//   S[rows, keys] = q K^T (8 bits in, q as three e5m2 values),  O[rows, d] += P V (f16 in), fp32 sums
 //
 // K's codes are multiplied as they lie in the cache, without widening: a bf16 value has 8
-// bits, an e4m3 one 4, so q, scaled by its row's power of two to at most 448, is hi + lo with
-// hi = e4m3(q) and lo = e4m3(q - hi), exactly for values down to 2^-10 of the row's largest
-// (below that off by 2^-10 of a unit, 2^-18 of the largest).  Two products in 8 bits cost
-// what one in 16 does.  V is widened to f16, P is f16 as in attn_decode_tensor.cuh,
+// bits, an e5m2 one 3 and a sign, so q, scaled by its row's power of two to at most 57344, is
+// the sum of q0 = e5m2(q), q1 = e5m2(q - q0) and q2 = e5m2(q - q0 - q1): what a rounding leaves is
+// at most 16 units (of the value's 8 bits) after the first, 1 after the second, 0 after the third.
+// That is exact as long as the last of the 8 bits is no less than e5m2's least, 2^-16, which
+// holds for values down to 2^-23 of the row's largest; those below are off by at most 2^-17,
+// 2^-31 of the largest.  (Two e4m3 values take two products in place of three, but leave
+// 2^-18 of the largest: with one value 1000 times the others, in a channel where the keys are
+// zero, scores were off by up to 0.08.)  V is widened to f16, P is f16 as in attn_decode_tensor.cuh,
 // whose references and factors these are.
 //
 // A CTA has two softmax groups of 128 threads (a thread per row) on 128-key tiles: with
@@ -50,12 +54,14 @@ struct GroupCfg {
   static constexpr int kCopies = kTurns ? 2 : 1;  // partials of a row
   static constexpr int kThreads = 32 * 15;
   static constexpr int kKeys = 128;
-  static constexpr int kStages = D == 64 ? 4 : kTurns ? 3 : 2;  // tiles of codes
-  static constexpr int kCodes = kKeys * D;                      // of K (V)
-  static constexpr int kBlock64 = kKeys * 128;                  // 64 d's of V in f16
+  static constexpr int kStages = D == 64 ? 4 : kTurns ? 3 : 2;  // tiles of K's codes
+  // tiles of V's, which wait in registers and as f16 too (one in place of two: no slower)
+  static constexpr int kStagesV = D == 128 && !kTurns ? 1 : kStages;
+  static constexpr int kCodes = kKeys * D;      // of K (V)
+  static constexpr int kBlock64 = kKeys * 128;  // 64 d's of V in f16
   static constexpr int kV16 = D / 64 * kBlock64;
-  static constexpr int kQ = R * D;                              // hi (lo) of q
-  static constexpr int k_off = 2 * kQ, v_off = k_off + kStages * 2 * kCodes;
+  static constexpr int kParts = 3, kQ = R * D;  // of q; bytes of one
+  static constexpr int k_off = kParts * kQ, v8_off = k_off + kStages * kCodes, v_off = v8_off + kStagesV * kCodes;
   static constexpr int nan_off = v_off + 2 * kV16;  // [D][R / 32] bits: rows that see a NaN of V
   static constexpr int bytes = nan_off + D * R / 8 + 1024;  // (and up to 1023 to align)
   // Scales and the like of a tile are kept until its softmax is done: the loader fills
@@ -68,9 +74,9 @@ struct GroupCfg {
   static_assert(bytes <= 232448 - 4096, "shared memory");
 };
 
-// Instruction descriptor: e4m3 A and B (K-major), fp32 D.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
-  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+// Instruction descriptor: e5m2 A, e4m3 B (K-major both), fp32 D.
+__host__ __device__ constexpr uint32_t idesc_codes_f32(int M, int N) {
+  return (1u << 4) | (1u << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 // High word of the descriptor of K-major rows of D bytes, swizzled over D bytes (128 or 64).
 template <int D>
@@ -97,17 +103,16 @@ __device__ __forceinline__ void store8(float* dst, const float* v) {
                : "memory");
 }
 
-// The codes of two values, and of what they leave.
-__device__ __forceinline__ void split_codes(float x, float y, uint32_t& hi, uint32_t& lo) {
-  uint16_t h;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
+// The e5m2 codes of two values, which then are what the codes leave of them.
+__device__ __forceinline__ uint32_t take_codes(float& x, float& y) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(c) : "f"(y), "f"(x));
   uint32_t f;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f) : "h"(h));
+  asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(f) : "h"(c));
   const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&f));
-  uint16_t l;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(l) : "f"(y - back.y), "f"(x - back.x));
-  hi = h;
-  lo = l;
+  x -= back.x;
+  y -= back.y;
+  return c;
 }
 
 template <int D, bool kTurns>
@@ -116,15 +121,16 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
                         const __grid_constant__ CUtensorMap tm_v) {
   using C = GroupCfg<D, kTurns>;
   using T = GroupTune;
-  constexpr int R = C::R, kStages = C::kStages, kKeys = C::kKeys, kUsers = kTurns ? 1 : 2;
+  constexpr int R = C::R, kStages = C::kStages, kStagesV = C::kStagesV, kKeys = C::kKeys, kUsers = kTurns ? 1 : 2;
   extern __shared__ uint8_t smem_raw[];
   struct Bars {
-    uint64_t full[kStages];    // a tile's codes are there
-    uint64_t k_free[kStages];  // its K has been multiplied (by every group that takes it)
-    uint64_t v_free[kStages];  // its V has been read
-    uint64_t v_full[2];        // V is there in f16
-    uint64_t v_used[2];        // and has been multiplied
-    uint64_t q_full, widened;  // of a piece: q in shared memory; all of V widened
+    uint64_t k_full[kStages];    // a tile's codes of K are there
+    uint64_t v_full8[kStagesV];  // and of V
+    uint64_t k_free[kStages];    // its K has been multiplied (by every group that takes it)
+    uint64_t v_free[kStagesV];   // its V has been read
+    uint64_t v_full[2];          // V is there in f16
+    uint64_t v_used[2];          // and has been multiplied
+    uint64_t q_full, widened;    // of a piece: q in shared memory; all of V widened
     // of a group
     uint64_t meta_full[2];     // a tile's scales are there
     uint64_t s_full[2][2];     // half of S is
@@ -151,8 +157,11 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(&bars.full[i], 8);
+      mbar_init(&bars.k_full[i], 8);
       mbar_init(&bars.k_free[i], kUsers);
+    }
+    for (int i = 0; i < kStagesV; ++i) {
+      mbar_init(&bars.v_full8[i], 8);
       mbar_init(&bars.v_free[i], 4);  // (a warp each)
     }
     for (int i = 0; i < 2; ++i) {
@@ -187,7 +196,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
 
   uint32_t i0 = 0, n = 0;  // tiles and pieces before this piece
   uint32_t c0 = 0;         // tiles of this warp's group
-  uint32_t loaded = 0;     // tiles that the loader began
+  uint32_t k_loaded = 0, v_loaded = 0;  // tiles whose copies the loader began
   bool ok = true;
   while (true) {
     if (threadIdx.x == 0) {
@@ -246,15 +255,12 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
           range.y = fmaxf(range.y, __shfl_xor_sync(0xffffffffu, range.y, o));
         }
         for (int u = 0; u < kTurn && t + u < p.t1; ++u, ++i) {
-          const int slot = i % kStages;
-          if (i >= kStages) {
-            ok = wait_on(&bars.k_free[slot], (i / kStages - 1) & 1, ctx);
-            if (ok) ok = wait_on(&bars.v_free[slot], (i / kStages - 1) & 1, ctx);
-          }
+          const int slot = i % kStages, slot_v = i % kStagesV, g = lane & 7, y = key & page_mask;
+          if (i >= kStages) ok = wait_on(&bars.k_free[slot], (i / kStages - 1) & 1, ctx);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           if (lane >> 3 == u) {
-            const int m = i % C::kMeta, g = lane & 7;
+            const int m = i % C::kMeta;
             s_ks[m][g] = take ? ks : 0.f;
             s_vs[m][g] = take ? vs : 0.f;
             s_lv[m][g] = take ? lg2(vs) : 0.f;
@@ -265,27 +271,38 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
               s_range[m] = range;
             }
             if (take) {
-              mbar_arrive_expect_tx(&bars.full[slot], 2 * 16 * D);
-              const int y = key & page_mask;
-              const uint32_t dst = smem_u32(smem + C::k_off + slot * 2 * C::kCodes) + g * 16 * D;
-              tma_load_4d(dst, &tm_k, 0, y, p.kvh, pid0, &bars.full[slot]);
-              tma_load_4d(dst + C::kCodes, &tm_v, 0, y, p.kvh, pid0, &bars.full[slot]);
+              mbar_arrive_expect_tx(&bars.k_full[slot], 16 * D);
+              tma_load_4d(smem_u32(smem + C::k_off + slot * C::kCodes) + g * 16 * D, &tm_k, 0, y, p.kvh, pid0,
+                          &bars.k_full[slot]);
             } else {
-              mbar_arrive(&bars.full[slot]);
+              mbar_arrive(&bars.k_full[slot]);
             }
           }
+          k_loaded = i + 1;
+          if (i >= kStagesV) ok = wait_on(&bars.v_free[slot_v], (i / kStagesV - 1) & 1, ctx);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          if (lane >> 3 == u) {
+            if (take) {
+              mbar_arrive_expect_tx(&bars.v_full8[slot_v], 16 * D);
+              tma_load_4d(smem_u32(smem + C::v8_off + slot_v * C::kCodes) + g * 16 * D, &tm_v, 0, y, p.kvh, pid0,
+                          &bars.v_full8[slot_v]);
+            } else {
+              mbar_arrive(&bars.v_full8[slot_v]);
+            }
+          }
+          v_loaded = i + 1;
         }
         pid0 = pid1;
         pid1 = pid2;
         ks = ks1;
         vs = vs1;
       }
-      if (i > i0) loaded = i;
     } else if (warp >= 13) {
       // ====================================================== products of a group: one thread
       const int g = warp - 13;
       constexpr int kEvery = kTurns ? 2 : 1;
-      constexpr uint32_t idesc_s = idesc_e4m3_f32(128, kKeys / 2), idesc_o = idesc_f16_f32(128, D, false, true);
+      constexpr uint32_t idesc_s = idesc_codes_f32(128, kKeys / 2), idesc_o = idesc_f16_f32(128, D, false, true);
       const int t0 = kTurns ? g : 0;
       if (lane > 0) {
         // (nothing to do)
@@ -294,7 +311,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         // have passed it
         for (int t = 0; t < tiles && ok; ++t) {
           const uint32_t i = i0 + t;
-          ok = mbar_wait(&bars.full[i % kStages], (i / kStages) & 1, ctx);
+          ok = mbar_wait(&bars.k_full[i % kStages], (i / kStages) & 1, ctx);
           if (ok) ok = mbar_wait(&bars.v_full[i & 1], (i >> 1) & 1, ctx);
           if (!ok) break;
           mbar_arrive(&bars.k_free[i % kStages]);
@@ -314,7 +331,7 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
           const int buf = i & 1, slot = i1 % kStages;
           const bool begun = t >= t0, more = t + kEvery < tiles;
           if (begun) ok = mbar_wait(&bars.v_full[buf], (i >> 1) & 1, ctx);
-          const uint32_t v = v_lo + ((buf * C::kV16) >> 4), k = k_lo + ((slot * 2 * C::kCodes) >> 4);
+          const uint32_t v = v_lo + ((buf * C::kV16) >> 4), k = k_lo + ((slot * C::kCodes) >> 4);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (begun) {
@@ -329,13 +346,13 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
               if (h == 1) mma_commit(&bars.v_used[buf]);
             }
             if (more) {
-              if (h == 0) ok = mbar_wait(&bars.full[slot], (i1 / kStages) & 1, ctx);
+              if (h == 0) ok = mbar_wait(&bars.k_full[slot], (i1 / kStages) & 1, ctx);
               if (ok && c > 0) ok = mbar_wait(&bars.o_done[g][h], (c - 1) & 1, ctx);
               if (!ok) break;
               tc_fence_after();
               if (h == 0) mbar_arrive(&bars.meta_full[g]);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {  // hi, then lo
+              for (int kk = 0; kk < C::kParts * (D / 32); ++kk) {  // q0, q1, q2
                 const int part = kk / (D / 32), at = kk % (D / 32) * 32;
                 mma_codes<D>(t_s + h * 64, q_lo + ((part * C::kQ + at) >> 4), k + ((h * 64 * D + at) >> 4), idesc_s,
                              kk > 0 ? 1u : 0u);
@@ -355,11 +372,11 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
       asm volatile("barrier.cta.sync 1, 128;" ::: "memory");
       for (int t = 0; t < tiles; ++t) {
         const uint32_t i = i0 + t;
-        const int slot = i % kStages, buf = i & 1, m = i % C::kMeta;
-        if (ok) ok = wait_on(&bars.full[slot], (i / kStages) & 1, ctx);
+        const int slot = i % kStagesV, buf = i & 1, m = i % C::kMeta;
+        if (ok) ok = wait_on(&bars.v_full8[slot], (i / kStagesV) & 1, ctx);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint8_t* base = smem + C::k_off + slot * 2 * C::kCodes + C::kCodes;
+        const uint8_t* base = smem + C::v8_off + slot * C::kCodes;
         uint32_t w[D / 4];
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {
@@ -434,8 +451,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
       const RowPlace<kShared> to(a, p, mine ? row : 0);
       const int pos = mine ? to.pos : -1;
       if (!kTurns || g == 0) {
-        // ---- q's row (all of its loads at once) as two e4m3 values each, the largest value in
-        // (224, 448]
+        // ---- q's row (all of its loads at once) as three e5m2 values each, the largest value in
+        // (28672, 57344]
         const uint4* src = reinterpret_cast<const uint4*>(a.q + to.orow * D);
         uint4 x[D / 8];
 #pragma unroll
@@ -451,7 +468,8 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         }
         const uint32_t bits = max(top << 16, top & 0xffff0000u);
         const bool finite = bits < 0x7f800000u;
-        const int ex = finite && bits ? max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), -100) : 0;
+        const int over = (bits & 0x7fffffu) > 0x600000u ? 1 : 0;
+        const int ex = finite && bits ? max((int)(bits >> 23) - 127 + over, -100) - 15 : 0;
         const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
         // (a row with an infinity or NaN has no softmax: all of it is NaN)
         const float more = finite ? 0.f : bad;
@@ -459,20 +477,22 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         uint8_t* dst = smem + (kTurns ? 0 : g) * 128 * D;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {  // 16 values
-          uint32_t hi[8], lo[8];
+          uint32_t part[C::kParts][8];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t w[4] = {x[2 * c + u].x, x[2 * c + u].y, x[2 * c + u].z, x[2 * c + u].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              split_codes(__uint_as_float(w[j] << 16) * inv, __uint_as_float(w[j] & 0xffff0000u) * inv, hi[4 * u + j],
-                          lo[4 * u + j]);
+            for (int j = 0; j < 4; ++j) {
+              float y = __uint_as_float(w[j] << 16) * inv, z = __uint_as_float(w[j] & 0xffff0000u) * inv;
+#pragma unroll
+              for (int i = 0; i < C::kParts; ++i) part[i][4 * u + j] = take_codes(y, z);
+            }
           }
-          const int at = code_offset<D>(th, c);
-          *reinterpret_cast<uint4*>(dst + at) = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16,
-                                                           hi[4] | hi[5] << 16, hi[6] | hi[7] << 16);
-          *reinterpret_cast<uint4*>(dst + C::kQ + at) = make_uint4(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16,
-                                                                   lo[4] | lo[5] << 16, lo[6] | lo[7] << 16);
+#pragma unroll
+          for (int i = 0; i < C::kParts; ++i)
+            *reinterpret_cast<uint4*>(dst + i * C::kQ + code_offset<D>(th, c)) =
+                make_uint4(part[i][0] | part[i][1] << 16, part[i][2] | part[i][3] << 16,
+                           part[i][4] | part[i][5] << 16, part[i][6] | part[i][7] << 16);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -686,9 +706,12 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
     tc_fence_after();
   }
   // copies and products have ended (so they have, unless a wait ran out somewhere)
-  if (warp == 12 && lane == 0)
-    for (uint32_t j = loaded < kStages ? 0 : loaded - kStages; j < loaded; ++j)
-      mbar_wait_drain(&bars.full[j % kStages], (j / kStages) & 1, nullptr);
+  if (warp == 12 && lane == 0) {
+    for (uint32_t j = k_loaded < kStages ? 0 : k_loaded - kStages; j < k_loaded; ++j)
+      mbar_wait_drain(&bars.k_full[j % kStages], (j / kStages) & 1, nullptr);
+    for (uint32_t j = v_loaded < kStagesV ? 0 : v_loaded - kStagesV; j < v_loaded; ++j)
+      mbar_wait_drain(&bars.v_full8[j % kStagesV], (j / kStagesV) & 1, nullptr);
+  }
   if (warp >= 13 && lane == 0) {
     mma_commit(&bars.drain[warp - 13]);
     mbar_wait_drain(&bars.drain[warp - 13], 0, nullptr);
