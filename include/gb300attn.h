@@ -513,7 +513,8 @@ GB300ATTN_API int attn_kv_copy_pages(const attn_kv_cache* cache, const int32_t* 
  *  workspace  >= attn_decode_workspace_bytes() bytes, 256-byte aligned; no
  *             initialisation needed.  Calls that overlap on the GPU need one
  *             each.  Where that size is 256 no scratch is used and NULL will do.
- * Results are bit-identical from run to run.  Large row counts take a kernel
+ * A query row with an infinity or NaN gives NaN where it sees a key.  Results are
+ * bit-identical from run to run.  Large row counts take a kernel
  * whose warps wait for one another, for at most a second: results of a CTA that
  * gave up are NaN. */
 typedef struct attn_decode_params {

@@ -457,23 +457,16 @@ __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
         uint4 x[D / 8];
 #pragma unroll
         for (int c = 0; c < D / 8; ++c) x[c] = mine ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-        // (magnitudes of bf16 order like their bits, two in a word)
         uint32_t top = 0u;
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          top = __vmaxu2(top, x[c].x & 0x7fff7fffu);
-          top = __vmaxu2(top, x[c].y & 0x7fff7fffu);
-          top = __vmaxu2(top, x[c].z & 0x7fff7fffu);
-          top = __vmaxu2(top, x[c].w & 0x7fff7fffu);
-        }
-        const uint32_t bits = max(top << 16, top & 0xffff0000u);
+        for (int c = 0; c < D / 8; ++c)
+          top = top_bf16x2(top_bf16x2(top_bf16x2(top_bf16x2(top, x[c].x), x[c].y), x[c].z), x[c].w);
+        const uint32_t bits = top_of(top);
         const bool finite = bits < 0x7f800000u;
         const int over = (bits & 0x7fffffu) > 0x600000u ? 1 : 0;
         const int ex = finite && bits ? max((int)(bits >> 23) - 127 + over, -100) - 15 : 0;
         const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-        // (a row with an infinity or NaN has no softmax: all of it is NaN)
-        const float more = finite ? 0.f : bad;
-        s_fac[r] = mine ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) + more : 0.f;
+        s_fac[r] = mine ? row_factor(a, ex, finite) : 0.f;
         uint8_t* dst = smem + (kTurns ? 0 : g) * 128 * D;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c) {  // 16 values

@@ -545,6 +545,17 @@ struct RowPlace {
     lse = ((int64_t)seq * a.h_q + head) * a.s_q + t;
   }
 };
+// The largest magnitudes of bf16 pairs: they order like their bits, two in a word.
+__device__ __forceinline__ uint32_t top_bf16x2(uint32_t top, uint32_t w) { return __vmaxu2(top, w & 0x7fff7fffu); }
+// As the bits of a float (0x7f800000 and above: an infinity or NaN is among them).
+__device__ __forceinline__ uint32_t top_of(uint32_t top) { return max(top << 16, top & 0xffff0000u); }
+// What the scores of a row are multiplied by, whose q was divided by 2^ex.  A row with an infinity or
+// NaN has no softmax (minus infinity for every score would pass for a row that sees no key): all
+// of it is NaN.
+__device__ __forceinline__ float row_factor(const DecodeArgs& a, int ex, bool finite) {
+  return finite ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) : __int_as_float(0x7fffffff);
+}
+
 // (the parts of a shared problem are folded in base 2)
 template <int M>
 __device__ __forceinline__ float lse_out(float lse2) {
@@ -734,18 +745,17 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
     for (int i = 0; i < kRows; ++i) {
       const int r = warp + i * kWarps;
       float x[kE];
-      float amax = 0.f;
+      uint32_t top = 0u;
 #pragma unroll
       for (int e = 0; e < kE; e += 2) {
         x[e] = __uint_as_float(qw[i][e / 2] << 16);
         x[e + 1] = __uint_as_float(qw[i][e / 2] & 0xffff0000u);
+        top = top_bf16x2(top, qw[i][e / 2]);
       }
-#pragma unroll
-      for (int e = 0; e < kE; ++e)
-        if (fabsf(x[e]) < INFINITY) amax = fmaxf(amax, fabsf(x[e]));
-      const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(amax));
+      const uint32_t bits = __reduce_max_sync(0xffffffffu, top_of(top));
+      const bool finite = bits < 0x7f800000u;
       // the row's largest value goes to [2^14, 2^15)
-      const int ex = bits ? max((int)(bits >> 23) - 127, -100) - 14 : 0;
+      const int ex = finite && bits ? max((int)(bits >> 23) - 127, -100) - 14 : 0;
       const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
       // value e of the lane's is element (d & 3) of k step (d >> 6) * 4 + ((d & 15) >> 2)
       // of lane (r & 7) * 4 + ((d >> 4) & 3), in pairs
@@ -759,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, Tune<D, NT>::kCtas) attn_decode_kern
             pack_f16(x[e] * inv, x[e + 1] * inv);
       }
       if (lane == 0) {
-        s_fac[r] = qin[i] ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) : 0.f;
+        s_fac[r] = qin[i] ? row_factor(a, ex, finite) : 0.f;
         s_pos[r] = qpos[i];
       }
     }

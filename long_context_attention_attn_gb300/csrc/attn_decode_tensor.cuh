@@ -444,22 +444,17 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         const int64_t orow = RowPlace<M>(a, p, mine ? row : 0).orow;
         const uint32_t my_tmem = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint4* src = reinterpret_cast<const uint4*>(a.q + orow * D);
-        float amax = 0.f;
+        uint32_t top = 0u;
 #pragma unroll 8
         for (int c = 0; c < D / 8; ++c) {
           const uint4 x = mine ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float x0 = fabsf(__uint_as_float(w[j] << 16)), x1 = fabsf(__uint_as_float(w[j] & 0xffff0000u));
-            if (x0 < INFINITY) amax = fmaxf(amax, x0);
-            if (x1 < INFINITY) amax = fmaxf(amax, x1);
-          }
+          top = top_bf16x2(top_bf16x2(top_bf16x2(top_bf16x2(top, x.x), x.y), x.z), x.w);
         }
-        const uint32_t bits = __float_as_uint(amax);
-        const int ex = bits ? max((int)(bits >> 23) - 127, -100) - 14 : 0;
+        const uint32_t bits = top_of(top);
+        const bool finite = bits < 0x7f800000u;
+        const int ex = finite && bits ? max((int)(bits >> 23) - 127, -100) - 14 : 0;
         const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-        s_fac[n & 1][th] = mine ? a.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23) : 0.f;
+        s_fac[n & 1][th] = mine ? row_factor(a, ex, finite) : 0.f;
 #pragma unroll 1
         for (int c = 0; c < D / 2; c += 16) {
           uint32_t f[16];
