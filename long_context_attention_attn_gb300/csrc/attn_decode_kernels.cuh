@@ -155,7 +155,7 @@ struct Span {
 // table can hold.
 __device__ __forceinline__ Span make_span(int len, int cap, int p0, int window, int sink, int block, int item_cost) {
   Span s;
-  s.hi = max(min(len, cap), 0);
+  s.hi = min(max(len, 0), cap);
   s.lo = window < 0 ? 0 : max(p0 - window, 0);
   s.sink_hi = window < 0 ? 0 : min(sink, s.hi);
   const int last = (s.hi + block - 1) / block;

@@ -140,11 +140,24 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
+// The rest of a wait, out of line.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (mbar_try_wait_sleep(bar, parity, kSleepHintNs)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 // mbar_wait, asleep once before the clock is read.
+template <bool kInline = true>
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, const WaitCtx& ctx) {
   if (mbar_try_wait_sleep(smem_u32(bar), parity, kSleepHintNs)) return true;
   if (*ctx.abort_flag) return false;
-  return mbar_wait(bar, parity, ctx);
+  return kInline ? mbar_wait(bar, parity, ctx) : wait_long(smem_u32(bar), parity, ctx.abort_flag);
 }
 
 template <int D, int NT>
@@ -208,6 +221,11 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
   using C = TensorCfg<D, NT>;
   using T = typename C::T;
   constexpr int R = C::R, kStages = C::kStages, NB = C::kBlocks, kKeys = C::kKeys;
+  // Six loops share the instruction caches: with the rest of every wait inlined their code falls out of
+  // them, and warps wait for instructions (48 sequences of 100 to 12000 tokens, Hkv 8, 64 and 128 rows,
+  // us inlined / out of line: d 64 207 / 201, 309 / 281, d 128 258 / 241, 338 / 326; d 256, whose
+  // products are longer, 443 / 457, 474 / 477).
+  constexpr bool kInline = D == 256;
   extern __shared__ uint8_t smem_raw[];
   struct Bars {
     uint64_t full[kStages];        // a tile's codes are there
@@ -324,7 +342,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
                          key + 31 <= p_first && (a.window < 0 || p_last - key <= a.window || key + 31 < p.sink(a));
         for (int u = 0; u < kTurn && t + u < p.t1; u += NB, ++i) {
           const int slot = i % kStages;
-          if (i >= kStages) ok = wait_on(&bars.free[slot], (i / kStages - 1) & 1, ctx);
+          if (i >= kStages) ok = wait_on<kInline>(&bars.free[slot], (i / kStages - 1) & 1, ctx);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           const int g = lane - 2 * u;  // this lane's group of the tile
@@ -366,13 +384,13 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     uint32_t i = 0, n = 0;
     bool ok = true;
     while (ok && walk.next(a, p, lane == 0, warp_sync)) {
-      ok = __all_sync(0xffffffffu, wait_on(&bars.q_full[n & 1], (n >> 1) & 1, ctx));
+      ok = __all_sync(0xffffffffu, wait_on<kInline>(&bars.q_full[n & 1], (n >> 1) & 1, ctx));
       for (int t = p.t0; t < p.t1 && ok; t += NB, ++i) {
         const int buf = i % C::kKBufs;
         // its buffer holds S (or P) of two tiles before
         if (ok && i >= 2)
-          ok = wait_on(C::kPBufs > 0 ? &bars.s_free[i & 1] : &bars.o_done[i & 1], ((i >> 1) - 1) & 1, ctx);
-        if (ok) ok = wait_on(&bars.k_full[buf], (i / C::kKBufs) & 1, ctx);
+          ok = wait_on<kInline>(C::kPBufs > 0 ? &bars.s_free[i & 1] : &bars.o_done[i & 1], ((i >> 1) - 1) & 1, ctx);
+        if (ok) ok = wait_on<kInline>(&bars.k_full[buf], (i / C::kKBufs) & 1, ctx);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && lane == 0) {
           tc_fence_after();
@@ -401,8 +419,8 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     while (ok && walk.next(a, p, lane == 0, warp_sync)) {
       for (int t = p.t0; t < p.t1 && ok; t += NB, ++i) {
         const int buf = i % C::kVBufs;
-        ok = wait_on(&bars.v_full[buf], (i / C::kVBufs) & 1, ctx);
-        if (ok) ok = wait_on(&bars.p_full[i & 1], (i >> 1) & 1, ctx);
+        ok = wait_on<kInline>(&bars.v_full[buf], (i / C::kVBufs) & 1, ctx);
+        if (ok) ok = wait_on<kInline>(&bars.p_full[i & 1], (i >> 1) & 1, ctx);
         ok = __all_sync(0xffffffffu, ok);
         if (ok && lane == 0) {
           tc_fence_after();
@@ -427,14 +445,14 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
     bool ok = true;
     while (walk.next(a, p, (threadIdx.x & 127) == 0, group_sync)) {
       if (is_v) {
-        if (ok && n > 1) ok = wait_on(&bars.done[n & 1], ((n >> 1) - 1) & 1, ctx);
+        if (ok && n > 1) ok = wait_on<kInline>(&bars.done[n & 1], ((n >> 1) - 1) & 1, ctx);
         if (ok && (a.s_q > 1 || M == kShared))
           for (int u = threadIdx.x & 127; u < D * 4; u += 128) s_nan(n)[u] = 0u;
         if (ok && (threadIdx.x & 127) == 0) s_any_nan[n & 1] = 0;
         group_sync();
         // ---- q's rows (a thread per row and copy) as f16, the largest value in [2^14,
         // 2^15), after the last S with the rows before them
-        if (ok && i > 0) ok = wait_on(&bars.s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
+        if (ok && i > 0) ok = wait_on<kInline>(&bars.s_full[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
         ok = __all_sync(0xffffffffu, ok);
       }
       if (is_v && ok) {
@@ -476,7 +494,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
       for (int t = p.t0; t < p.t1; t += NB, ++i) {
         if (wb >= NB) continue;
         const int slot = i % kStages;
-        if (ok) ok = wait_on(&bars.full[slot], (i / kStages) & 1, ctx);
+        if (ok) ok = wait_on<kInline>(&bars.full[slot], (i / kStages) & 1, ctx);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;
         const uint8_t* base = smem + slot * 2 * C::kCodes + (is_v ? C::kCodes : 0);
@@ -532,10 +550,10 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         mbar_arrive(&bars.free[slot]);
         // the f16 tile that was there has been multiplied
         if (is_v) {
-          if (i >= C::kVBufs) ok = wait_on(&bars.o_done[i & 1], ((i >> 1) - 1) & 1, ctx);
+          if (i >= C::kVBufs) ok = wait_on<kInline>(&bars.o_done[i & 1], ((i >> 1) - 1) & 1, ctx);
         } else if (i >= C::kKBufs) {
           const uint32_t j = i - C::kKBufs;
-          ok = wait_on(&bars.s_full[j & 1], (j >> 1) & 1, ctx);
+          ok = wait_on<kInline>(&bars.s_full[j & 1], (j >> 1) & 1, ctx);
         }
         if (!ok) continue;
         uint8_t* dst = smem + (is_v ? C::v_off + i % C::kVBufs * C::kHalf : C::k_off + i % C::kKBufs * C::kHalf);
@@ -576,7 +594,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
       const RowPlace<M> to(a, p, mine ? row : 0);
       const int64_t orow = to.orow;
       const int pos = mine ? to.pos : -1;
-      if (ok) ok = wait_on(&bars.q_full[n & 1], (n >> 1) & 1, ctx);
+      if (ok) ok = wait_on<kInline>(&bars.q_full[n & 1], (n >> 1) & 1, ctx);
       const float fac = s_fac[n & 1][th];
       // the references of P and of P * v_scale (negated; at first below every score),
       // 2^(m - mo + kShift), the sum of P
@@ -587,8 +605,8 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         const int m = i % C::kMeta;
         const bool first = t == p.t0;
         const uint32_t t_s = my_tmem + C::col_s + (i & 1) * kKeys;
-        if (ok) ok = wait_on(&bars.meta_full[i & 1], (i >> 1) & 1, ctx);
-        if (ok) ok = wait_on(&bars.s_full[i & 1], (i >> 1) & 1, ctx);
+        if (ok) ok = wait_on<kInline>(&bars.meta_full[i & 1], (i >> 1) & 1, ctx);
+        if (ok) ok = wait_on<kInline>(&bars.s_full[i & 1], (i >> 1) & 1, ctx);
         __syncwarp();
         tc_fence_after();
         uint32_t pk[W / 2];
@@ -678,7 +696,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
             nmo = nmo1;
             b = ex2(nmo1 - nm1 + kShift);
             if (!first) {
-              if (ok) ok = wait_on(&bars.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
+              if (ok) ok = wait_on<kInline>(&bars.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
               __syncwarp();
               tc_fence_after();
 #pragma unroll 1
@@ -700,7 +718,7 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
           // P's place is free after its last O
           if (ok && i >= C::kPBufs) {
             const uint32_t j = i - C::kPBufs;
-            ok = wait_on(&bars.o_done[j & 1], (j >> 1) & 1, ctx);
+            ok = wait_on<kInline>(&bars.o_done[j & 1], (j >> 1) & 1, ctx);
           }
           __syncwarp();
         }
@@ -720,8 +738,8 @@ attn_decode_tensor_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMa
         tc_fence_before();
         if (ok) mbar_arrive(&bars.p_full[i & 1]);
       }
-      if (ok) ok = wait_on(&bars.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
-      if (ok) ok = wait_on(&bars.widened[n & 1], (n >> 1) & 1, ctx);
+      if (ok) ok = wait_on<kInline>(&bars.o_done[(i - 1) & 1], ((i - 1) >> 1) & 1, ctx);
+      if (ok) ok = wait_on<kInline>(&bars.widened[n & 1], (n >> 1) & 1, ctx);
       __syncwarp();
       tc_fence_after();
 
