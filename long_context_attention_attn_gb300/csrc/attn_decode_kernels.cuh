@@ -1301,9 +1301,10 @@ struct Kernel {
     const cudaError_t e = resident(&n);
     if (e != cudaSuccess) return e;
     // blocks of the longest sequence that the page table can hold, as far as the
-    // window and the kept tokens reach (which may begin and end inside blocks)
+    // window and the kept tokens reach (which may begin and end inside blocks); a group's
+    // reach from its shortest member's window to the end of what is shared
     int64_t blocks = (p.max_pages * p.cache.page_size + T::kBlock - 1) / T::kBlock;
-    if (p.window_left >= 0) {
+    if (M != kShared && p.window_left >= 0) {
       const int64_t seen = (p.window_left + p.s_q) / T::kBlock + 2 + (p.sink_tokens + T::kBlock - 1) / T::kBlock;
       if (seen < blocks) blocks = seen;
     }
