@@ -567,8 +567,8 @@ GB300ATTN_API int attn_decode_test_timeout(const attn_decode_params* p, attn_str
  * attn_decode needs one launch and no scratch (some 16 sequences of 2k tokens, 4 of
  * 8k), this is attn_decode, which is then the faster.  A query row with an infinity or
  * NaN gives NaN where it sees a key.  Results are bit-identical from run to run, and
- * differ from attn_decode's by the order of sums and, with d 64 or 128 and more than
- * 32 rows (max_group * s_q * h_q / h_kv), by how far q's bits reach: its values are
+ * differ from attn_decode's by the order of sums and, with more than 32 rows
+ * (max_group * s_q * h_q / h_kv) at d 64 or 64 at d 128, by how far q's bits reach: its values are
  * exact down to 2^-23 of their row's largest and off by at most 2^-31 of that below
  * (elsewhere, as in attn_decode: 2^-31 and 2^-39).  Where groups disagree with what is
  * said here results are unspecified; no other memory is read or written. */

@@ -861,8 +861,9 @@ def attn_decode_shared(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlen
     every sequence of i's group; group j is the sequences group_start[j] .. group_start[j + 1] - 1 (int32
     [n_groups + 1], from 0 to n; None: all sequences are one group).  ``max_group`` is the most sequences
     of a group (default: n); it decides how many rows a CTA takes.  The rest is as in
-    :func:`attn_decode`, whose results these are but for the order of sums (and, with d 64 or 128 and more
-    than 32 rows of a kv head, for q's values below 2^-23 of their row's largest: off by 2^-31 of that at most)."""
+    :func:`attn_decode`, whose results these are but for the order of sums (and, with more than 32 rows of a
+    kv head at d 64 or 64 at d 128, for q's values below 2^-23 of their row's largest: off by 2^-31 of that
+    at most)."""
     base, index, out, lse = _decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seqlens, window_left,
                                            sink_tokens, scale, out, lse, out_fp32)
     p = _shared_params(base, index, q.shape[0], shared_pages, group_start, max_group)

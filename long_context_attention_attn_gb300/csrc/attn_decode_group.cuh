@@ -1,5 +1,5 @@
-// The shared keys of groups with more than 32 rows, on the tensor-memory path, included by
-// attn_decode_shared.cu.
+// The shared keys of groups with more than 32 rows (64 at d 128), on the tensor-memory path,
+// included by attn_decode_shared.cu.
 //
 //   S[rows, keys] = q K^T (8 bits in, q as three e5m2 values),  O[rows, d] += P V (f16 in), fp32 sums
 //

@@ -1399,8 +1399,11 @@ cudaError_t with_rows(const attn_decode_params& p, int64_t groups, int64_t rows,
     const cudaError_t e = Kernel<D, 2, M>::shape(p, groups, &sh);
     if (e != cudaSuccess) return e;
     if (!sh.cluster) {
-      if (rows > 64) return use(Kernel<D, 16, M>());
-      if (rows > 32) return use(Kernel<D, 8, M>());
+      // (shared keys of more rows: attn_decode_group.cuh)
+      if constexpr (M != kShared || D == 256)
+        if (rows > 64) return use(Kernel<D, 16, M>());
+      if constexpr (M != kShared || D >= 128)
+        if (rows > 32) return use(Kernel<D, 8, M>());
       if constexpr (D < 256) return use(Kernel<D, 4, M>());
     }
   }

@@ -230,6 +230,10 @@ __global__ void __launch_bounds__(kFoldThreads)
   }
 }
 
+// From more rows than this on a group's keys take attn_decode_group.cuh.
+template <int D>
+constexpr int kGroupRows = D == 64 ? 32 : 64;
+
 // f(kernel of the shared keys, its shape, kernel of the own keys, its shape)
 template <int D, typename F>
 cudaError_t with_both(const attn_decode_shared_params& p, F&& f) {
@@ -239,10 +243,11 @@ cudaError_t with_both(const attn_decode_shared_params& p, F&& f) {
     return with_rows<D, kOwn>(q, 0, rows, [&](auto ko, const Shape& so) { return f(ks, ss, ko, so); });
   };
   if constexpr (D < 256) {
-    // (us by the warp-level kernel and by this one, d 128: 24 rows over 32768 keys 34.6 / 45.9, 32 rows
-    // 36.5 / 53.6; by attn_decode_tensor.cuh and by this one: 48 rows 45.7 / 46.1, 64 rows 46.3 / 47.7, d 64
-    // 40.3 / 37.5; 2048 rows with 128 and with 256 rows a CTA 395 / 308)
-    if (most > 32) {
+    // (us of the whole call, Hkv 8, 60 to 200 own tokens, by attn_decode_tensor.cuh and by this one, 40 / 48 /
+    // 64 / 96 / 128 rows over 32768 keys: d 64 38.7 39.4 40.2 48.8 51.0 and 38.3 39.4 39.9 41.2 42.0; d 128
+    // 42.6 44.1 46.1 58.5 60.0 and 47.2 48.0 48.4 51.7 55.8; over 8192: d 64 20.5 20.7 25.1 34.1 34.1 and 20.6
+    // 20.7 24.8 28.3 31.4, d 128 29.6 31.4 33.9 39.2 40.1 and 32.4 33.9 32.5 34.9 39.0)
+    if (most > kGroupRows<D>) {
       auto use = [&](auto k) {
         Shape sh;
         const cudaError_t e = k.shape(q, p.n_groups, &sh);
