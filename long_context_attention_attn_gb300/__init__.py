@@ -510,13 +510,20 @@ def rope_frequencies(rot: int, base: float = 10000.0, *, factor: float = 1.0, me
     factor (positions squeezed); "base" raises the base by factor^(rot / (rot - 2)) (the fastest pair as
     before, the slowest divided by factor); "parts" divides those of fewer than ``slow`` turns in the
     trained length by factor, keeps those of more than ``fast``, and mixes the two in proportion to the
-    turns between."""
-    if rot < 2 or rot % 2 or not factor > 0 or not base > 0:
-        raise ValueError("rope_frequencies: rot must be even, base and factor positive")
+    turns between (slow < fast)."""
+    if rot < 2 or rot % 2 or not 0 < factor < math.inf or not 0 < base < math.inf:
+        raise ValueError("rope_frequencies: rot must be even, base and factor positive and finite")
     if method not in ("linear", "base", "parts"):
         raise ValueError("rope_frequencies: method is linear, base or parts")
+    if method == "parts" and not (0 < trained < math.inf and -math.inf < slow < fast):
+        raise ValueError("rope_frequencies: trained must be positive and finite, slow less than fast")
     if method == "base" and rot > 2:
-        base = base * factor ** (rot / (rot - 2))
+        try:
+            base = base * factor ** (rot / (rot - 2))
+        except OverflowError:
+            base = math.inf
+        if not 0 < base < math.inf:
+            raise ValueError("rope_frequencies: base and factor lie too far apart")
     f = torch.pow(torch.tensor(base, dtype=torch.float64), -torch.arange(0, rot, 2, dtype=torch.float64) / rot)
     if method == "linear":
         f = f / factor
