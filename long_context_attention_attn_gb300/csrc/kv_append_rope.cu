@@ -195,11 +195,11 @@ __device__ __forceinline__ void append_unit(const AppendArgs& a, const Turning& 
 }
 
 // (two prompts of 32768 tokens: 276 us at 80 registers, 254 at 64)
-template <int T, int kC>
+template <int T>
 constexpr int kMinCtas = T <= 128 ? 8 : T == 256 ? 4 : 1;
 
 template <int T, int kC, int D, bool kPairs>
-__global__ void __launch_bounds__(T < 128 ? 128 : T, kMinCtas<T, kC>)
+__global__ void __launch_bounds__(T < 128 ? 128 : T, kMinCtas<T>)
     kv_append_rope_kernel(const AppendArgs a, const __grid_constant__ TurnArgs t) {
   constexpr int kWarps = (T < 128 ? 128 : T) / 32;
   __shared__ __align__(16) union {

@@ -22,7 +22,7 @@ struct RopeArgs {
   void* q_out;
   void* k_out;
   const int* pos;
-  int64_t tokens, q_stride, k_stride, q_out_stride, k_out_stride, items;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride, items;
   int h_q, h, d, chunks, heads_per_chunk;
   bool copy;
   Turning turning;
@@ -68,7 +68,6 @@ cudaError_t launch_rope(const attn_rope_params& p, cudaStream_t st) {
   a.q_out = p.q_out;
   a.k_out = p.k_out;
   a.pos = p.pos;
-  a.tokens = p.tokens;
   a.q_stride = p.q_stride > 0 ? p.q_stride : p.h_q * p.d;
   a.k_stride = p.k_stride > 0 ? p.k_stride : p.h_k * p.d;
   a.q_out_stride = p.q_out_stride > 0 ? p.q_out_stride : p.h_q * p.d;
@@ -79,7 +78,7 @@ cudaError_t launch_rope(const attn_rope_params& p, cudaStream_t st) {
   a.copy = (p.h_q > 0 && p.q != p.q_out) || (p.h_k > 0 && p.k != p.k_out);
   const attn_rotation& r = p.rotation;
   a.turning = Turning{r.freqs, (int)r.rot, (int)r.offset, r.amplitude == 0.f ? 1.f : r.amplitude, p.inverse != 0};
-  // Few tokens: several warps share a token's heads, down to two rounds of loads each.
+  // Few tokens: several warps share a token's heads, down to one round of loads each.
   const int values = p.fp32 ? 8 : 16;  // of a unit
   const int per = 32 / (a.copy ? a.d / values : a.turning.rot / values);
   int64_t chunks = (int64_t)sm_count() * 16 / p.tokens;
