@@ -29,7 +29,7 @@ struct RopeArgs {
 };
 
 template <typename E, bool kInterleaved>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const __grid_constant__ RopeArgs a) {
   __shared__ __align__(16) float tab[kWarps][kMaxRot];
   const int warp = threadIdx.x / 32;
   uint64_t turns[4];
