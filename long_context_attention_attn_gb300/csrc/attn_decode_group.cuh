@@ -117,7 +117,7 @@ __device__ __forceinline__ uint32_t take_codes(float& x, float& y) {
 
 template <int D, bool kTurns>
 __global__ void __launch_bounds__(GroupCfg<D, kTurns>::kThreads, 1)
-    decode_group_kernel(const DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
+    decode_group_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v) {
   using C = GroupCfg<D, kTurns>;
   using T = GroupTune;

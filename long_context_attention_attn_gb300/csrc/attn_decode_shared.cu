@@ -59,7 +59,8 @@ constexpr int kFoldMost = 64;  // partials at a time
 // has fewer rows than its threads hold, several threads share a row's partials.
 template <int D>
 __global__ void __launch_bounds__(kFoldThreads)
-    decode_shared_fold_kernel(const DecodeArgs a, const Part shared, const Part own, int n_groups, int heads) {
+    decode_shared_fold_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ Part shared,
+                              const __grid_constant__ Part own, int n_groups, int heads) {
   constexpr int kVec = D / 4, RP = kFoldThreads / kVec;
   __shared__ int64_t before_s[kThreads + 1], before_o[kThreads + 1];
   __shared__ RowPieces rows_s[RP], rows_o[RP];
