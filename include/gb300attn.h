@@ -351,7 +351,7 @@ GB300ATTN_API int attn_fwd_noalloc_status(attn_stream_t stream);
 /* Position rotation of attention's inputs (the pages pass q and k already
  * turned).  Pair i of a head's rotated part turns by the angle pos * freqs[i]:
  *   y1 = amplitude (x1 cos - x2 sin),  y2 = amplitude (x2 cos + x1 sin)
- *  freqs        fp64 [rot / 2], 8-byte aligned: radians per position.  Angles
+ *  freqs        fp64 [rot / 2], 8-byte aligned, finite: radians per position.  Angles
  *               are taken modulo a turn in 64-bit fixed point: exact for every
  *               32-bit position up to the rounding of freqs / 2 pi.
  *  rot          values of a head that turn: a multiple of 16, 16 .. 256
@@ -567,9 +567,9 @@ GB300ATTN_API int attn_decode_test_timeout(const attn_decode_params* p, attn_str
  * attn_decode needs one launch and no scratch (some 16 sequences of 2k tokens, 4 of
  * 8k), this is attn_decode, which is then the faster.  A query row with an infinity or
  * NaN gives NaN where it sees a key.  Results are bit-identical from run to run, and
- * differ from attn_decode's by the order of sums and, with more than 32 rows
- * (max_group * s_q * h_q / h_kv) at d 64 or 64 at d 128, by how far q's bits reach: its values are
- * exact down to 2^-23 of their row's largest and off by at most 2^-31 of that below
+ * differ from attn_decode's by the order of sums and, with more than 32 rows at d 64
+ * or 64 at d 128 (max_group * s_q * h_q / h_kv), by how far q's bits reach: its values
+ * are exact down to 2^-23 of their row's largest and off by at most 2^-31 of that below
  * (elsewhere, as in attn_decode: 2^-31 and 2^-39).  Where groups disagree with what is
  * said here results are unspecified; no other memory is read or written. */
 typedef struct attn_decode_shared_params {

@@ -595,7 +595,7 @@ def rope(q, k, pos, freqs, *, interleaved: bool = False, offset: int = 0, amplit
     turns in place.
 
     q [b, s, Hq, d], k [b, s, Hkv, d] bf16 (or both fp32; either may be None, token rows may lie apart, as
-    in a packed [b, s, Hq + 2 Hkv, d]); pos int32 [b, s]; freqs fp64 [rot / 2] radians per position
+    in a packed [b, s, Hq + 2 Hkv, d]); pos int32 [b, s]; freqs fp64 [rot / 2], finite, radians a position
     (:func:`rope_frequencies`).  The ``rot`` values of each head from ``offset`` on turn (multiples of 16
     and 8): pair i is values (i, i + rot / 2) of them, or (2 i, 2 i + 1) with ``interleaved``, and becomes
     ``amplitude`` * (x1 cos - x2 sin, x2 cos + x1 sin) of pos * freqs[i].  The rest is copied."""

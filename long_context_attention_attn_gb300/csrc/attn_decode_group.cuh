@@ -25,10 +25,11 @@
 // keys: P of a half lies over its S, and the S of the next tile's half is computed as soon
 // as O has it, while the softmax works on the other half.
 //
-// Bound by latency: 2048 rows over 32768 keys, Hkv 8, d 128, in 259 us (1070 TFLOP/s, 56 % of
-// the measured rate), tensor pipe 42 % and issue 49 % of the time.  A half of 64 keys takes a softmax
-// warp some 2000 cycles for 280 instructions, two such warps to a scheduler; from P to O
-// to the next S of the same half are 1700 more, beside the other half's softmax.
+// Bound by latency: 2048 rows over 32768 keys, Hkv 8, d 128, in 286 us (970 TFLOP/s, 50 % of
+// the measured rate), tensor pipe 52 % and issue 43 % of the time.  With two products for q (259 us, 42 %
+// and 49 %) a half of 64 keys took a softmax warp some 2000 cycles for 280 instructions, two such
+// warps to a scheduler, and from P to O to the next S of the same half were 1700 more, beside the
+// other half's softmax; the third product lengthens that chain.
 //
 // Every wait ends as in attn_decode_tensor.cuh.
 #pragma once
@@ -39,12 +40,13 @@ enum { kAllRows = 1, kAllKeys = 2 };
 struct GroupTune {
   static constexpr int kBlock = 128;  // a tile
   // q's conversion, the first copies' latency and the last O, in tiles (us with 1 / 3 / 6: three
-  // groups under a window 37.8 / 34.1 / 34.5; 16 sequences behind 60000 tokens, d 64, 46 / 45 / 38;
-  // 64 behind 8192 71.9 / 71.6 / 70.5)
+  // groups under a window 37.3 / 34.3 / 34.9; 16 sequences behind 60000 tokens, d 64, 57 / 55 / 51;
+  // 64 behind 8192, own 100 to 2000, 73.6 / 71.6 / 71.3, own 60 to 200 47.8 / 44.5 / 44.9)
   static constexpr int kItemCost = 6;
   // Longer runs take fewer CTAs, beside which the own keys begin: that pays only where those
-  // are many (us with 4 / 5 / 8: 64 sequences behind 2048 tokens, own 60 to 200, 35.5 / 42.8 / 48.2;
-  // 64 behind 8192, own 100 to 2000, 71.7 / 67.8 / 63.9)
+  // are many (us with 4 / 5 / 8: 64 sequences behind 2048 tokens, own 60 to 200, 35.5 / 35.7 / 42.0;
+  // three groups under a window 34.9 / 36.5 / 42.2; 64 behind 8192, own 60 to 200, 44.9 / 39.6 /
+  // 45.3, own 100 to 2000 71.3 / 70.9 / 59.6)
   static constexpr int kMinRun = 4;
 };
 

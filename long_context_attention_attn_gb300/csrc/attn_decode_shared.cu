@@ -12,8 +12,9 @@
 //
 // The shared keys have members * s_q * g rows, 4 d flops each for 2 d bytes: from about
 // 140 rows on they are bound by the products, below by reading the keys; the own
-// keys by reading them.  us (attn_decode's in brackets), Hkv 8, d 128: 64 sequences behind
-// 8192 tokens, Hq 32, 45 (111); 64 behind 16384 57 (207); 128 behind 32768, Hq 128, 303.
+// keys by reading them.  us (attn_decode's in brackets), Hkv 8, d 128, 60 to 200 own tokens: 64
+// sequences behind 8192, Hq 32, 45 (112); 64 behind 16384 56 (209); 128 behind 32768, Hq 128,
+// 320 (1024).  d 256, Hkv 8, Hq 64: 32 sequences behind 16384 77 (199).
 #include "attn_decode_kernels.cuh"
 
 namespace gb300 {
@@ -244,10 +245,10 @@ cudaError_t with_both(const attn_decode_shared_params& p, F&& f) {
     return with_rows<D, kOwn>(q, 0, rows, [&](auto ko, const Shape& so) { return f(ks, ss, ko, so); });
   };
   if constexpr (D < 256) {
-    // (us of the whole call, Hkv 8, 60 to 200 own tokens, by attn_decode_tensor.cuh and by this one, 40 / 48 /
-    // 64 / 96 / 128 rows over 32768 keys: d 64 38.7 39.4 40.2 48.8 51.0 and 38.3 39.4 39.9 41.2 42.0; d 128
-    // 42.6 44.1 46.1 58.5 60.0 and 47.2 48.0 48.4 51.7 55.8; over 8192: d 64 20.5 20.7 25.1 34.1 34.1 and 20.6
-    // 20.7 24.8 28.3 31.4, d 128 29.6 31.4 33.9 39.2 40.1 and 32.4 33.9 32.5 34.9 39.0)
+    // (us of the whole call, Hkv 8, 60 to 200 own tokens, by attn_decode_tensor.cuh / attn_decode_group.cuh:
+    // d 64, 32768 keys, 40 rows 38.2 / 37.0, 64 rows 39.4 / 38.4, 96 rows 47.8 / 39.8, 128 rows 49.0 / 40.5;
+    // d 128, 32768 keys, 40 rows 41.6 / 46.1, 64 rows 45.3 / 47.6, 80 rows 58.2 / 49.9, 128 rows 58.8 / 54.1;
+    // 8192 keys, 40 rows 27.9 / 30.0, 64 rows 31.2 / 31.4, 96 rows 36.5 / 34.3, 128 rows 38.5 / 37.8)
     if (most > kGroupRows<D>) {
       auto use = [&](auto k) {
         Shape sh;
@@ -289,8 +290,8 @@ Part part_of(const DecodeArgs& a, const Shape& sh) {
 // small (by the page table's width) that it takes a cluster of CTAs per item, one launch in
 // place of three that wait for one another (and uses no scratch).  us of attn_decode and of
 // the three, Hq 32, Hkv 8, d 128, own tokens 60 to 200, by clusters: 4 sequences behind 2048
-// tokens 9.1 / 15.4, behind 8192 15.1 / 20.1; 16 behind 2048 14.7 / 27.3; by the list: 8 behind
-// 8192 23.3 / 25.5, behind 16384 35.1 / 28.8; 32 behind 4096 37.4 / 33.3.
+// tokens 8.8 / 15.4, behind 8192 14.8 / 16.7; 16 behind 2048 14.8 / 25.6; by the list: 8 behind
+// 8192 23.4 / 22.1, behind 16384 35.3 / 26.1; 32 behind 4096 37.7 / 32.0.
 static cudaError_t plain_is_better(const attn_decode_shared_params& p, bool* plain, size_t* bytes) {
   const cudaError_t e = decode_workspace(p.base, bytes);
   *plain = p.max_group <= 1 || *bytes == 0;
