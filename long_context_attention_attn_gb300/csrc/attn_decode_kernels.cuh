@@ -1383,8 +1383,8 @@ struct Kernel {
 // and where the list cuts the work a CTA widens each code for more rows: up to 32 rows
 // 32 (at d = 256 the registers end at 16), above 64 or 128 on the tensor-memory path.
 // 48 sequences of 100 to 12000 tokens, Hkv 8, us at 32 / 64 / 128 rows by the
-// warp-level kernel and by the other: d 64 109 / 208 / 407 and 157 / 170 / 283; d 128
-// 161 / 294 / 567 and 190 / 232 / 300; d 256 326 / 635 / 1252 and 364 / 422 / 452.
+// warp-level kernel and by the other: d 64 112 / 214 / 396 and 201 / 201 / 281; d 128
+// 186 / 334 / 641 and 235 / 241 / 327; d 256 360 / 703 / 1390 and 402 / 442 / 474.
 // (rows: of an item, at most)
 template <int D, int M, typename F>
 cudaError_t with_rows(const attn_decode_params& p, int64_t groups, int64_t rows, F&& f) {

@@ -27,7 +27,7 @@
 // besides its tiles is 8 us.  Instruction fetch is felt everywhere (no-instruction
 // stalls 1.6 per issue, six loops at once), so what is rarely run is rolled.  Tried,
 // d 128, us of 48 sequences of 100 to 12000 tokens, Hkv 8, at 64 / 128 rows (this
-// one 221 / 303 at that time, 232 / 300 now): scales looked up tile by tile 247 /
+// one 221 / 303 at that time, of a batch of 9 % fewer tokens than the figures below): scales looked up tile by tile 247 /
 // 321; P over S, codes widened in place 317 / 305; keys on the M side (a thread per
 // key, votes over threads) 273 / 495.
 #pragma once
